@@ -334,17 +334,16 @@ def _own_quantize(sg, s, st):
                                              ct.data_ptr(), nr, 0, 1, st))
         return dict(q=q[:, :cols], scales=c, q_t=qt[:, :rows], scales_t=ct)
     c = _new((_up(cols, BLOCK) // BLOCK, rows), torch.float32)
-    _ok(sg, sg.sgemm_fp8_quantize_rows(rows, cols, x.data_ptr(), kind, x.stride(0), _ptr(gather), x.shape[0],
-                                       q.data_ptr(), ld, c.data_ptr(), rows, st))
-    got = dict(q=q[:, :cols], scales=c)
-    if s["form"] == "rows+cols":
-        padded = s["padded"]
-        qt, ct = _new((cols, padded), FP8), _new((padded // BLOCK, cols), torch.float32)
-        _ok(sg, sg.sgemm_fp8_quantize_cols(rows, cols, x.data_ptr(), kind, x.stride(0), _ptr(gather), x.shape[0],
-                                           s["offsets"].numel() - 1, s["offsets"].data_ptr(), padded, qt.data_ptr(),
-                                           padded, ct.data_ptr(), cols, st))
-        got["q_t"], got["scales_t"] = qt, ct
-    return got
+    if s["form"] == "rows":
+        _ok(sg, sg.sgemm_fp8_quantize_rows(rows, cols, x.data_ptr(), kind, x.stride(0), _ptr(gather), x.shape[0],
+                                           q.data_ptr(), ld, c.data_ptr(), rows, st))
+        return dict(q=q[:, :cols], scales=c)
+    padded = s["padded"]
+    qt, ct = _new((cols, padded), FP8), _new((padded // BLOCK, cols), torch.float32)
+    _ok(sg, sg.sgemm_fp8_quantize_both(rows, cols, x.data_ptr(), kind, x.stride(0), _ptr(gather), x.shape[0],
+                                       s["offsets"].numel() - 1, s["offsets"].data_ptr(), padded, q.data_ptr(), ld,
+                                       c.data_ptr(), rows, qt.data_ptr(), padded, ct.data_ptr(), cols, st))
+    return dict(q=q[:, :cols], scales=c, q_t=qt, scales_t=ct)
 
 
 def _own_product(sg, s, st):
