@@ -35,6 +35,18 @@ EXPORTED = ("sgemm", "sgemm_ex", "sgemm_check_status", "sgemm_error_string",
             "sgemm_test_fail_next_allocs", "sgemm_general", "sgemm_general_ex", "sgemm_general_plan",
             "sgemm_general_plan_launches")
 
+# Every function declared in include/sgemm_experts.h.
+EXPORTED_EXPERTS = ("sgemm_fp8_quantize_rows", "sgemm_fp8_quantize_cols", "sgemm_fp8_quantize_both",
+                    "sgemm_fp8_quantize_blocks", "sgemm_fp8", "sgemm_fp8_grouped", "sgemm_fp8_grouped_k",
+                    "sgemm_fp8_plan", "sgemm_route", "sgemm_route_backward", "sgemm_dispatch", "sgemm_combine",
+                    "sgemm_combine_backward")
+
+# Matrix types, scale forms of B, router scores and product modes of sgemm_experts.h.
+SGEMM_F32, SGEMM_BF16 = 0, 1
+SGEMM_SCALE_BLOCKS, SGEMM_SCALE_ROWS = 0, 1
+SGEMM_SCORE_SOFTMAX, SGEMM_SCORE_SIGMOID = 0, 1
+SGEMM_FP8_DENSE, SGEMM_FP8_GROUPED, SGEMM_FP8_GROUPED_K = 0, 1, 2
+
 _lock = threading.Lock()
 _lib = None
 
@@ -101,6 +113,30 @@ def load(rebuild: bool = False):
                                        ctypes.POINTER(ctypes.c_int),
                                        ctypes.POINTER(ctypes.c_int),
                                        ctypes.POINTER(ctypes.c_int)]
+            i, f = ctypes.c_int, ctypes.c_float
+            for name, args in {
+                "sgemm_fp8_quantize_rows": [_i64, _i64, _vp, i, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp],
+                "sgemm_fp8_quantize_cols": [_i64, _i64, _vp, i, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _vp,
+                                            _i64, _vp],
+                "sgemm_fp8_quantize_both": [_i64, _i64, _vp, i, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _vp,
+                                            _i64, _vp, _i64, _vp, _i64, _vp],
+                "sgemm_fp8_quantize_blocks": [_i64, _i64, _vp, i, _i64, _i64, i, _vp, _i64, _i64, _vp, _i64, _i64,
+                                              _i64, _vp],
+                "sgemm_fp8": [i, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, f, _vp, i, _i64, _vp],
+                "sgemm_fp8_grouped": [_i64, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64,
+                                      _i64, f, _vp, i, _i64, _vp],
+                "sgemm_fp8_grouped_k": [_i64, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, f,
+                                        _vp, i, _i64, _i64, _vp],
+                "sgemm_fp8_plan": [i, _i64, _i64, _i64, _i64, i, _vp, _vp, _vp, _vp],
+                "sgemm_route": [_i64, _i64, _vp, i, _i64, _vp, i, i, i, i, i, i, f, _vp, _vp, _vp],
+                "sgemm_route_backward": [_i64, _i64, _vp, i, _i64, i, i, i, f, _vp, _vp, _vp, _i64, _vp],
+                "sgemm_dispatch": [_i64, i, _i64, _vp, _vp, _vp, _vp, _vp],
+                "sgemm_combine": [_i64, i, _i64, _i64, _vp, i, _i64, _vp, _vp, _vp, _i64, _vp],
+                "sgemm_combine_backward": [_i64, i, _i64, _i64, _vp, i, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp,
+                                           _vp],
+            }.items():
+                getattr(lib, name).restype = ctypes.c_int
+                getattr(lib, name).argtypes = args
             _lib = lib
     return _lib
 
@@ -233,3 +269,92 @@ def sgemm_general_plan_launches(op_a, op_b, M, N, K, alpha, lda, stride_a, ldb, 
 def config_ids() -> dict:
     """Map of configuration name -> id."""
     return {sgemm_config_name(i): i for i in range(sgemm_num_configs())}
+
+
+# ---------------------------------------------------------------------------
+# include/sgemm_experts.h: routing, 8-bit quantisation and products, the sum of
+# the experts' outputs. Arguments and status codes as there.
+
+
+def sgemm_fp8_quantize_rows(rows, cols, src, type, ld, gather, src_rows, q, ldq, scales, lds, stream=0) -> int:
+    """e4m3 with a scale per row and 128 columns, of rows of src (gathered by `gather` unless 0)."""
+    return load().sgemm_fp8_quantize_rows(rows, cols, src, type, ld, gather, src_rows, q, ldq, scales, lds, stream)
+
+
+def sgemm_fp8_quantize_cols(rows, cols, src, type, ld, gather, src_rows, groups, offsets, padded, q_t, ldq_t,
+                            scales_t, lds_t, stream=0) -> int:
+    """The transpose with a scale per column and 128 rows of a group, each group from a multiple of 128 on."""
+    return load().sgemm_fp8_quantize_cols(rows, cols, src, type, ld, gather, src_rows, groups, offsets, padded, q_t,
+                                          ldq_t, scales_t, lds_t, stream)
+
+
+def sgemm_fp8_quantize_both(rows, cols, src, type, ld, gather, src_rows, groups, offsets, padded, q, ldq, scales,
+                            lds, q_t, ldq_t, scales_t, lds_t, stream=0) -> int:
+    """sgemm_fp8_quantize_rows() and sgemm_fp8_quantize_cols() from one read of src."""
+    return load().sgemm_fp8_quantize_both(rows, cols, src, type, ld, gather, src_rows, groups, offsets, padded, q,
+                                          ldq, scales, lds, q_t, ldq_t, scales_t, lds_t, stream)
+
+
+def sgemm_fp8_quantize_blocks(rows, cols, src, type, ld, stride_src, transpose, q, ldq, stride_q, scales, lds,
+                              stride_s, batch, stream=0) -> int:
+    """e4m3 with a scale per 128 x 128 block (weights), or the transpose of that."""
+    return load().sgemm_fp8_quantize_blocks(rows, cols, src, type, ld, stride_src, transpose, q, ldq, stride_q,
+                                            scales, lds, stride_s, batch, stream)
+
+
+def sgemm_fp8(b_form, M, N, K, A, lda, sa, ld_sa, B, ldb, sb, ld_sb, beta, C, c_type, ldc, stream=0) -> int:
+    """C = A . B^T + beta * C on e4m3 operands with a scale per block of 128."""
+    return load().sgemm_fp8(b_form, M, N, K, A, lda, sa, ld_sa, B, ldb, sb, ld_sb, beta, C, c_type, ldc, stream)
+
+
+def sgemm_fp8_grouped(groups, offsets, rows, N, K, A, lda, sa, ld_sa, B, ldb, stride_b, sb, ld_sb, stride_sb, beta,
+                      C, c_type, ldc, stream=0) -> int:
+    """Each group of rows of A times its own B: the experts' products."""
+    return load().sgemm_fp8_grouped(groups, offsets, rows, N, K, A, lda, sa, ld_sa, B, ldb, stride_b, sb, ld_sb,
+                                    stride_sb, beta, C, c_type, ldc, stream)
+
+
+def sgemm_fp8_grouped_k(groups, offsets, padded, M, N, A, lda, sa, ld_sa, B, ldb, sb, ld_sb, beta, C, c_type, ldc,
+                        stride_c, stream=0) -> int:
+    """One product per group over that group's rows: the experts' weight gradients."""
+    return load().sgemm_fp8_grouped_k(groups, offsets, padded, M, N, A, lda, sa, ld_sa, B, ldb, sb, ld_sb, beta, C,
+                                      c_type, ldc, stride_c, stream)
+
+
+def sgemm_fp8_plan(mode, groups, M, N, K, num_sms):
+    """Host-only: (status, columns, swap, split, grid) of the kernel an 8-bit product takes."""
+    cols, swap, split, grid = ctypes.c_int(-1), ctypes.c_int(-1), ctypes.c_int(-1), ctypes.c_int64(-1)
+    rc = load().sgemm_fp8_plan(mode, groups, M, N, K, num_sms, ctypes.addressof(cols), ctypes.addressof(swap),
+                               ctypes.addressof(split), ctypes.addressof(grid))
+    return rc, cols.value, swap.value, split.value, grid.value
+
+
+def sgemm_route(T, E, logits, type, ld, bias, score, groups, kept, two, k, renorm, scale, weights, indices,
+                stream=0) -> int:
+    """The k experts of each token and their weights."""
+    return load().sgemm_route(T, E, logits, type, ld, bias, score, groups, kept, two, k, renorm, scale, weights,
+                              indices, stream)
+
+
+def sgemm_route_backward(T, E, logits, type, ld, score, k, renorm, scale, indices, grad_w, grad_logits, ld_g,
+                         stream=0) -> int:
+    """Gradient of sgemm_route()'s weights with respect to the logits."""
+    return load().sgemm_route_backward(T, E, logits, type, ld, score, k, renorm, scale, indices, grad_w, grad_logits,
+                                       ld_g, stream)
+
+
+def sgemm_dispatch(T, k, E, indices, offsets, row_of, token_of, stream=0) -> int:
+    """The (token, slot) pairs sorted by expert."""
+    return load().sgemm_dispatch(T, k, E, indices, offsets, row_of, token_of, stream)
+
+
+def sgemm_combine(T, k, cols, rows, Y, type, ldy, row_of, weights, out, ld_out, stream=0) -> int:
+    """out[t] = sum_j weights[t, j] * Y[row_of[t, j]]."""
+    return load().sgemm_combine(T, k, cols, rows, Y, type, ldy, row_of, weights, out, ld_out, stream)
+
+
+def sgemm_combine_backward(T, k, cols, rows, grad_out, type, ld_go, Y, ldy, row_of, weights, grad_y, ld_gy, grad_w,
+                           stream=0) -> int:
+    """Gradients of sgemm_combine() with respect to Y and the weights."""
+    return load().sgemm_combine_backward(T, k, cols, rows, grad_out, type, ld_go, Y, ldy, row_of, weights, grad_y,
+                                         ld_gy, grad_w, stream)

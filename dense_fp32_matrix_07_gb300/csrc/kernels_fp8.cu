@@ -1,0 +1,819 @@
+// Block-scaled 8-bit products on the 5th-generation tensor cores:
+//
+//   C[m, n] = sum_kb sa[kb, m] * sb[kb, n] * (sum_{k in block kb} A[m, k] * B[n, k])  + beta * C[m, n]
+//
+// with A and B in e4m3, K contiguous, one scale for each 128 values along K
+// (and, for weights, for 128 rows at once). The inner sums are
+// tcgen05.mma .kind::f8f6f4 into tensor memory, one K block at a time; the
+// outer, scaled sum is kept in FP32 registers, because the scales are FP32
+// numbers that change with the block: each finished block is read back with
+// tcgen05.ld and added with one FMA per element (two where both operands are
+// scaled per row).
+//
+// Roles of a CTA:
+//   warp 0      TMA producer: one 128-byte-wide slab of each operand per K
+//               block (128-byte swizzle), full/empty barrier per stage;
+//   warp 1      TMEM owner and MMA issuer: 4 MMAs (K 32 each) per block into
+//               one of NBUF accumulators, then a commit that frees the stage
+//               and one that hands the accumulator on;
+//   warps 2, 3  scales: asynchronous 4-byte copies into a ring of their own,
+//               since rows of scales start at any address;
+//   warps 4..   promotion and epilogue: warp 4 + i reads lanes 32 (i % 4) ..
+//               of accumulator columns (i / 4) * CW ..
+//
+// The 128 lanes of tensor memory hold rows of A and the columns rows of B
+// ("wide"), or, where there are few rows of A, the other way round ("swap"):
+// the tile then spends MMA columns, registers and promotion only on the rows
+// of A there are, and reads each weight once.
+//
+// Work is a list of (token tile, weight tile) pairs, walked by a persistent
+// grid. Grouped products find their groups from the offsets in device memory:
+// every CTA builds the prefix sum of its groups' tiles (or K blocks) in
+// shared memory first. A tile may read rows past its group's end: they are
+// the next group's, or zero fill, and are never stored.
+//
+// Few tiles: `split` CTAs of a cluster share a tile's K blocks. Each leaves
+// its partial sums in its own shared memory, and after a cluster barrier CTA
+// r adds columns r, r + split, ... over the CTAs in rank order: the result
+// does not depend on timing.
+//
+// Every wait is bounded; a role that gives up sets the device error word and
+// goes to the teardown, which drains copies and MMAs.
+#include "common.cuh"
+#include "experts.cuh"
+#include "ptx.cuh"
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+namespace sgemm_gb300 {
+
+namespace {
+
+template <int BN_, bool SWAP_>
+struct Fp8Cfg {
+    static constexpr int BN = BN_;
+    static constexpr bool SWAP = SWAP_;
+    static constexpr int ROW_BYTES = kBlock;                 // one K block per slab row
+    static constexpr int P_TILE = 128 * ROW_BYTES;           // lanes' operand
+    static constexpr int Q_TILE = BN * ROW_BYTES;            // columns' operand
+    static constexpr int STAGE_BYTES = P_TILE + Q_TILE;
+    static constexpr int STAGES = BN == 256 ? 4 : BN == 128 ? 6 : 7;
+    static constexpr int NBUF = BN == 256 ? 2 : 4;           // accumulators in tensor memory
+    static constexpr int TMEM_COLS = NBUF * BN < 32 ? 32 : NBUF * BN;
+    static constexpr int EPI_WARPS = BN >= 128 ? 8 : 4;
+    static constexpr int CW = BN / (EPI_WARPS / 4);          // columns per epilogue warp
+    static constexpr int CHUNK = CW < 32 ? CW : 32;          // columns per tcgen05.ld
+    static constexpr int THREADS = 128 + 32 * EPI_WARPS;
+    static constexpr int SDEPTH = BN == 256 ? 4 : 8;         // ring of scales
+    static constexpr int SLOT = 128 + BN;                    // floats of one slot
+    static constexpr bool CAN_SPLIT = SWAP && BN <= 64;
+    static constexpr int STAGING = SWAP ? 0 : EPI_WARPS * 2048;
+    static constexpr int PARTIAL = CAN_SPLIT ? BN * 128 * 4 : 0;
+    static constexpr int NUM_BARS = 2 * STAGES + 2 * NBUF + 2 * SDEPTH + 1;
+    static constexpr int OFF_STAGING = STAGES * STAGE_BYTES;
+    static constexpr int OFF_PARTIAL = OFF_STAGING + STAGING;
+    static constexpr int OFF_SCALES = OFF_PARTIAL + PARTIAL;
+    static constexpr int OFF_TABLE = OFF_SCALES + SDEPTH * SLOT * 4;
+    static constexpr int OFF_BARS = OFF_TABLE + (kMaxGroups + 2) * 4;
+    static constexpr int SMEM_BYTES = 1024 + OFF_BARS + NUM_BARS * 8 + 16;
+    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
+    static_assert(TMEM_COLS <= 512 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "tensor memory columns");
+    static_assert(OFF_BARS % 8 == 0, "barrier alignment");
+};
+
+struct Fp8Params {
+    int mode;
+    int M, N;                    // rows of A, rows of B
+    int nk;                      // K blocks in all
+    const float *sa, *sb;
+    int64_t ld_sa, ld_sb, stride_sb;
+    int groups;
+    const int32_t *offsets;
+    int token_tiles;             // dense and grouped-K products; grouped rows: from the table
+    int weight_tiles;
+    int split;
+    float beta;
+    void *C;
+    int64_t ldc, stride_c;
+    int c_bf16, vec_c;
+    unsigned int *status;
+};
+
+// One tile: its group, first row of A and of B, the end of its rows of A,
+// and its K blocks.
+struct Fp8Item {
+    int group, a_row, a_end, b_row, kb0, kb1;
+};
+
+__device__ __forceinline__ int clamp_to(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
+
+// Rows [lo, hi) of group g, forced into [0, rows] whatever the offsets hold.
+__device__ __forceinline__ void group_range(const int32_t *offsets, int g, int rows, int &lo, int &hi)
+{
+    lo = clamp_to(offsets[g], 0, rows);
+    hi = clamp_to(offsets[g + 1], lo, rows);
+}
+
+// The group that owns entry x of the prefix table: table[g] <= x < table[g+1].
+__device__ __forceinline__ int find_group(const int *table, int groups, int x)
+{
+    int lo = 0, hi = groups - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (table[mid] <= x)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+constexpr int kRaster = 16;   // token tiles walked together, so that a wave of CTAs shares both operands in L2
+
+template <class Cfg>
+__device__ __forceinline__ Fp8Item fp8_item(const Fp8Params &p, const int *table, int64_t t, int rank)
+{
+    constexpr int TT = Cfg::SWAP ? Cfg::BN : 128;    // rows of A per tile
+    constexpr int WT = Cfg::SWAP ? 128 : Cfg::BN;    // rows of B per tile
+    Fp8Item it;
+    it.group = 0;
+    int tokens = p.token_tiles;
+    if (p.mode == kFp8GroupRows) tokens = table[p.groups];
+    if (p.mode == kFp8GroupK) {
+        const int64_t per = (int64_t)p.token_tiles * p.weight_tiles;
+        it.group = (int)(t / per);
+        t -= it.group * per;
+    }
+    const int64_t band = (int64_t)kRaster * p.weight_tiles;
+    const int first = (int)(t / band) * kRaster;
+    const int high = tokens - first < kRaster ? tokens - first : kRaster;
+    const int r = (int)(t % band);
+    const int tt = first + r % high;
+    it.b_row = (r / high) * WT;
+    if (p.mode == kFp8GroupRows) {
+        it.group = find_group(table, p.groups, tt);
+        int lo, hi;
+        group_range(p.offsets, it.group, p.M, lo, hi);
+        it.a_row = lo + (tt - table[it.group]) * TT;
+        it.a_end = hi;
+    } else {
+        it.a_row = tt * TT;
+        it.a_end = p.M;
+    }
+    int k0 = 0, k1 = p.nk;
+    if (p.mode == kFp8GroupK) {
+        k0 = table[it.group];
+        k1 = table[it.group + 1];
+    }
+    it.kb0 = k0 + (int)((int64_t)(k1 - k0) * rank / p.split);
+    it.kb1 = k0 + (int)((int64_t)(k1 - k0) * (rank + 1) / p.split);
+    return it;
+}
+
+// One element of C, and old values where beta asks for them.
+__device__ __forceinline__ void store_c(const Fp8Params &p, int64_t at, float v)
+{
+    if (p.c_bf16) {
+        __nv_bfloat16 *c = static_cast<__nv_bfloat16 *>(p.C) + at;
+        if (p.beta != 0.0f) v = fmaf(p.beta, __bfloat162float(*c), v);
+        *c = __float2bfloat16_rn(v);
+    } else {
+        float *c = static_cast<float *>(p.C) + at;
+        if (p.beta != 0.0f) v = fmaf(p.beta, *c, v);
+        *c = v;
+    }
+}
+
+// D (+)= P . Q^T on e4m3 operands, one thread issues.
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor of .kind::f8f6f4, both operands e4m3 (format 0) and
+// K-major, FP32 accumulation.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n)
+{
+    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+template <int CHUNK>
+__device__ __forceinline__ void tmem_ld_chunk(uint32_t taddr, uint32_t (&v)[CHUNK])
+{
+    if constexpr (CHUNK == 32) {
+        ptx::tmem_ld32(taddr, v);
+    } else {
+        static_assert(CHUNK == 16, "tensor memory chunk");
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                     "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+                       "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+                       "=r"(v[14]), "=r"(v[15])
+                     : "r"(taddr)
+                     : "memory");
+    }
+}
+
+// Waits for this thread's tcgen05.ld and ties the loaded registers to the
+// wait, so that no use of them can be scheduled before it.
+template <int CHUNK>
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&v)[CHUNK])
+{
+    ptx::tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < CHUNK; j += 8)
+        asm volatile("" : "+r"(v[j]), "+r"(v[j + 1]), "+r"(v[j + 2]), "+r"(v[j + 3]), "+r"(v[j + 4]), "+r"(v[j + 5]),
+                     "+r"(v[j + 6]), "+r"(v[j + 7]));
+}
+
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const float *src, bool there)
+{
+    const int bytes = there ? 4 : 0;   // 0: writes a zero without reading
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// This thread's arrival on `bar` once its cp.async copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank)
+{
+    float v;
+    asm volatile("{\n\t.reg .b32 ra;\n\tmapa.shared::cluster.u32 ra, %1, %2;\n\t"
+                 "ld.shared::cluster.f32 %0, [ra];\n\t}"
+                 : "=f"(v)
+                 : "r"(addr), "r"(rank)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float4 ld_shared_f32x4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void st_shared_f32(uint32_t addr, float v)
+{
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+__device__ __forceinline__ void st_shared_u32x4(uint32_t addr, uint4 v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared_u32x4(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// ROWS_FORM: B's scales are per row. LANES_SCALED: every lane of the
+// accumulator has a scale of its own, else all share one; COLS_SCALED: the
+// same of the columns (shared: by the CW columns of a warp).
+template <class Cfg, bool ROWS_FORM>
+__global__ void __launch_bounds__(Cfg::THREADS, 1)
+fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_constant__ CUtensorMap mapQ,
+                   const __grid_constant__ Fp8Params p)
+{
+    constexpr int BN = Cfg::BN, STAGES = Cfg::STAGES, NBUF = Cfg::NBUF, SD = Cfg::SDEPTH, CW = Cfg::CW;
+    constexpr int CHUNK = Cfg::CHUNK;
+    constexpr bool SWAP = Cfg::SWAP;
+    constexpr bool LANES_SCALED = ROWS_FORM || !SWAP;
+    constexpr bool COLS_SCALED = ROWS_FORM || SWAP;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    int *const table = reinterpret_cast<int *>(smem_raw + (base - raw) + Cfg::OFF_TABLE);
+    const uint32_t bars = base + Cfg::OFF_BARS;
+    auto stage_p = [&](int s) { return base + s * Cfg::STAGE_BYTES; };
+    auto stage_q = [&](int s) { return base + s * Cfg::STAGE_BYTES + Cfg::P_TILE; };
+    auto full_bar = [&](int s) { return bars + 8u * s; };
+    auto empty_bar = [&](int s) { return bars + 8u * (STAGES + s); };
+    auto accf_bar = [&](int b) { return bars + 8u * (2 * STAGES + b); };
+    auto acce_bar = [&](int b) { return bars + 8u * (2 * STAGES + NBUF + b); };
+    auto sfull_bar = [&](int s) { return bars + 8u * (2 * STAGES + 2 * NBUF + s); };
+    auto sempty_bar = [&](int s) { return bars + 8u * (2 * STAGES + 2 * NBUF + SD + s); };
+    const uint32_t drain_bar = bars + 8u * (2 * STAGES + 2 * NBUF + 2 * SD);
+    const uint32_t tmem_slot = bars + 8u * Cfg::NUM_BARS;
+    auto scale_slot = [&](int s) { return base + Cfg::OFF_SCALES + s * (Cfg::SLOT * 4); };
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int split = Cfg::CAN_SPLIT ? p.split : 1;
+    const int rank = split > 1 ? (int)ptx::cluster_ctarank() : 0;
+    if (split > 1 && ptx::cluster_nctarank() != (uint32_t)split) {
+        // Launched without its cluster, it would read peers that do not exist.
+        if (threadIdx.x == 0) atomicOr(p.status, kStatusLaunchConfig);
+        return;
+    }
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            ptx::mbar_init(full_bar(s), 1);
+            ptx::mbar_init(empty_bar(s), 1);
+        }
+        for (int b = 0; b < NBUF; ++b) {
+            ptx::mbar_init(accf_bar(b), 1);
+            ptx::mbar_init(acce_bar(b), Cfg::EPI_WARPS);
+        }
+        for (int s = 0; s < SD; ++s) {
+            ptx::mbar_init(sfull_bar(s), 64);
+            ptx::mbar_init(sempty_bar(s), Cfg::EPI_WARPS);
+        }
+        ptx::mbar_init(drain_bar, 1);
+        ptx::mbar_init_fence();
+    }
+    if (warp == 1) ptx::tmem_alloc(tmem_slot, Cfg::TMEM_COLS);
+    if (p.mode != kFp8Dense) {
+        // table[g] = tiles (or K blocks) of the groups before g.
+        const int unit = p.mode == kFp8GroupK ? kBlock : (SWAP ? BN : 128);
+        const int rows = p.mode == kFp8GroupK ? INT32_MAX : p.M;
+        for (int g = threadIdx.x; g < p.groups; g += Cfg::THREADS) {
+            int lo, hi;
+            group_range(p.offsets, g, rows, lo, hi);
+            table[g] = (int)(((int64_t)hi - lo + unit - 1) / unit);
+        }
+        __syncthreads();
+        if (warp == 0) {
+            int64_t carry = 0;
+            for (int g0 = 0; g0 < p.groups; g0 += 32) {
+                const int g = g0 + lane;
+                const int64_t mine = g < p.groups ? table[g] : 0;
+                int64_t sum = mine;
+#pragma unroll
+                for (int d = 1; d < 32; d *= 2) {
+                    const int64_t up = __shfl_up_sync(0xffffffffu, sum, d);
+                    if (lane >= d) sum += up;
+                }
+                // Offsets that are not a partition may sum to anything: no
+                // entry passes what the kernel can walk.
+                const int64_t most = p.mode == kFp8GroupK ? p.nk : (1 << 30);
+                const int64_t before = carry + sum - mine;
+                if (g < p.groups) table[g] = (int)(before < most ? before : most);
+                carry += __shfl_sync(0xffffffffu, sum, 31);
+                if (g0 + 32 >= p.groups && lane == 0) table[p.groups] = (int)(carry < most ? carry : most);
+            }
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t taddr = *reinterpret_cast<uint32_t *>(smem_raw + (tmem_slot - raw));
+
+    const int64_t t_first = (int64_t)blockIdx.x / split, t_step = (int64_t)gridDim.x / split;
+    int64_t tiles = p.mode == kFp8Dense       ? (int64_t)p.token_tiles * p.weight_tiles
+                    : p.mode == kFp8GroupRows ? (int64_t)table[p.groups] * p.weight_tiles
+                                              : (int64_t)p.token_tiles * p.weight_tiles * p.groups;
+    if (split > 1 && tiles > t_step) tiles = t_step;   // a split grid has one tile per cluster
+
+    if (warp == 0) {
+        // ------------------------------ TMA producer ------------------------------
+        if (lane == 0) {
+            ptx::prefetch_tensormap(&mapP);
+            ptx::prefetch_tensormap(&mapQ);
+            const uint64_t policy = ptx::policy_evict_last();
+            uint32_t it = 0;
+            bool ok = true;
+            for (int64_t t = t_first; ok && t < tiles; t += t_step) {
+                const Fp8Item w = fp8_item<Cfg>(p, table, t, rank);
+                const int z = p.mode == kFp8GroupRows ? w.group : 0;
+                for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+                    const int s = (int)(it % STAGES);
+                    if (!ptx::wait_phase(empty_bar(s), ((it / STAGES) & 1) ^ 1)) {
+                        atomicOr(p.status, kStatusTimeout);
+                        ok = false;
+                        break;
+                    }
+                    ptx::mbar_arrive_expect_tx(full_bar(s), Cfg::STAGE_BYTES);
+                    ptx::tma_load_3d(stage_p(s), &mapP, full_bar(s), kb * kBlock, SWAP ? w.b_row : w.a_row,
+                                     SWAP ? z : 0, policy);
+                    ptx::tma_load_3d(stage_q(s), &mapQ, full_bar(s), kb * kBlock, SWAP ? w.a_row : w.b_row,
+                                     SWAP ? 0 : z, policy);
+                }
+            }
+            // Every byte bound for this CTA lands before it leaves.
+            for (uint32_t back = 0; back < STAGES && back < it; ++back) {
+                const uint32_t i = it - 1 - back;
+                if (!ptx::wait_phase(full_bar((int)(i % STAGES)), (i / STAGES) & 1)) atomicOr(p.status, kStatusTimeout);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------ MMA issuer ------------------------------
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_e4m3(128, BN);
+            uint32_t it = 0;
+            bool ok = true;
+            for (int64_t t = t_first; ok && t < tiles; t += t_step) {
+                const Fp8Item w = fp8_item<Cfg>(p, table, t, rank);
+                for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+                    const int s = (int)(it % STAGES), b = (int)(it % NBUF);
+                    if (!ptx::wait_phase(acce_bar(b), ((it / NBUF) & 1) ^ 1) ||
+                        !ptx::wait_phase(full_bar(s), (it / STAGES) & 1)) {
+                        atomicOr(p.status, kStatusTimeout);
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    const uint32_t d = taddr + (uint32_t)(b * BN);
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_f8(d, ptx::sdesc_kmajor(stage_p(s) + ks * 32, Cfg::ROW_BYTES),
+                               ptx::sdesc_kmajor(stage_q(s) + ks * 32, Cfg::ROW_BYTES), idesc, ks != 0 ? 1u : 0u);
+                    ptx::mma_commit(empty_bar(s));
+                    ptx::mma_commit(accf_bar(b));
+                }
+            }
+            // Everything issued finishes before TMEM is released.
+            ptx::mma_commit(drain_bar);
+            if (!ptx::wait_phase(drain_bar, 0)) atomicOr(p.status, kStatusTimeout);
+        }
+        __syncwarp();
+    } else if (warp < 4) {
+        // ------------------------------ scales ------------------------------
+        // Slot: [0, 128) of the lanes (or [0] alone where they share one),
+        // [128, 128 + BN) of the columns (or one for each 128 of them).
+        const int th = threadIdx.x - 64;
+        uint32_t it = 0;
+        bool ok = true;
+        for (int64_t t = t_first; ok && t < tiles; t += t_step) {
+            const Fp8Item w = fp8_item<Cfg>(p, table, t, rank);
+            const float *sbg = p.sb + (p.mode == kFp8GroupRows ? w.group * p.stride_sb : 0);
+            for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+                const int s = (int)(it % SD);
+                if (!ptx::wait_phase_warp(sempty_bar(s), ((it / SD) & 1) ^ 1)) {
+                    if (lane == 0) atomicOr(p.status, kStatusTimeout);
+                    ok = false;
+                    break;
+                }
+                const uint32_t slot = scale_slot(s);
+                const float *sa = p.sa + (int64_t)kb * p.ld_sa;
+                const uint32_t a_at = slot + (SWAP ? 128 * 4 : 0), b_at = slot + (SWAP ? 0 : 128 * 4);
+                constexpr int ta = SWAP ? BN : 128, tb = SWAP ? 128 : BN;
+                for (int i = th; i < ta; i += 64) {
+                    const bool there = w.a_row + i < w.a_end;
+                    cp_async_4(a_at + 4 * i, there ? sa + w.a_row + i : p.sa, there);
+                }
+                if constexpr (ROWS_FORM) {
+                    const float *sb = p.sb + (int64_t)kb * p.ld_sb;
+                    for (int i = th; i < tb; i += 64) {
+                        const bool there = w.b_row + i < p.N;
+                        cp_async_4(b_at + 4 * i, there ? sb + w.b_row + i : p.sb, there);
+                    }
+                } else if (th < (tb + 127) / 128) {
+                    const int row = w.b_row + 128 * th;
+                    const bool there = row < p.N;
+                    cp_async_4(b_at + 4 * th, there ? sbg + (int64_t)(row / 128) * p.ld_sb + kb : p.sb, there);
+                }
+                cp_async_arrive(sfull_bar(s));
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
+        // ------------------------ promotion and epilogue ------------------------
+        const int ew = warp - 4, q = ew & 3, half = ew >> 2;
+        const int row = 32 * q + lane;                    // lane of tensor memory
+        uint32_t it = 0;
+        bool ok = true;
+        for (int64_t t = t_first; ok && t < tiles; t += t_step) {
+            const Fp8Item w = fp8_item<Cfg>(p, table, t, rank);
+            float2 acc[CW / 2];
+#pragma unroll
+            for (int j = 0; j < CW / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
+            for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+                const int s = (int)(it % SD), b = (int)(it % NBUF);
+                if (!ptx::wait_phase_warp(sfull_bar(s), (it / SD) & 1) ||
+                    !ptx::wait_phase_warp(accf_bar(b), (it / NBUF) & 1)) {
+                    if (lane == 0) atomicOr(p.status, kStatusTimeout);
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t slot = scale_slot(s);
+                float fl = ld_shared_f32(slot + (LANES_SCALED ? 4 * row : 0));
+                if constexpr (!COLS_SCALED) fl *= ld_shared_f32(slot + 128 * 4 + 4 * ((half * CW) / 128));
+                const float2 f2 = make_float2(fl, fl);
+                const uint32_t tm = taddr + ((uint32_t)(32 * q) << 16) + (uint32_t)(b * BN + half * CW);
+#pragma unroll
+                for (int c0 = 0; c0 < CW; c0 += CHUNK) {
+                    uint32_t v[CHUNK];
+                    tmem_ld_chunk<CHUNK>(tm + c0, v);
+                    tmem_ld_wait_for<CHUNK>(v);
+                    if (c0 == CW - CHUNK) {
+                        // The accumulator is read: the MMA warp may reuse it.
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(acce_bar(b));
+                    }
+#pragma unroll
+                    for (int j = 0; j < CHUNK; j += 4) {
+                        const float2 v0 = make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+                        const float2 v1 = make_float2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
+                        float2 &a0 = acc[(c0 + j) / 2], &a1 = acc[(c0 + j) / 2 + 1];
+                        if constexpr (COLS_SCALED) {
+                            const float4 sc = ld_shared_f32x4(slot + 128 * 4 + 4 * (half * CW + c0 + j));
+                            a0 = __ffma2_rn(__fmul2_rn(v0, f2), make_float2(sc.x, sc.y), a0);
+                            a1 = __ffma2_rn(__fmul2_rn(v1, f2), make_float2(sc.z, sc.w), a1);
+                        } else {
+                            a0 = __ffma2_rn(v0, f2, a0);
+                            a1 = __ffma2_rn(v1, f2, a1);
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(sempty_bar(s));
+            }
+            if (!ok && split == 1) break;
+            const int64_t c_base = p.mode == kFp8GroupK ? w.group * p.stride_c : 0;
+            if constexpr (SWAP) {
+                // Lane = row of B (column of C), column = row of A.
+                if (split == 1) {
+                    const int n = w.b_row + row;
+#pragma unroll
+                    for (int j = 0; j < CW; ++j) {
+                        const int m = w.a_row + half * CW + j;
+                        if (n < p.N && m < w.a_end)
+                            store_c(p, c_base + (int64_t)m * p.ldc + n, (j & 1) ? acc[j / 2].y : acc[j / 2].x);
+                    }
+                } else {
+                    const uint32_t part = base + Cfg::OFF_PARTIAL;
+#pragma unroll
+                    for (int j = 0; j < CW; ++j)
+                        st_shared_f32(part + 4 * ((half * CW + j) * 128 + row), (j & 1) ? acc[j / 2].y : acc[j / 2].x);
+                }
+            } else {
+                // Lane = row of A; 64 bytes of each of 32 rows at a time go
+                // through shared memory, so that a warp's stores cover whole
+                // 64-byte pieces of 8 rows instead of 16 bytes of 32.
+                const uint32_t st = base + Cfg::OFF_STAGING + ew * 2048;
+                const int row0 = w.a_row + 32 * q;
+                // Writes `cols` columns from col0 on: 16 floats, or 32 bfloat16.
+                auto flush = [&](const uint32_t (&u)[16], int cols, int col0) {
+                    __syncwarp();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        st_shared_u32x4(st + 64 * lane + 16 * (c ^ ((lane >> 1) & 3)),
+                                        make_uint4(u[4 * c], u[4 * c + 1], u[4 * c + 2], u[4 * c + 3]));
+                    __syncwarp();
+                    if (p.vec_c && p.beta == 0.0f && col0 + cols <= p.N) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = 8 * i + (lane >> 2), c = lane & 3;
+                            const uint4 x = ld_shared_u32x4(st + 64 * r + 16 * (c ^ ((r >> 1) & 3)));
+                            if (row0 + r < w.a_end) {
+                                const int64_t at = c_base + (int64_t)(row0 + r) * p.ldc + col0;
+                                *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.C) + at * (64 / cols) + 16 * c) = x;
+                            }
+                        }
+                        return;
+                    }
+                    for (int i = 0; i < cols; ++i) {
+                        const int e = 32 * i + lane, r = e / cols, c = e % cols, byte = c * (64 / cols);
+                        const uint32_t a = st + 64 * r + 16 * ((byte >> 4) ^ ((r >> 1) & 3)) + (byte & 15);
+                        if (row0 + r < w.a_end && col0 + c < p.N) {
+                            const int64_t at = c_base + (int64_t)(row0 + r) * p.ldc + col0 + c;
+                            if (cols == 32) {
+                                uint16_t x;
+                                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(a) : "memory");
+                                static_cast<uint16_t *>(p.C)[at] = x;
+                            } else {
+                                store_c(p, at, ld_shared_f32(a));
+                            }
+                        }
+                    }
+                };
+                const int col_base = w.b_row + half * CW;
+                uint32_t u[16];
+                if (p.c_bf16 && p.beta == 0.0f) {
+#pragma unroll
+                    for (int h = 0; h < CW; h += 32) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) u[j] = pack_bf16(acc[h / 2 + j].x, acc[h / 2 + j].y);
+                        flush(u, 32, col_base + h);
+                    }
+                } else {
+#pragma unroll
+                    for (int h = 0; h < CW; h += 16) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            u[j] = __float_as_uint((j & 1) ? acc[h / 2 + j / 2].y : acc[h / 2 + j / 2].x);
+                        flush(u, 16, col_base + h);
+                    }
+                }
+            }
+        }
+        ptx::tc_fence_before();
+    }
+
+    // ------------------------------ teardown ------------------------------
+    __syncthreads();
+    if constexpr (Cfg::CAN_SPLIT) {
+        if (split > 1) {
+            // One tile per cluster: every CTA's partial sums are in its
+            // shared memory. CTA `rank` adds every split-th column of the
+            // tile over the CTAs in rank order.
+            ptx::cluster_sync_all();
+            if (t_first < tiles) {
+                const Fp8Item w = fp8_item<Cfg>(p, table, t_first, rank);
+                const int64_t c_base = p.mode == kFp8GroupK ? w.group * p.stride_c : 0;
+                const uint32_t part = base + Cfg::OFF_PARTIAL;
+                for (int i = threadIdx.x; i < (BN / split) * 128; i += Cfg::THREADS) {
+                    const int col = (i >> 7) * split + rank, l = i & 127;
+                    const int m = w.a_row + col, n = w.b_row + l;
+                    if (m < w.a_end && n < p.N) {
+                        float v = 0.0f;
+                        for (int r = 0; r < split; ++r) v += ld_cluster_f32(part + 4 * (col * 128 + l), (uint32_t)r);
+                        store_c(p, c_base + (int64_t)m * p.ldc + n, v);
+                    }
+                }
+            }
+            ptx::cluster_sync_all();
+        }
+    }
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(taddr, Cfg::TMEM_COLS);
+    }
+}
+
+// Tensor map of an 8-bit operand: `rows` rows of K bytes, `groups` of them
+// `stride` bytes apart, in boxes of one K block by box_rows rows.
+cudaError_t encode_fp8(CUtensorMap *map, const uint8_t *ptr, int64_t rows, int64_t k, int64_t ld, int64_t groups,
+                       int64_t stride, int box_rows)
+{
+    static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+        void *fnp = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fnp, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            fnp = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fnp);
+    }();
+    if (!encode) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {(cuuint64_t)k, (cuuint64_t)rows, (cuuint64_t)groups};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld, (cuuint64_t)stride};
+    const cuuint32_t box[3] = {(cuuint32_t)kBlock, (cuuint32_t)box_rows, 1};
+    const cuuint32_t elem[3] = {1, 1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t *>(ptr), dims, strides, box,
+                              elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+using Wide256 = Fp8Cfg<256, false>;
+using Wide128 = Fp8Cfg<128, false>;
+using Swap128 = Fp8Cfg<128, true>;
+using Swap64 = Fp8Cfg<64, true>;
+using Swap32 = Fp8Cfg<32, true>;
+using Swap16 = Fp8Cfg<16, true>;
+
+template <class Cfg>
+cudaError_t prepare_cfg()
+{
+    cudaError_t e = cudaFuncSetAttribute(fp8_product_kernel<Cfg, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Cfg::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(fp8_product_kernel<Cfg, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Cfg::SMEM_BYTES);
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <class Cfg>
+cudaError_t launch_cfg(const Fp8Args &g, const Fp8Plan &plan, cudaStream_t stream)
+{
+    constexpr int tt = Cfg::SWAP ? Cfg::BN : 128, wt = Cfg::SWAP ? 128 : Cfg::BN;
+    CUtensorMap map_a, map_b;
+    const int64_t bg = g.mode == kFp8GroupRows ? g.groups : 1;
+    const int64_t sb = bg > 1 ? g.stride_b : (g.N * g.ldb);
+    cudaError_t e;
+    if (g.K > 0) {
+        e = encode_fp8(&map_a, g.A, g.M, g.K, g.lda, 1, g.M * g.lda, tt);
+        if (e == cudaSuccess) e = encode_fp8(&map_b, g.B, g.N, g.K, g.ldb, bg, sb, wt);
+    } else {
+        // The empty sum: no copy is ever issued, the maps only have to be valid.
+        const uint8_t *any = reinterpret_cast<const uint8_t *>(reinterpret_cast<uintptr_t>(g.C) & ~uintptr_t(15));
+        e = encode_fp8(&map_a, any, 1, 1, 16, 1, 16, tt);
+        if (e == cudaSuccess) e = encode_fp8(&map_b, any, 1, 1, 16, 1, 16, wt);
+    }
+    if (e != cudaSuccess) return e;
+    Fp8Params p{};
+    p.mode = g.mode;
+    p.M = (int)g.M;
+    p.N = (int)g.N;
+    p.nk = (int)ceil_div(g.K, kBlock);
+    p.sa = g.sa;
+    p.sb = g.sb;
+    p.ld_sa = g.ld_sa;
+    p.ld_sb = g.ld_sb;
+    p.stride_sb = g.stride_sb;
+    p.groups = g.groups;
+    p.offsets = g.offsets;
+    p.token_tiles = (int)ceil_div(g.M, tt);
+    p.weight_tiles = (int)ceil_div(g.N, wt);
+    p.split = plan.split;
+    p.beta = g.beta;
+    p.C = g.C;
+    p.ldc = g.ldc;
+    p.stride_c = g.stride_c;
+    p.c_bf16 = g.c_bf16;
+    const int64_t per16 = g.c_bf16 ? 8 : 4;
+    p.vec_c = ((reinterpret_cast<uintptr_t>(g.C) & 15u) == 0 && g.ldc % per16 == 0 &&
+               (g.mode != kFp8GroupK || g.stride_c % per16 == 0)) ? 1 : 0;
+    p.status = g.status;
+    CUtensorMap &mp = Cfg::SWAP ? map_b : map_a, &mq = Cfg::SWAP ? map_a : map_b;
+    void *args[] = {&mp, &mq, &p};
+    const void *fn = g.rows_form ? reinterpret_cast<const void *>(fp8_product_kernel<Cfg, true>)
+                                 : reinterpret_cast<const void *>(fp8_product_kernel<Cfg, false>);
+    cudaLaunchConfig_t lc = {};
+    cudaLaunchAttribute attrs[1];
+    if (plan.split > 1) {
+        attrs[0].id = cudaLaunchAttributeClusterDimension;
+        attrs[0].val.clusterDim.x = (unsigned)plan.split;
+        attrs[0].val.clusterDim.y = 1;
+        attrs[0].val.clusterDim.z = 1;
+        lc.attrs = attrs;
+        lc.numAttrs = 1;
+    }
+    lc.gridDim = dim3((unsigned)plan.grid);
+    lc.blockDim = dim3(Cfg::THREADS);
+    lc.dynamicSmemBytes = Cfg::SMEM_BYTES;
+    lc.stream = stream;
+    e = cudaLaunchKernelExC(&lc, fn, args);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+Fp8Plan plan_fp8(const Fp8Args &g)
+{
+    Fp8Plan p{256, false, 1, 0};
+    const int64_t nk = ceil_div(g.K, kBlock);
+    // Rows of A per group (all rows of a dense product).
+    const int64_t per = g.mode == kFp8GroupRows ? ceil_div(g.M, g.groups) : g.M;
+    if (g.mode != kFp8GroupK && per <= 128) {
+        p.swap = true;
+        p.cols = per <= 16 ? 16 : per <= 32 ? 32 : per <= 64 ? 64 : 128;
+    } else if (ceil_div(g.M, 128) * ceil_div(g.N, 256) * (g.mode == kFp8GroupK ? g.groups : 1) < g.num_sms) {
+        p.cols = 128;
+    }
+    const int tt = p.swap ? p.cols : 128, wt = p.swap ? 128 : p.cols;
+    const int64_t groups_hit = g.mode == kFp8GroupRows ? (g.groups < g.M ? g.groups : g.M) : 0;
+    int64_t tiles = (g.mode == kFp8GroupRows ? g.M / tt + groups_hit : ceil_div(g.M, tt)) * ceil_div(g.N, wt);
+    if (g.mode == kFp8GroupK) tiles *= g.groups;
+    // Few tiles: clusters of 2, 4 or 8 CTAs share each tile's K blocks.
+    if (p.swap && p.cols <= 64)
+        while (p.split < 8 && tiles * p.split * 2 <= g.num_sms && nk >= p.split * 4) p.split *= 2;
+    const int64_t most = g.num_sms / p.split * p.split;
+    p.grid = tiles * p.split < most ? tiles * p.split : most;
+    return p;
+}
+
+cudaError_t prepare_fp8()
+{
+    cudaError_t e = prepare_cfg<Wide256>();
+    if (e == cudaSuccess) e = prepare_cfg<Wide128>();
+    if (e == cudaSuccess) e = prepare_cfg<Swap128>();
+    if (e == cudaSuccess) e = prepare_cfg<Swap64>();
+    if (e == cudaSuccess) e = prepare_cfg<Swap32>();
+    if (e == cudaSuccess) e = prepare_cfg<Swap16>();
+    return e;
+}
+
+cudaError_t launch_fp8(const Fp8Args &g, cudaStream_t stream)
+{
+    const Fp8Plan p = plan_fp8(g);
+    if (!p.swap) return p.cols == 256 ? launch_cfg<Wide256>(g, p, stream) : launch_cfg<Wide128>(g, p, stream);
+    switch (p.cols) {
+    case 16: return launch_cfg<Swap16>(g, p, stream);
+    case 32: return launch_cfg<Swap32>(g, p, stream);
+    case 64: return launch_cfg<Swap64>(g, p, stream);
+    default: return launch_cfg<Swap128>(g, p, stream);
+    }
+}
+
+}  // namespace sgemm_gb300

@@ -4,6 +4,7 @@
 #include "../../include/sgemm.h"
 #include "common.cuh"
 #include "configs.cuh"
+#include "experts.cuh"
 #include "schedule.cuh"
 
 #include <atomic>
@@ -54,7 +55,7 @@ int device_state(DeviceState **out)
             cudaGetLastError();
             return SGEMM_ERR_CUDA;
         }
-        if (configs_prepare_device() != cudaSuccess) {
+        if (configs_prepare_device() != cudaSuccess || prepare_fp8() != cudaSuccess || prepare_route() != cudaSuccess) {
             cudaGetLastError();
             return SGEMM_ERR_CUDA;
         }
@@ -136,6 +137,17 @@ cudaError_t device_status_word(unsigned int **out)
 {
     return cudaGetSymbolAddress(reinterpret_cast<void **>(out), g_status_word);
 }
+
+int device_info(DeviceInfo *out)
+{
+    DeviceState *dev = nullptr;
+    const int rc = device_state(&dev);
+    if (rc != SGEMM_OK) return rc;
+    *out = DeviceInfo{dev->status, dev->num_sms, dev->pool};
+    return SGEMM_OK;
+}
+
+bool take_alloc_failure() { return take_test_alloc_failure(); }
 
 // Operand of a product that the TMA path reads in place only when its base
 // is 16-byte aligned and its rows are a multiple of 16 bytes long.
