@@ -50,6 +50,8 @@ namespace sgemm_gb300 {
 
 namespace {
 
+constexpr int kScaleBatch = 4;   // K blocks whose scales are handed over together
+
 template <int BN_, bool SWAP_>
 struct Fp8Cfg {
     static constexpr int BN = BN_;
@@ -65,12 +67,15 @@ struct Fp8Cfg {
     static constexpr int CW = BN / (EPI_WARPS / 4);          // columns per epilogue warp
     static constexpr int CHUNK = CW < 32 ? CW : 32;          // columns per tcgen05.ld
     static constexpr int THREADS = 128 + 32 * EPI_WARPS;
-    static constexpr int SDEPTH = BN == 256 ? 4 : 8;         // ring of scales
-    static constexpr int SLOT = 128 + BN;                    // floats of one slot
+    // Registers move from the first four warps to the eight that hold 128
+    // sums per thread: 168 * 384 at launch, 56 * 128 + 224 * 256 after.
+    static constexpr int EPI_REGS = BN == 256 ? 224 : 0;
+    static constexpr int SDEPTH = BN == 256 ? 2 : 3;         // ring of scales
+    static constexpr int SLOT = kScaleBatch * (128 + BN);    // floats of one slot
     static constexpr bool CAN_SPLIT = SWAP && BN <= 64;
     static constexpr int STAGING = SWAP ? 0 : EPI_WARPS * 2048;
     static constexpr int PARTIAL = CAN_SPLIT ? BN * 128 * 4 : 0;
-    static constexpr int NUM_BARS = 2 * STAGES + 2 * NBUF + 2 * SDEPTH + 1;
+    static constexpr int NUM_BARS = 2 * STAGES + NBUF + 2 * SDEPTH + 1;
     static constexpr int OFF_STAGING = STAGES * STAGE_BYTES;
     static constexpr int OFF_PARTIAL = OFF_STAGING + STAGING;
     static constexpr int OFF_SCALES = OFF_PARTIAL + PARTIAL;
@@ -132,7 +137,7 @@ __device__ __forceinline__ int find_group(const int *table, int groups, int x)
 constexpr int kRaster = 16;   // token tiles walked together, so that a wave of CTAs shares both operands in L2
 
 template <class Cfg>
-__device__ __forceinline__ Fp8Item fp8_item(const Fp8Params &p, const int *table, int64_t t, int rank)
+__device__ __forceinline__ Fp8Item fp8_item(const Fp8Params &p, const int *table, uint32_t t, int rank)
 {
     constexpr int TT = Cfg::SWAP ? Cfg::BN : 128;    // rows of A per tile
     constexpr int WT = Cfg::SWAP ? 128 : Cfg::BN;    // rows of B per tile
@@ -141,16 +146,16 @@ __device__ __forceinline__ Fp8Item fp8_item(const Fp8Params &p, const int *table
     int tokens = p.token_tiles;
     if (p.mode == kFp8GroupRows) tokens = table[p.groups];
     if (p.mode == kFp8GroupK) {
-        const int64_t per = (int64_t)p.token_tiles * p.weight_tiles;
+        const uint32_t per = (uint32_t)p.token_tiles * p.weight_tiles;
         it.group = (int)(t / per);
         t -= it.group * per;
     }
-    const int64_t band = (int64_t)kRaster * p.weight_tiles;
-    const int first = (int)(t / band) * kRaster;
-    const int high = tokens - first < kRaster ? tokens - first : kRaster;
-    const int r = (int)(t % band);
-    const int tt = first + r % high;
-    it.b_row = (r / high) * WT;
+    const uint32_t band = (uint32_t)kRaster * p.weight_tiles;
+    const uint32_t first = t / band * kRaster;
+    const uint32_t high = tokens - first < kRaster ? tokens - first : kRaster;
+    const uint32_t r = t % band;
+    const int tt = (int)(first + r % high);
+    it.b_row = (int)(r / high) * WT;
     if (p.mode == kFp8GroupRows) {
         it.group = find_group(table, p.groups, tt);
         int lo, hi;
@@ -185,6 +190,17 @@ __device__ __forceinline__ void store_c(const Fp8Params &p, int64_t at, float v)
     }
 }
 
+// One lane of a converged warp, always the same one. Loops that issue copies
+// or MMAs are run by the whole warp with the issue alone under this predicate:
+// inside a branch of one lane the compiler could keep neither the addresses
+// nor the descriptors in uniform registers, which the instructions take.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+
 // D (+)= P . Q^T on e4m3 operands, one thread issues.
 __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                        uint32_t accumulate)
@@ -203,11 +219,24 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n)
     return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
+// CHUNK consecutive columns of this warp's 32 lanes, and the wait for them.
+// Tensor memory is not memory to the compiler: both are ordered among the
+// volatile instructions (barriers, each other) and leave plain loads free to
+// move; the wait is tied to the loaded registers, so that no use of them can
+// be scheduled before it.
 template <int CHUNK>
 __device__ __forceinline__ void tmem_ld_chunk(uint32_t taddr, uint32_t (&v)[CHUNK])
 {
     if constexpr (CHUNK == 32) {
-        ptx::tmem_ld32(taddr, v);
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                     "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                     "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+                       "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+                       "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]),
+                       "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]),
+                       "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+                     : "r"(taddr));
     } else {
         static_assert(CHUNK == 16, "tensor memory chunk");
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -215,17 +244,14 @@ __device__ __forceinline__ void tmem_ld_chunk(uint32_t taddr, uint32_t (&v)[CHUN
                      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
                        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
                        "=r"(v[14]), "=r"(v[15])
-                     : "r"(taddr)
-                     : "memory");
+                     : "r"(taddr));
     }
 }
 
-// Waits for this thread's tcgen05.ld and ties the loaded registers to the
-// wait, so that no use of them can be scheduled before it.
 template <int CHUNK>
 __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&v)[CHUNK])
 {
-    ptx::tmem_ld_wait();
+    asm volatile("tcgen05.wait::ld.sync.aligned;");
 #pragma unroll
     for (int j = 0; j < CHUNK; j += 8)
         asm volatile("" : "+r"(v[j]), "+r"(v[j + 1]), "+r"(v[j + 2]), "+r"(v[j + 3]), "+r"(v[j + 4]), "+r"(v[j + 5]),
@@ -259,13 +285,6 @@ __device__ __forceinline__ float ld_shared_f32(uint32_t addr)
 {
     float v;
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
-
-__device__ __forceinline__ float4 ld_shared_f32x4(uint32_t addr)
-{
-    float4 v;
-    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
     return v;
 }
 
@@ -313,12 +332,12 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
     auto stage_p = [&](int s) { return base + s * Cfg::STAGE_BYTES; };
     auto stage_q = [&](int s) { return base + s * Cfg::STAGE_BYTES + Cfg::P_TILE; };
     auto full_bar = [&](int s) { return bars + 8u * s; };
-    auto empty_bar = [&](int s) { return bars + 8u * (STAGES + s); };
-    auto accf_bar = [&](int b) { return bars + 8u * (2 * STAGES + b); };
-    auto acce_bar = [&](int b) { return bars + 8u * (2 * STAGES + NBUF + b); };
-    auto sfull_bar = [&](int s) { return bars + 8u * (2 * STAGES + 2 * NBUF + s); };
-    auto sempty_bar = [&](int s) { return bars + 8u * (2 * STAGES + 2 * NBUF + SD + s); };
-    const uint32_t drain_bar = bars + 8u * (2 * STAGES + 2 * NBUF + 2 * SD);
+    // MMAs of a stage done: the stage is free and its accumulator is complete.
+    auto done_bar = [&](int s) { return bars + 8u * (STAGES + s); };
+    auto acce_bar = [&](int b) { return bars + 8u * (2 * STAGES + b); };
+    auto sfull_bar = [&](int s) { return bars + 8u * (2 * STAGES + NBUF + s); };
+    auto sempty_bar = [&](int s) { return bars + 8u * (2 * STAGES + NBUF + SD + s); };
+    const uint32_t drain_bar = bars + 8u * (2 * STAGES + NBUF + 2 * SD);
     const uint32_t tmem_slot = bars + 8u * Cfg::NUM_BARS;
     auto scale_slot = [&](int s) { return base + Cfg::OFF_SCALES + s * (Cfg::SLOT * 4); };
 
@@ -334,12 +353,9 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             ptx::mbar_init(full_bar(s), 1);
-            ptx::mbar_init(empty_bar(s), 1);
+            ptx::mbar_init(done_bar(s), 1);
         }
-        for (int b = 0; b < NBUF; ++b) {
-            ptx::mbar_init(accf_bar(b), 1);
-            ptx::mbar_init(acce_bar(b), Cfg::EPI_WARPS);
-        }
+        for (int b = 0; b < NBUF; ++b) ptx::mbar_init(acce_bar(b), Cfg::EPI_WARPS);
         for (int s = 0; s < SD; ++s) {
             ptx::mbar_init(sfull_bar(s), 64);
             ptx::mbar_init(sempty_bar(s), Cfg::EPI_WARPS);
@@ -371,7 +387,7 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
                 }
                 // Offsets that are not a partition may sum to anything: no
                 // entry passes what the kernel can walk.
-                const int64_t most = p.mode == kFp8GroupK ? p.nk : (1 << 30);
+                const int64_t most = p.mode == kFp8GroupK ? p.nk : INT32_MAX / p.weight_tiles - 2 * kRaster;
                 const int64_t before = carry + sum - mine;
                 if (g < p.groups) table[g] = (int)(before < most ? before : most);
                 carry += __shfl_sync(0xffffffffu, sum, 31);
@@ -384,110 +400,127 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
     ptx::tc_fence_after();
     const uint32_t taddr = *reinterpret_cast<uint32_t *>(smem_raw + (tmem_slot - raw));
 
-    const int64_t t_first = (int64_t)blockIdx.x / split, t_step = (int64_t)gridDim.x / split;
-    int64_t tiles = p.mode == kFp8Dense       ? (int64_t)p.token_tiles * p.weight_tiles
-                    : p.mode == kFp8GroupRows ? (int64_t)table[p.groups] * p.weight_tiles
-                                              : (int64_t)p.token_tiles * p.weight_tiles * p.groups;
+    const uint32_t t_first = blockIdx.x / split, t_step = gridDim.x / split;
+    uint32_t tiles = (uint32_t)p.weight_tiles * (uint32_t)(p.mode == kFp8Dense       ? p.token_tiles
+                                                           : p.mode == kFp8GroupRows ? table[p.groups]
+                                                                                     : p.token_tiles * p.groups);
     if (split > 1 && tiles > t_step) tiles = t_step;   // a split grid has one tile per cluster
 
+    if constexpr (Cfg::EPI_REGS > 0) {
+        if (warp < 4) ptx::setmaxnreg_dec<56>();
+    }
     if (warp == 0) {
         // ------------------------------ TMA producer ------------------------------
-        if (lane == 0) {
+        if (elect_one()) {
             ptx::prefetch_tensormap(&mapP);
             ptx::prefetch_tensormap(&mapQ);
-            const uint64_t policy = ptx::policy_evict_last();
-            uint32_t it = 0;
-            bool ok = true;
-            for (int64_t t = t_first; ok && t < tiles; t += t_step) {
-                const Fp8Item w = fp8_item<Cfg>(p, table, t, rank);
-                const int z = p.mode == kFp8GroupRows ? w.group : 0;
-                for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
-                    const int s = (int)(it % STAGES);
-                    if (!ptx::wait_phase(empty_bar(s), ((it / STAGES) & 1) ^ 1)) {
-                        atomicOr(p.status, kStatusTimeout);
-                        ok = false;
-                        break;
-                    }
+        }
+        const uint64_t policy = ptx::policy_evict_last();
+        uint32_t it = 0;
+        bool ok = true;
+        for (uint32_t t = t_first; ok && t < tiles; t += t_step) {
+            const Fp8Item w = fp8_item<Cfg>(p, table, t, rank);
+            const int z = p.mode == kFp8GroupRows ? w.group : 0;
+            for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+                const int s = (int)(it % STAGES);
+                if (!ptx::wait_phase_warp(done_bar(s), ((it / STAGES) & 1) ^ 1)) {
+                    if (lane == 0) atomicOr(p.status, kStatusTimeout);
+                    ok = false;
+                    break;
+                }
+                if (elect_one()) {
                     ptx::mbar_arrive_expect_tx(full_bar(s), Cfg::STAGE_BYTES);
                     ptx::tma_load_3d(stage_p(s), &mapP, full_bar(s), kb * kBlock, SWAP ? w.b_row : w.a_row,
                                      SWAP ? z : 0, policy);
                     ptx::tma_load_3d(stage_q(s), &mapQ, full_bar(s), kb * kBlock, SWAP ? w.a_row : w.b_row,
                                      SWAP ? 0 : z, policy);
                 }
-            }
-            // Every byte bound for this CTA lands before it leaves.
-            for (uint32_t back = 0; back < STAGES && back < it; ++back) {
-                const uint32_t i = it - 1 - back;
-                if (!ptx::wait_phase(full_bar((int)(i % STAGES)), (i / STAGES) & 1)) atomicOr(p.status, kStatusTimeout);
+                __syncwarp();
             }
         }
-        __syncwarp();
+        // Every byte bound for this CTA lands before it leaves.
+        for (uint32_t back = 0; back < STAGES && back < it; ++back) {
+            const uint32_t i = it - 1 - back;
+            if (!ptx::wait_phase_warp(full_bar((int)(i % STAGES)), (i / STAGES) & 1) && lane == 0)
+                atomicOr(p.status, kStatusTimeout);
+        }
     } else if (warp == 1) {
         // ------------------------------ MMA issuer ------------------------------
-        if (lane == 0) {
-            constexpr uint32_t idesc = idesc_e4m3(128, BN);
-            uint32_t it = 0;
-            bool ok = true;
-            for (int64_t t = t_first; ok && t < tiles; t += t_step) {
-                const Fp8Item w = fp8_item<Cfg>(p, table, t, rank);
-                for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
-                    const int s = (int)(it % STAGES), b = (int)(it % NBUF);
-                    if (!ptx::wait_phase(acce_bar(b), ((it / NBUF) & 1) ^ 1) ||
-                        !ptx::wait_phase(full_bar(s), (it / STAGES) & 1)) {
-                        atomicOr(p.status, kStatusTimeout);
-                        ok = false;
-                        break;
-                    }
-                    ptx::tc_fence_after();
+        constexpr uint32_t idesc = idesc_e4m3(128, BN);
+        const uint64_t desc_p = ptx::sdesc_kmajor(stage_p(0), Cfg::ROW_BYTES);
+        const uint64_t desc_q = ptx::sdesc_kmajor(stage_q(0), Cfg::ROW_BYTES);
+        uint32_t it = 0;
+        bool ok = true;
+        for (uint32_t t = t_first; ok && t < tiles; t += t_step) {
+            const Fp8Item w = fp8_item<Cfg>(p, table, t, rank);
+            for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+                const int s = (int)(it % STAGES), b = (int)(it % NBUF);
+                if (!ptx::wait_phase_warp(acce_bar(b), ((it / NBUF) & 1) ^ 1) ||
+                    !ptx::wait_phase_warp(full_bar(s), (it / STAGES) & 1)) {
+                    if (lane == 0) atomicOr(p.status, kStatusTimeout);
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                if (elect_one()) {
+                    // Addresses in the descriptors count 16 bytes.
                     const uint32_t d = taddr + (uint32_t)(b * BN);
+                    const uint64_t off = (uint64_t)(s * (Cfg::STAGE_BYTES / 16));
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
-                        mma_f8(d, ptx::sdesc_kmajor(stage_p(s) + ks * 32, Cfg::ROW_BYTES),
-                               ptx::sdesc_kmajor(stage_q(s) + ks * 32, Cfg::ROW_BYTES), idesc, ks != 0 ? 1u : 0u);
-                    ptx::mma_commit(empty_bar(s));
-                    ptx::mma_commit(accf_bar(b));
+                        mma_f8(d, desc_p + off + 2 * ks, desc_q + off + 2 * ks, idesc, ks != 0 ? 1u : 0u);
+                    ptx::mma_commit(done_bar(s));
                 }
+                __syncwarp();
             }
-            // Everything issued finishes before TMEM is released.
-            ptx::mma_commit(drain_bar);
-            if (!ptx::wait_phase(drain_bar, 0)) atomicOr(p.status, kStatusTimeout);
         }
+        // Everything issued finishes before TMEM is released.
+        if (elect_one()) ptx::mma_commit(drain_bar);
         __syncwarp();
+        if (!ptx::wait_phase_warp(drain_bar, 0) && lane == 0) atomicOr(p.status, kStatusTimeout);
     } else if (warp < 4) {
         // ------------------------------ scales ------------------------------
-        // Slot: [0, 128) of the lanes (or [0] alone where they share one),
-        // [128, 128 + BN) of the columns (or one for each 128 of them).
+        // A slot holds the scales of up to kScaleBatch K blocks of one tile:
+        // 128 per block for the lanes (or the first alone where they share
+        // one), then BN per block for the columns (or one per 128 of them).
         const int th = threadIdx.x - 64;
         uint32_t it = 0;
         bool ok = true;
-        for (int64_t t = t_first; ok && t < tiles; t += t_step) {
+        for (uint32_t t = t_first; ok && t < tiles; t += t_step) {
             const Fp8Item w = fp8_item<Cfg>(p, table, t, rank);
             const float *sbg = p.sb + (p.mode == kFp8GroupRows ? w.group * p.stride_sb : 0);
-            for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+            constexpr int ta = SWAP ? BN : 128, tb = SWAP ? 128 : BN;
+            for (int k0 = w.kb0; k0 < w.kb1; k0 += kScaleBatch, ++it) {
                 const int s = (int)(it % SD);
                 if (!ptx::wait_phase_warp(sempty_bar(s), ((it / SD) & 1) ^ 1)) {
                     if (lane == 0) atomicOr(p.status, kStatusTimeout);
                     ok = false;
                     break;
                 }
-                const uint32_t slot = scale_slot(s);
-                const float *sa = p.sa + (int64_t)kb * p.ld_sa;
-                const uint32_t a_at = slot + (SWAP ? 128 * 4 : 0), b_at = slot + (SWAP ? 0 : 128 * 4);
-                constexpr int ta = SWAP ? BN : 128, tb = SWAP ? 128 : BN;
-                for (int i = th; i < ta; i += 64) {
-                    const bool there = w.a_row + i < w.a_end;
-                    cp_async_4(a_at + 4 * i, there ? sa + w.a_row + i : p.sa, there);
-                }
-                if constexpr (ROWS_FORM) {
-                    const float *sb = p.sb + (int64_t)kb * p.ld_sb;
-                    for (int i = th; i < tb; i += 64) {
-                        const bool there = w.b_row + i < p.N;
-                        cp_async_4(b_at + 4 * i, there ? sb + w.b_row + i : p.sb, there);
+                const uint32_t slot = base + Cfg::OFF_SCALES + s * (Cfg::SLOT * 4);
+                const int blocks = w.kb1 - k0 < kScaleBatch ? w.kb1 - k0 : kScaleBatch;
+                for (int j = 0; j < blocks; ++j) {
+                    const int kb = k0 + j;
+                    const uint32_t lanes_at = slot + 4 * (128 * j), cols_at = slot + 4 * (kScaleBatch * 128 + BN * j);
+                    const uint32_t a_at = SWAP ? cols_at : lanes_at, b_at = SWAP ? lanes_at : cols_at;
+                    const float *sa = p.sa + (int64_t)kb * p.ld_sa;
+#pragma unroll
+                    for (int i = th; i < ta; i += 64) {
+                        const bool there = w.a_row + i < w.a_end;
+                        cp_async_4(a_at + 4 * i, there ? sa + w.a_row + i : p.sa, there);
                     }
-                } else if (th < (tb + 127) / 128) {
-                    const int row = w.b_row + 128 * th;
-                    const bool there = row < p.N;
-                    cp_async_4(b_at + 4 * th, there ? sbg + (int64_t)(row / 128) * p.ld_sb + kb : p.sb, there);
+                    if constexpr (ROWS_FORM) {
+                        const float *sb = p.sb + (int64_t)kb * p.ld_sb;
+#pragma unroll
+                        for (int i = th; i < tb; i += 64) {
+                            const bool there = w.b_row + i < p.N;
+                            cp_async_4(b_at + 4 * i, there ? sb + w.b_row + i : p.sb, there);
+                        }
+                    } else if (th < (tb + 127) / 128) {
+                        const int row = w.b_row + 128 * th;
+                        const bool there = row < p.N;
+                        cp_async_4(b_at + 4 * th, there ? sbg + (int64_t)(row / 128) * p.ld_sb + kb : p.sb, there);
+                    }
                 }
                 cp_async_arrive(sfull_bar(s));
             }
@@ -497,55 +530,97 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
         // ------------------------ promotion and epilogue ------------------------
         const int ew = warp - 4, q = ew & 3, half = ew >> 2;
         const int row = 32 * q + lane;                    // lane of tensor memory
-        uint32_t it = 0;
+        const uint32_t lanes = taddr + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * CW);
+        const float *const slots = reinterpret_cast<const float *>(smem_raw + (base - raw) + Cfg::OFF_SCALES);
+        if constexpr (Cfg::EPI_REGS > 0) ptx::setmaxnreg_inc<Cfg::EPI_REGS>();
+        uint32_t it = 0, batch = 0;
         bool ok = true;
-        for (int64_t t = t_first; ok && t < tiles; t += t_step) {
+        for (uint32_t t = t_first; ok && t < tiles; t += t_step) {
             const Fp8Item w = fp8_item<Cfg>(p, table, t, rank);
             float2 acc[CW / 2];
 #pragma unroll
             for (int j = 0; j < CW / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
-            for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
-                const int s = (int)(it % SD), b = (int)(it % NBUF);
-                if (!ptx::wait_phase_warp(sfull_bar(s), (it / SD) & 1) ||
-                    !ptx::wait_phase_warp(accf_bar(b), (it / NBUF) & 1)) {
+            // The loads run one chunk ahead of the sums, across K blocks too:
+            // the next block's first chunk is requested before this block's
+            // last one is added.
+            uint32_t v[2][CHUNK];
+            float2 f2 = make_float2(0.0f, 0.0f);
+            const float *cols = nullptr;
+            auto begin = [&](uint32_t i, uint32_t (&dst)[CHUNK]) {
+                if (!ptx::wait_phase_warp(done_bar((int)(i % STAGES)), (i / STAGES) & 1)) {
                     if (lane == 0) atomicOr(p.status, kStatusTimeout);
-                    ok = false;
-                    break;
+                    return false;
                 }
                 ptx::tc_fence_after();
-                const uint32_t slot = scale_slot(s);
-                float fl = ld_shared_f32(slot + (LANES_SCALED ? 4 * row : 0));
-                if constexpr (!COLS_SCALED) fl *= ld_shared_f32(slot + 128 * 4 + 4 * ((half * CW) / 128));
-                const float2 f2 = make_float2(fl, fl);
-                const uint32_t tm = taddr + ((uint32_t)(32 * q) << 16) + (uint32_t)(b * BN + half * CW);
+                tmem_ld_chunk<CHUNK>(lanes + (uint32_t)((int)(i % NBUF) * BN), dst);
+                return true;
+            };
+            // Scales of K block j of the current batch.
+            auto scales_of = [&](int j) {
+                const float *slot = slots + (int)(batch % SD) * Cfg::SLOT;
+                cols = slot + kScaleBatch * 128 + BN * j + half * CW;
+                float fl = slot[128 * j + (LANES_SCALED ? row : 0)];
+                if constexpr (!COLS_SCALED) fl *= slot[kScaleBatch * 128 + BN * j + (half * CW) / 128];
+                f2 = make_float2(fl, fl);
+            };
+            auto add = [&](int c0, const uint32_t (&x)[CHUNK]) {
 #pragma unroll
-                for (int c0 = 0; c0 < CW; c0 += CHUNK) {
-                    uint32_t v[CHUNK];
-                    tmem_ld_chunk<CHUNK>(tm + c0, v);
-                    tmem_ld_wait_for<CHUNK>(v);
-                    if (c0 == CW - CHUNK) {
-                        // The accumulator is read: the MMA warp may reuse it.
-                        ptx::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(acce_bar(b));
-                    }
-#pragma unroll
-                    for (int j = 0; j < CHUNK; j += 4) {
-                        const float2 v0 = make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
-                        const float2 v1 = make_float2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
-                        float2 &a0 = acc[(c0 + j) / 2], &a1 = acc[(c0 + j) / 2 + 1];
-                        if constexpr (COLS_SCALED) {
-                            const float4 sc = ld_shared_f32x4(slot + 128 * 4 + 4 * (half * CW + c0 + j));
-                            a0 = __ffma2_rn(__fmul2_rn(v0, f2), make_float2(sc.x, sc.y), a0);
-                            a1 = __ffma2_rn(__fmul2_rn(v1, f2), make_float2(sc.z, sc.w), a1);
-                        } else {
-                            a0 = __ffma2_rn(v0, f2, a0);
-                            a1 = __ffma2_rn(v1, f2, a1);
-                        }
+                for (int j = 0; j < CHUNK; j += 4) {
+                    const float2 v0 = make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+                    const float2 v1 = make_float2(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
+                    float2 &a0 = acc[(c0 + j) / 2], &a1 = acc[(c0 + j) / 2 + 1];
+                    if constexpr (COLS_SCALED) {
+                        const float4 sc = *reinterpret_cast<const float4 *>(cols + c0 + j);
+                        a0 = __ffma2_rn(__fmul2_rn(v0, f2), make_float2(sc.x, sc.y), a0);
+                        a1 = __ffma2_rn(__fmul2_rn(v1, f2), make_float2(sc.z, sc.w), a1);
+                    } else {
+                        a0 = __ffma2_rn(v0, f2, a0);
+                        a1 = __ffma2_rn(v1, f2, a1);
                     }
                 }
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(sempty_bar(s));
+            };
+            constexpr int NCH = CW / CHUNK;
+            if (w.kb0 < w.kb1) ok = begin(it, v[0]);
+            // Two K blocks per round where a block is one chunk, so that the
+            // register buffers' roles are known at compile time.
+            constexpr int ROUND = NCH == 1 ? 2 : 1;
+            static_assert(NCH == 1 || NCH % 2 == 0, "chunks alternate between two buffers");
+            int j = 0;                                    // K block of the batch
+            for (int kb = w.kb0; ok && kb < w.kb1;) {
+#pragma unroll
+                for (int h = 0; h < ROUND; ++h) {
+                    if (!ok || kb >= w.kb1) break;
+                    const int b = (int)(it % NBUF);
+                    if (j == 0 && !ptx::wait_phase_warp(sfull_bar((int)(batch % SD)), (batch / SD) & 1)) {
+                        if (lane == 0) atomicOr(p.status, kStatusTimeout);
+                        ok = false;
+                        break;
+                    }
+                    scales_of(j);
+#pragma unroll
+                    for (int c = 0; c < NCH; ++c) {
+                        const int at = NCH == 1 ? h : c & 1;
+                        tmem_ld_wait_for<CHUNK>(v[at]);
+                        if (c + 1 < NCH) {
+                            tmem_ld_chunk<CHUNK>(lanes + (uint32_t)(b * BN + (c + 1) * CHUNK), v[at ^ 1]);
+                        } else {
+                            // The accumulator is read: the MMA warp may reuse it.
+                            ptx::tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) ptx::mbar_arrive(acce_bar(b));
+                            if (kb + 1 < w.kb1) ok = begin(it + 1, v[at ^ 1]);
+                        }
+                        add(c * CHUNK, v[at]);
+                    }
+                    ++it;
+                    ++kb;
+                    if (++j == kScaleBatch || kb == w.kb1) {
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(sempty_bar((int)(batch % SD)));
+                        ++batch;
+                        j = 0;
+                    }
+                }
             }
             if (!ok && split == 1) break;
             const int64_t c_base = p.mode == kFp8GroupK ? w.group * p.stride_c : 0;
@@ -735,6 +810,11 @@ cudaError_t launch_cfg(const Fp8Args &g, const Fp8Plan &plan, cudaStream_t strea
     p.offsets = g.offsets;
     p.token_tiles = (int)ceil_div(g.M, tt);
     p.weight_tiles = (int)ceil_div(g.N, wt);
+    // Tiles are counted in 32 bits (2^31 of them would be a C of 2^42 elements).
+    const int64_t groups_hit = g.groups < g.M ? g.groups : g.M;
+    const int64_t tokens = g.mode == kFp8Dense ? p.token_tiles
+                           : g.mode == kFp8GroupRows ? g.M / tt + groups_hit : (int64_t)p.token_tiles * g.groups;
+    if (tokens + 2 * kRaster > INT32_MAX / p.weight_tiles - 2 * kRaster) return cudaErrorInvalidValue;
     p.split = plan.split;
     p.beta = g.beta;
     p.C = g.C;
