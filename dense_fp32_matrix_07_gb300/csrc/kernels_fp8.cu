@@ -45,12 +45,13 @@
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
+#include <type_traits>
 
 namespace sgemm_gb300 {
 
 namespace {
 
-constexpr int kScaleBatch = 4;   // K blocks whose scales are handed over together
+constexpr int kScaleBatch = 2;   // K blocks whose scales are handed over together
 
 template <int BN_, bool SWAP_>
 struct Fp8Cfg {
@@ -65,12 +66,12 @@ struct Fp8Cfg {
     static constexpr int TMEM_COLS = NBUF * BN < 32 ? 32 : NBUF * BN;
     static constexpr int EPI_WARPS = BN >= 128 ? 8 : 4;
     static constexpr int CW = BN / (EPI_WARPS / 4);          // columns per epilogue warp
-    static constexpr int CHUNK = CW < 32 ? CW : 32;          // columns per tcgen05.ld
+    static constexpr int CHUNK = CW < 32 || BN == 256 ? 16 : 32;          // columns per tcgen05.ld
     static constexpr int THREADS = 128 + 32 * EPI_WARPS;
     // Registers move from the first four warps to the eight that hold 128
     // sums per thread: 168 * 384 at launch, 56 * 128 + 224 * 256 after.
-    static constexpr int EPI_REGS = BN == 256 ? 224 : 0;
-    static constexpr int SDEPTH = BN == 256 ? 2 : 3;         // ring of scales
+    static constexpr int EPI_REGS = BN == 256 ? 224 : BN == 128 ? 200 : 0;
+    static constexpr int SDEPTH = BN == 256 ? 4 : 6;         // ring of scales
     static constexpr int SLOT = kScaleBatch * (128 + BN);    // floats of one slot
     static constexpr bool CAN_SPLIT = SWAP && BN <= 64;
     static constexpr int STAGING = SWAP ? 0 : EPI_WARPS * 2048;
@@ -190,25 +191,82 @@ __device__ __forceinline__ void store_c(const Fp8Params &p, int64_t at, float v)
     }
 }
 
-// One lane of a converged warp, always the same one. Loops that issue copies
-// or MMAs are run by the whole warp with the issue alone under this predicate:
-// inside a branch of one lane the compiler could keep neither the addresses
-// nor the descriptors in uniform registers, which the instructions take.
-__device__ __forceinline__ bool elect_one()
+// The loops of the roles are straight lines: a taken branch costs an
+// instruction fetch of 50 to 100 cycles here, where twelve warps run five
+// different pieces of code, and these loops have about 500 cycles per K block.
+// So copies, MMAs and arrivals are predicated instructions (`on` nonzero in
+// the one lane that issues them) instead of branches of one lane, loops run
+// over whole batches of K blocks, and waits branch away only to wait.
+
+// Nonzero in one lane of a converged warp, always the same one.
+__device__ __forceinline__ uint32_t elect_one()
 {
     uint32_t one;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
-    return one != 0;
+    return one;
 }
 
-// D (+)= P . Q^T on e4m3 operands, one thread issues.
-__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                       uint32_t accumulate)
+__device__ __forceinline__ void mbar_arrive_if(uint32_t on, uint32_t bar)
+{
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+                 "@q mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
+                 "r"(on)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mbar_expect_if(uint32_t on, uint32_t bar, uint32_t bytes)
+{
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
+                 "@q mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+                 "r"(bytes), "r"(on)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_load_if(uint32_t on, uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t x,
+                                            int32_t y, int32_t z, uint64_t policy)
+{
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %7, 0;\n\t"
+                 "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+                 " [%0], [%1, {%2, %3, %4}], [%5], %6;\n\t}" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy), "r"(on)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mma_commit_if(uint32_t on, uint32_t bar)
+{
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+                 "r"(on)
+                 : "memory");
+}
+
+// Whether phase `parity` of the barrier is complete, without waiting. A wait
+// costs over a hundred cycles even when there is nothing to wait for, so the
+// loops below look at the next block's barriers while they work on this one,
+// and wait only where that look came too early.
+__device__ __forceinline__ uint32_t mbar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return done;
+}
+
+// ptx::wait_phase_warp(), off the straight line: `early` is mbar_test()'s look.
+#define FP8_WAIT(early, bar, parity) \
+    (__builtin_expect(__all_sync(0xffffffffu, (early)) != 0, 1) || ptx::wait_phase_warp(bar, parity))
+
+// D (+)= P . Q^T on e4m3 operands.
+__device__ __forceinline__ void mma_f8_if(uint32_t on, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(on)
         : "memory");
 }
 
@@ -407,11 +465,12 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
     if (split > 1 && tiles > t_step) tiles = t_step;   // a split grid has one tile per cluster
 
     if constexpr (Cfg::EPI_REGS > 0) {
-        if (warp < 4) ptx::setmaxnreg_dec<56>();
+        if (warp < 4) ptx::setmaxnreg_dec<BN == 256 ? 56 : 104>();
     }
     if (warp == 0) {
         // ------------------------------ TMA producer ------------------------------
-        if (elect_one()) {
+        const uint32_t on = elect_one();
+        if (on) {
             ptx::prefetch_tensormap(&mapP);
             ptx::prefetch_tensormap(&mapQ);
         }
@@ -423,19 +482,17 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
             const int z = p.mode == kFp8GroupRows ? w.group : 0;
             for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
                 const int s = (int)(it % STAGES);
-                if (!ptx::wait_phase_warp(done_bar(s), ((it / STAGES) & 1) ^ 1)) {
+                const uint32_t phase = ((it / STAGES) & 1) ^ 1;
+                if (!FP8_WAIT(mbar_test(done_bar(s), phase), done_bar(s), phase)) {
                     if (lane == 0) atomicOr(p.status, kStatusTimeout);
                     ok = false;
                     break;
                 }
-                if (elect_one()) {
-                    ptx::mbar_arrive_expect_tx(full_bar(s), Cfg::STAGE_BYTES);
-                    ptx::tma_load_3d(stage_p(s), &mapP, full_bar(s), kb * kBlock, SWAP ? w.b_row : w.a_row,
-                                     SWAP ? z : 0, policy);
-                    ptx::tma_load_3d(stage_q(s), &mapQ, full_bar(s), kb * kBlock, SWAP ? w.a_row : w.b_row,
-                                     SWAP ? 0 : z, policy);
-                }
-                __syncwarp();
+                mbar_expect_if(on, full_bar(s), Cfg::STAGE_BYTES);
+                tma_load_if(on, stage_p(s), &mapP, full_bar(s), kb * kBlock, SWAP ? w.b_row : w.a_row, SWAP ? z : 0,
+                            policy);
+                tma_load_if(on, stage_q(s), &mapQ, full_bar(s), kb * kBlock, SWAP ? w.a_row : w.b_row, SWAP ? 0 : z,
+                            policy);
             }
         }
         // Every byte bound for this CTA lands before it leaves.
@@ -449,34 +506,35 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
         constexpr uint32_t idesc = idesc_e4m3(128, BN);
         const uint64_t desc_p = ptx::sdesc_kmajor(stage_p(0), Cfg::ROW_BYTES);
         const uint64_t desc_q = ptx::sdesc_kmajor(stage_q(0), Cfg::ROW_BYTES);
-        uint32_t it = 0;
+        const uint32_t on = elect_one();
+        uint32_t it = 0, early = 0;
         bool ok = true;
         for (uint32_t t = t_first; ok && t < tiles; t += t_step) {
             const Fp8Item w = fp8_item<Cfg>(p, table, t, rank);
             for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
                 const int s = (int)(it % STAGES), b = (int)(it % NBUF);
-                if (!ptx::wait_phase_warp(acce_bar(b), ((it / NBUF) & 1) ^ 1) ||
-                    !ptx::wait_phase_warp(full_bar(s), (it / STAGES) & 1)) {
+                if (!__builtin_expect(__all_sync(0xffffffffu, early) != 0, 1) &&
+                    (!ptx::wait_phase_warp(acce_bar(b), ((it / NBUF) & 1) ^ 1) ||
+                     !ptx::wait_phase_warp(full_bar(s), (it / STAGES) & 1))) {
                     if (lane == 0) atomicOr(p.status, kStatusTimeout);
                     ok = false;
                     break;
                 }
                 ptx::tc_fence_after();
-                if (elect_one()) {
-                    // Addresses in the descriptors count 16 bytes.
-                    const uint32_t d = taddr + (uint32_t)(b * BN);
-                    const uint64_t off = (uint64_t)(s * (Cfg::STAGE_BYTES / 16));
+                // Addresses in the descriptors count 16 bytes.
+                const uint32_t d = taddr + (uint32_t)(b * BN);
+                const uint64_t off = (uint64_t)(s * (Cfg::STAGE_BYTES / 16));
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        mma_f8(d, desc_p + off + 2 * ks, desc_q + off + 2 * ks, idesc, ks != 0 ? 1u : 0u);
-                    ptx::mma_commit(done_bar(s));
-                }
-                __syncwarp();
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_f8_if(on, d, desc_p + off + 2 * ks, desc_q + off + 2 * ks, idesc, ks != 0 ? 1u : 0u);
+                mma_commit_if(on, done_bar(s));
+                const uint32_t next = it + 1;
+                early = mbar_test(acce_bar((int)(next % NBUF)), ((next / NBUF) & 1) ^ 1) &
+                        mbar_test(full_bar((int)(next % STAGES)), (next / STAGES) & 1);
             }
         }
         // Everything issued finishes before TMEM is released.
-        if (elect_one()) ptx::mma_commit(drain_bar);
-        __syncwarp();
+        mma_commit_if(on, drain_bar);
         if (!ptx::wait_phase_warp(drain_bar, 0) && lane == 0) atomicOr(p.status, kStatusTimeout);
     } else if (warp < 4) {
         // ------------------------------ scales ------------------------------
@@ -544,26 +602,27 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
             // the next block's first chunk is requested before this block's
             // last one is added.
             uint32_t v[2][CHUNK];
-            float2 f2 = make_float2(0.0f, 0.0f);
-            const float *cols = nullptr;
-            auto begin = [&](uint32_t i, uint32_t (&dst)[CHUNK]) {
-                if (!ptx::wait_phase_warp(done_bar((int)(i % STAGES)), (i / STAGES) & 1)) {
-                    if (lane == 0) atomicOr(p.status, kStatusTimeout);
-                    return false;
-                }
+            float fl = 0.0f, fl_next = 0.0f;
+            const float *cols = nullptr, *cols_next = nullptr;
+            // Waits for block i's sums and requests their first chunk.
+            auto begin = [&](uint32_t i, uint32_t early, uint32_t (&dst)[CHUNK]) {
+                ok = ok && FP8_WAIT(early, done_bar((int)(i % STAGES)), (i / STAGES) & 1);
                 ptx::tc_fence_after();
                 tmem_ld_chunk<CHUNK>(lanes + (uint32_t)((int)(i % NBUF) * BN), dst);
-                return true;
             };
-            // Scales of K block j of the current batch.
-            auto scales_of = [&](int j) {
-                const float *slot = slots + (int)(batch % SD) * Cfg::SLOT;
-                cols = slot + kScaleBatch * 128 + BN * j + half * CW;
-                float fl = slot[128 * j + (LANES_SCALED ? row : 0)];
-                if constexpr (!COLS_SCALED) fl *= slot[kScaleBatch * 128 + BN * j + (half * CW) / 128];
-                f2 = make_float2(fl, fl);
+            auto batch_test = [&](uint32_t bt) { return mbar_test(sfull_bar((int)(bt % SD)), (bt / SD) & 1); };
+            auto batch_wait = [&](uint32_t bt, uint32_t early) {
+                ok = ok && FP8_WAIT(early, sfull_bar((int)(bt % SD)), (bt / SD) & 1);
+            };
+            // Scales of K block j of a batch: the lane's, and the columns' place.
+            auto scales_of = [&](uint32_t bt, int j, float &f, const float *&at) {
+                const float *slot = slots + (int)(bt % SD) * Cfg::SLOT;
+                at = slot + kScaleBatch * 128 + BN * j + half * CW;
+                f = slot[128 * j + (LANES_SCALED ? row : 0)];
+                if constexpr (!COLS_SCALED) f *= slot[kScaleBatch * 128 + BN * j + (half * CW) / 128];
             };
             auto add = [&](int c0, const uint32_t (&x)[CHUNK]) {
+                const float2 f2 = make_float2(fl, fl);
 #pragma unroll
                 for (int j = 0; j < CHUNK; j += 4) {
                     const float2 v0 = make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
@@ -580,48 +639,59 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
                 }
             };
             constexpr int NCH = CW / CHUNK;
-            if (w.kb0 < w.kb1) ok = begin(it, v[0]);
-            // Two K blocks per round where a block is one chunk, so that the
-            // register buffers' roles are known at compile time.
-            constexpr int ROUND = NCH == 1 ? 2 : 1;
-            static_assert(NCH == 1 || NCH % 2 == 0, "chunks alternate between two buffers");
-            int j = 0;                                    // K block of the batch
-            for (int kb = w.kb0; ok && kb < w.kb1;) {
+            // Block j of a batch, whose first chunk has been requested: adds it,
+            // and requests the first chunk of the block after it, if any.
+            auto block = [&](auto J, bool more) {
+                constexpr int j = decltype(J)::value;
+                constexpr bool turn = j + 1 == kScaleBatch;   // the next block is another batch's
+                const int b = (int)(it % NBUF);
+                const uint32_t next = it + 1;
+                uint32_t early = 0, early_scales = 0;
 #pragma unroll
-                for (int h = 0; h < ROUND; ++h) {
-                    if (!ok || kb >= w.kb1) break;
-                    const int b = (int)(it % NBUF);
-                    if (j == 0 && !ptx::wait_phase_warp(sfull_bar((int)(batch % SD)), (batch / SD) & 1)) {
-                        if (lane == 0) atomicOr(p.status, kStatusTimeout);
-                        ok = false;
-                        break;
+                for (int c = 0; c < NCH; ++c) {
+                    const int at = NCH == 1 ? j & 1 : c & 1;
+                    tmem_ld_wait_for<CHUNK>(v[at]);
+                    if (c + 1 < NCH) tmem_ld_chunk<CHUNK>(lanes + (uint32_t)(b * BN + (c + 1) * CHUNK), v[at ^ 1]);
+                    if (c == 0) {
+                        early = mbar_test(done_bar((int)(next % STAGES)), (next / STAGES) & 1);
+                        if (turn) early_scales = batch_test(batch + 1);
                     }
-                    scales_of(j);
-#pragma unroll
-                    for (int c = 0; c < NCH; ++c) {
-                        const int at = NCH == 1 ? h : c & 1;
-                        tmem_ld_wait_for<CHUNK>(v[at]);
-                        if (c + 1 < NCH) {
-                            tmem_ld_chunk<CHUNK>(lanes + (uint32_t)(b * BN + (c + 1) * CHUNK), v[at ^ 1]);
-                        } else {
-                            // The accumulator is read: the MMA warp may reuse it.
-                            ptx::tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) ptx::mbar_arrive(acce_bar(b));
-                            if (kb + 1 < w.kb1) ok = begin(it + 1, v[at ^ 1]);
+                    if (c + 1 == NCH) {
+                        // The accumulator is read: the MMA warp may reuse it.
+                        ptx::tc_fence_before();
+                        mbar_arrive_if(lane == 0, acce_bar(b));
+                        if (more) {
+                            if (turn) batch_wait(batch + 1, early_scales);
+                            scales_of(turn ? batch + 1 : batch, turn ? 0 : j + 1, fl_next, cols_next);
+                            begin(next, early, v[at ^ 1]);
                         }
-                        add(c * CHUNK, v[at]);
                     }
-                    ++it;
-                    ++kb;
-                    if (++j == kScaleBatch || kb == w.kb1) {
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(sempty_bar((int)(batch % SD)));
-                        ++batch;
-                        j = 0;
-                    }
+                    add(c * CHUNK, v[at]);
                 }
+                fl = fl_next;
+                cols = cols_next;
+                ++it;
+            };
+            static_assert((NCH == 1 || NCH % 2 == 0) && kScaleBatch == 2, "chunks alternate between two buffers");
+            using std::integral_constant;
+            if (w.kb0 < w.kb1) {
+                batch_wait(batch, batch_test(batch));
+                scales_of(batch, 0, fl, cols);
+                begin(it, 0, v[0]);
             }
+            for (int kb = w.kb0; ok && kb < w.kb1; kb += kScaleBatch) {
+                const int left = w.kb1 - kb;
+                if (left >= kScaleBatch) {
+                    block(integral_constant<int, 0>{}, true);
+                    block(integral_constant<int, 1>{}, left > kScaleBatch);
+                } else {
+                    block(integral_constant<int, 0>{}, false);
+                }
+                __syncwarp();
+                mbar_arrive_if(lane == 0, sempty_bar((int)(batch % SD)));
+                ++batch;
+            }
+            if (!ok && lane == 0) atomicOr(p.status, kStatusTimeout);
             if (!ok && split == 1) break;
             const int64_t c_base = p.mode == kFp8GroupK ? w.group * p.stride_c : 0;
             if constexpr (SWAP) {
