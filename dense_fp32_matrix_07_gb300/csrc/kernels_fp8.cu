@@ -52,6 +52,7 @@ namespace sgemm_gb300 {
 namespace {
 
 constexpr int kScaleBatch = 2;   // K blocks whose scales are handed over together
+constexpr int kStaging = 4096;   // bytes an epilogue warp turns its tile through: 128 of each of 32 rows
 
 template <int BN_, bool SWAP_>
 struct Fp8Cfg {
@@ -61,20 +62,21 @@ struct Fp8Cfg {
     static constexpr int P_TILE = 128 * ROW_BYTES;           // lanes' operand
     static constexpr int Q_TILE = BN * ROW_BYTES;            // columns' operand
     static constexpr int STAGE_BYTES = P_TILE + Q_TILE;
-    static constexpr int STAGES = BN == 256 ? 4 : BN == 128 ? 6 : 7;
+    static constexpr int STAGES = BN == 256 ? 3 : BN == 128 ? 5 : 7;
     static constexpr int NBUF = BN == 256 ? 2 : 4;           // accumulators in tensor memory
     static constexpr int TMEM_COLS = NBUF * BN < 32 ? 32 : NBUF * BN;
     static constexpr int EPI_WARPS = BN >= 128 ? 8 : 4;
     static constexpr int CW = BN / (EPI_WARPS / 4);          // columns per epilogue warp
-    static constexpr int CHUNK = CW < 32 || BN == 256 ? 16 : 32;          // columns per tcgen05.ld
+    static constexpr int CHUNK = CW < 32 || BN == 256 ? 16 : 32;   // columns per tcgen05.ld
     static constexpr int THREADS = 128 + 32 * EPI_WARPS;
-    // Registers move from the first four warps to the eight that hold 128
-    // sums per thread: 168 * 384 at launch, 56 * 128 + 224 * 256 after.
-    static constexpr int EPI_REGS = BN == 256 ? 224 : BN == 128 ? 200 : 0;
+    // Registers move from the first four warps to the eight that hold up to
+    // 128 sums per thread: 168 * 384 at launch, 72 * 128 + 216 * 256 (or
+    // 104 * 128 + 200 * 256) after.
+    static constexpr int EPI_REGS = BN == 256 ? 216 : BN == 128 ? 200 : 0;
     static constexpr int SDEPTH = BN == 256 ? 4 : 6;         // ring of scales
     static constexpr int SLOT = kScaleBatch * (128 + BN);    // floats of one slot
     static constexpr bool CAN_SPLIT = SWAP && BN <= 64;
-    static constexpr int STAGING = SWAP ? 0 : EPI_WARPS * 2048;
+    static constexpr int STAGING = SWAP ? 0 : EPI_WARPS * kStaging;
     static constexpr int PARTIAL = CAN_SPLIT ? BN * 128 * 4 : 0;
     static constexpr int NUM_BARS = 2 * STAGES + NBUF + 2 * SDEPTH + 1;
     static constexpr int OFF_STAGING = STAGES * STAGE_BYTES;
@@ -88,6 +90,25 @@ struct Fp8Cfg {
     static_assert(OFF_BARS % 8 == 0, "barrier alignment");
 };
 
+// Division by a number the host knows: n / d for n < 2^31.
+struct FastDiv {
+    uint32_t d, mul, shift;   // n / d = (umulhi(n, mul) + n) >> shift, in 33 bits
+};
+
+FastDiv fast_div(uint32_t d)
+{
+    FastDiv f{d, 0, 0};
+    while ((uint64_t(1) << f.shift) < d) ++f.shift;
+    f.mul = (uint32_t)(((uint64_t(1) << 32) * ((uint64_t(1) << f.shift) - d)) / d + 1);
+    return f;
+}
+
+__device__ __forceinline__ uint32_t div(uint32_t n, const FastDiv &f)
+{
+    // umulhi(n, mul) <= n < 2^31: the sum fits 32 bits.
+    return (__umulhi(n, f.mul) + n) >> f.shift;
+}
+
 struct Fp8Params {
     int mode;
     int M, N;                    // rows of A, rows of B
@@ -98,6 +119,7 @@ struct Fp8Params {
     const int32_t *offsets;
     int token_tiles;             // dense and grouped-K products; grouped rows: from the table
     int weight_tiles;
+    FastDiv by_weights, by_group;   // weight_tiles; tiles of one group (grouped-K products)
     int split;
     float beta;
     void *C;
@@ -147,24 +169,31 @@ __device__ __forceinline__ Fp8Item fp8_item(const Fp8Params &p, const int *table
     int tokens = p.token_tiles;
     if (p.mode == kFp8GroupRows) tokens = table[p.groups];
     if (p.mode == kFp8GroupK) {
-        const uint32_t per = (uint32_t)p.token_tiles * p.weight_tiles;
-        it.group = (int)(t / per);
-        t -= it.group * per;
+        it.group = (int)div(t, p.by_group);
+        t -= it.group * p.by_group.d;
     }
-    const uint32_t band = (uint32_t)kRaster * p.weight_tiles;
-    const uint32_t first = t / band * kRaster;
-    const uint32_t high = tokens - first < kRaster ? tokens - first : kRaster;
-    const uint32_t r = t % band;
-    const int tt = (int)(first + r % high);
-    it.b_row = (int)(r / high) * WT;
+    // Bands of kRaster token tiles, the token tile fastest.
+    static_assert((kRaster & (kRaster - 1)) == 0, "a power of two");
+    const uint32_t band = div(t / kRaster, p.by_weights), first = band * kRaster;
+    const uint32_t r = t - first * p.weight_tiles;
+    const uint32_t high = tokens - first;
+    uint32_t wt, tt;
+    if (high >= kRaster) {
+        wt = r / kRaster;
+        tt = first + r % kRaster;
+    } else {
+        wt = r / high;
+        tt = first + r - wt * high;
+    }
+    it.b_row = (int)wt * WT;
     if (p.mode == kFp8GroupRows) {
-        it.group = find_group(table, p.groups, tt);
+        it.group = find_group(table, p.groups, (int)tt);
         int lo, hi;
         group_range(p.offsets, it.group, p.M, lo, hi);
-        it.a_row = lo + (tt - table[it.group]) * TT;
+        it.a_row = lo + ((int)tt - table[it.group]) * TT;
         it.a_end = hi;
     } else {
-        it.a_row = tt * TT;
+        it.a_row = (int)tt * TT;
         it.a_end = p.M;
     }
     int k0 = 0, k1 = p.nk;
@@ -172,8 +201,14 @@ __device__ __forceinline__ Fp8Item fp8_item(const Fp8Params &p, const int *table
         k0 = table[it.group];
         k1 = table[it.group + 1];
     }
-    it.kb0 = k0 + (int)((int64_t)(k1 - k0) * rank / p.split);
-    it.kb1 = k0 + (int)((int64_t)(k1 - k0) * (rank + 1) / p.split);
+    it.kb0 = k0;
+    it.kb1 = k1;
+    if constexpr (Cfg::CAN_SPLIT) {
+        if (p.split > 1) {
+            it.kb0 = k0 + (int)((int64_t)(k1 - k0) * rank / p.split);
+            it.kb1 = k0 + (int)((int64_t)(k1 - k0) * (rank + 1) / p.split);
+        }
+    }
     return it;
 }
 
@@ -424,7 +459,7 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
     if (warp == 1) ptx::tmem_alloc(tmem_slot, Cfg::TMEM_COLS);
     if (p.mode != kFp8Dense) {
         // table[g] = tiles (or K blocks) of the groups before g.
-        const int unit = p.mode == kFp8GroupK ? kBlock : (SWAP ? BN : 128);
+        const int unit = p.mode == kFp8GroupK ? kBlock : SWAP ? BN : 128;
         const int rows = p.mode == kFp8GroupK ? INT32_MAX : p.M;
         for (int g = threadIdx.x; g < p.groups; g += Cfg::THREADS) {
             int lo, hi;
@@ -465,7 +500,7 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
     if (split > 1 && tiles > t_step) tiles = t_step;   // a split grid has one tile per cluster
 
     if constexpr (Cfg::EPI_REGS > 0) {
-        if (warp < 4) ptx::setmaxnreg_dec<BN == 256 ? 56 : 104>();
+        if (warp < 4) ptx::setmaxnreg_dec<BN == 256 ? 72 : 104>();
     }
     if (warp == 0) {
         // ------------------------------ TMA producer ------------------------------
@@ -711,37 +746,43 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
                         st_shared_f32(part + 4 * ((half * CW + j) * 128 + row), (j & 1) ? acc[j / 2].y : acc[j / 2].x);
                 }
             } else {
-                // Lane = row of A; 64 bytes of each of 32 rows at a time go
+                // Lane = row of A; 128 bytes of each of 32 rows at a time go
                 // through shared memory, so that a warp's stores cover whole
-                // 64-byte pieces of 8 rows instead of 16 bytes of 32.
-                const uint32_t st = base + Cfg::OFF_STAGING + ew * 2048;
+                // 128-byte pieces of 4 rows instead of 16 bytes of 32.
+                const uint32_t st = base + Cfg::OFF_STAGING + ew * kStaging;
                 const int row0 = w.a_row + 32 * q;
-                // Writes `cols` columns from col0 on: 16 floats, or 32 bfloat16.
-                auto flush = [&](const uint32_t (&u)[16], int cols, int col0) {
+                // Writes 128 bytes of columns from col0 on: 32 floats, or 64 bfloat16.
+                auto flush = [&](const uint32_t (&u)[32], int cols, int col0) {
+                    const int size = 128 / cols;
                     __syncwarp();
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        st_shared_u32x4(st + 64 * lane + 16 * (c ^ ((lane >> 1) & 3)),
+                    for (int c = 0; c < 8; ++c)
+                        st_shared_u32x4(st + 128 * lane + 16 * (c ^ (lane & 7)),
                                         make_uint4(u[4 * c], u[4 * c + 1], u[4 * c + 2], u[4 * c + 3]));
                     __syncwarp();
                     if (p.vec_c && p.beta == 0.0f && col0 + cols <= p.N) {
+                        uint4 x[8];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int r = 8 * i + (lane >> 2), c = lane & 3;
-                            const uint4 x = ld_shared_u32x4(st + 64 * r + 16 * (c ^ ((r >> 1) & 3)));
-                            if (row0 + r < w.a_end) {
-                                const int64_t at = c_base + (int64_t)(row0 + r) * p.ldc + col0;
-                                *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.C) + at * (64 / cols) + 16 * c) = x;
-                            }
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = 4 * i + (lane >> 3), c = lane & 7;
+                            x[i] = ld_shared_u32x4(st + 128 * r + 16 * (c ^ (r & 7)));
+                        }
+                        uint8_t *dst = static_cast<uint8_t *>(p.C) +
+                                       (c_base + (int64_t)(row0 + (lane >> 3)) * p.ldc + col0) * size + 16 * (lane & 7);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            if (row0 + 4 * i + (lane >> 3) < w.a_end) *reinterpret_cast<uint4 *>(dst) = x[i];
+                            dst += 4 * p.ldc * size;
                         }
                         return;
                     }
+#pragma unroll 8
                     for (int i = 0; i < cols; ++i) {
-                        const int e = 32 * i + lane, r = e / cols, c = e % cols, byte = c * (64 / cols);
-                        const uint32_t a = st + 64 * r + 16 * ((byte >> 4) ^ ((r >> 1) & 3)) + (byte & 15);
+                        const int e = 32 * i + lane, r = e / cols, c = e % cols, byte = c * size;
+                        const uint32_t a = st + 128 * r + 16 * ((byte >> 4) ^ (r & 7)) + (byte & 15);
                         if (row0 + r < w.a_end && col0 + c < p.N) {
                             const int64_t at = c_base + (int64_t)(row0 + r) * p.ldc + col0 + c;
-                            if (cols == 32) {
+                            if (cols == 64) {
                                 uint16_t x;
                                 asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(a) : "memory");
                                 static_cast<uint16_t *>(p.C)[at] = x;
@@ -752,21 +793,21 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
                     }
                 };
                 const int col_base = w.b_row + half * CW;
-                uint32_t u[16];
+                uint32_t u[32];
                 if (p.c_bf16 && p.beta == 0.0f) {
 #pragma unroll
-                    for (int h = 0; h < CW; h += 32) {
+                    for (int h = 0; h < CW; h += 64) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) u[j] = pack_bf16(acc[h / 2 + j].x, acc[h / 2 + j].y);
-                        flush(u, 32, col_base + h);
+                        for (int j = 0; j < 32; ++j) u[j] = pack_bf16(acc[h / 2 + j].x, acc[h / 2 + j].y);
+                        flush(u, 64, col_base + h);
                     }
                 } else {
 #pragma unroll
-                    for (int h = 0; h < CW; h += 16) {
+                    for (int h = 0; h < CW; h += 32) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
+                        for (int j = 0; j < 32; ++j)
                             u[j] = __float_as_uint((j & 1) ? acc[h / 2 + j / 2].y : acc[h / 2 + j / 2].x);
-                        flush(u, 16, col_base + h);
+                        flush(u, 32, col_base + h);
                     }
                 }
             }
@@ -885,6 +926,8 @@ cudaError_t launch_cfg(const Fp8Args &g, const Fp8Plan &plan, cudaStream_t strea
     const int64_t tokens = g.mode == kFp8Dense ? p.token_tiles
                            : g.mode == kFp8GroupRows ? g.M / tt + groups_hit : (int64_t)p.token_tiles * g.groups;
     if (tokens + 2 * kRaster > INT32_MAX / p.weight_tiles - 2 * kRaster) return cudaErrorInvalidValue;
+    p.by_weights = fast_div((uint32_t)p.weight_tiles);
+    p.by_group = fast_div((uint32_t)((int64_t)p.token_tiles * p.weight_tiles));
     p.split = plan.split;
     p.beta = g.beta;
     p.C = g.C;

@@ -106,7 +106,7 @@ def check_product(C, want, S, nk, bf16, old=None):
 # M, N, K around every tile edge (16, 32, 64, 128 columns, 128 and 256 rows), K tails, split K, several waves.
 SHAPES = [(1, 1, 1), (1, 129, 16), (3, 257, 127), (16, 128, 129), (17, 4096, 1024), (33, 640, 513), (64, 1024, 2048),
           (65, 384, 256), (127, 130, 385), (128, 256, 128), (129, 255, 300), (300, 511, 1000), (1000, 777, 640),
-          (2500, 1200, 272), (8, 7000, 4096)]
+          (2500, 1200, 272), (8, 7000, 4096), (3000, 1700, 400), (5121, 1025, 1296)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
@@ -142,7 +142,7 @@ def test_product(cuda_device, shape, form, ctype):
         assert C.outside_untouched()
 
 
-@pytest.mark.parametrize("M", [1, 20, 40, 100, 130, 1100])
+@pytest.mark.parametrize("M", [1, 20, 40, 100, 130, 1100, 5100])
 @pytest.mark.parametrize("form", [sg.SGEMM_SCALE_BLOCKS, sg.SGEMM_SCALE_ROWS], ids=["blocks", "rows"])
 def test_integer_products_are_exact(cuda_device, M, form):
     N, K = 777, 1300
@@ -211,12 +211,13 @@ COUNTS = {
     "ragged": [127, 129, 0, 300, 1, 128],
     "none": [0, 0, 0],
     "many": [3, 0, 1, 2] * 100,
+    "prompts": [700, 0, 257, 1300, 256, 3],
 }
 
 
 @pytest.mark.parametrize("name", list(COUNTS))
 @pytest.mark.parametrize("ctype", [sg.SGEMM_F32, sg.SGEMM_BF16], ids=["f32", "bf16"])
-@pytest.mark.parametrize("NK", [(200, 144), (512, 700)], ids=["200x144", "512x700"])
+@pytest.mark.parametrize("NK", [(200, 144), (512, 700), (2200, 272)], ids=["200x144", "512x700", "2200x272"])
 def test_grouped(cuda_device, name, ctype, NK):
     (N, K), counts = NK, COUNTS[name]
     E, R = len(counts), sum(counts) + 5               # five rows that no group has
@@ -245,8 +246,8 @@ def test_grouped(cuda_device, name, ctype, NK):
     assert C.outside_untouched()
 
 
-@pytest.mark.parametrize("name", ["decode", "ragged", "one_heavy", "none"])
-@pytest.mark.parametrize("MN", [(130, 100), (384, 512)], ids=["130x100", "384x512"])
+@pytest.mark.parametrize("name", ["decode", "ragged", "one_heavy", "none", "prompts"])
+@pytest.mark.parametrize("MN", [(130, 100), (384, 512), (1000, 1100)], ids=["130x100", "384x512", "1000x1100"])
 def test_grouped_k(cuda_device, name, MN):
     """The weight gradients, from the tokens on: the quantiser's layout and the product together."""
     (M, N), counts = MN, COUNTS[name]
