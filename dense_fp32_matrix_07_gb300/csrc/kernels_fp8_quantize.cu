@@ -40,43 +40,118 @@ __device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d
     return lo | (hi << 16);
 }
 
-// N consecutive values from p (N * sizeof(T) a multiple of 16, p 16-byte aligned).
-template <int N>
-__device__ __forceinline__ void load_vec(const float *p, float (&v)[N])
-{
-#pragma unroll
-    for (int j = 0; j < N; j += 4) {
-        const float4 x = *reinterpret_cast<const float4 *>(p + j);
-        v[j] = x.x, v[j + 1] = x.y, v[j + 2] = x.z, v[j + 3] = x.w;
-    }
-}
+// Eight consecutive values of a row as they are stored: pairs of bfloat16 in
+// four registers, or eight floats.
+template <class T>
+struct Eight;
 
-template <int N>
-__device__ __forceinline__ void load_vec(const __nv_bfloat16 *p, float (&v)[N])
-{
-    static_assert(N % 8 == 0, "16-byte pieces");
+template <>
+struct Eight<float> {
+    float v[8];
+    __device__ __forceinline__ void zero()
+    {
 #pragma unroll
-    for (int j = 0; j < N; j += 8) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(p + j);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[j + 2 * i] = __uint_as_float(w[i] << 16);
-            v[j + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
     }
-}
+    __device__ __forceinline__ void load(const float *p)
+    {
+        const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+    __device__ __forceinline__ void set(int j, const float *p) { v[j] = *p; }
+    __device__ __forceinline__ float2 pair(int j) const { return make_float2(v[2 * j], v[2 * j + 1]); }
+    // Magnitude bits of pair j, as one or two numbers packed for max_of().
+    __device__ __forceinline__ uint2 mags(int j) const { return make_uint2(magnitude(v[2 * j]), magnitude(v[2 * j + 1])); }
+    static __device__ __forceinline__ uint2 max_of(uint2 a, uint2 b) { return make_uint2(umax(a.x, b.x), umax(a.y, b.y)); }
+    static __device__ __forceinline__ uint2 none() { return make_uint2(0, 0); }
+    static __device__ __forceinline__ uint32_t first(uint2 m) { return m.x; }
+    static __device__ __forceinline__ uint32_t second(uint2 m) { return m.y; }
+    using Mags = uint2;
+};
 
-// Values c .. c + N - 1 of a row of `cols`, zeros past its end.
-template <int N, class T>
-__device__ __forceinline__ void load_row(const T *row, int64_t c, int64_t cols, bool vec, float (&v)[N])
+template <>
+struct Eight<__nv_bfloat16> {
+    uint32_t v[4];
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = 0;
+    }
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p)
+    {
+        const uint4 a = *reinterpret_cast<const uint4 *>(p);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    }
+    __device__ __forceinline__ void set(int j, const __nv_bfloat16 *p)
+    {
+        const uint32_t x = *reinterpret_cast<const uint16_t *>(p);
+        v[j / 2] |= (j & 1) ? x << 16 : x;
+    }
+    __device__ __forceinline__ float2 pair(int j) const
+    {
+        return make_float2(__uint_as_float(v[j] << 16), __uint_as_float(v[j] & 0xffff0000u));
+    }
+    __device__ __forceinline__ uint32_t mags(int j) const { return v[j] & 0x7fff7fffu; }
+    static __device__ __forceinline__ uint32_t max_of(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+    static __device__ __forceinline__ uint32_t none() { return 0; }
+    static __device__ __forceinline__ uint32_t first(uint32_t m) { return m << 16; }
+    static __device__ __forceinline__ uint32_t second(uint32_t m) { return m & 0xffff0000u; }
+    using Mags = uint32_t;
+};
+
+// Values c .. c + 7 of a row of `cols`, zeros past its end.
+template <class T>
+__device__ __forceinline__ void load_row(const T *row, int64_t c, int64_t cols, bool vec, Eight<T> &x)
 {
-    if (vec && c + N <= cols) {
-        load_vec<N>(row + c, v);
+    if (vec && c + 8 <= cols) {
+        x.load(row + c);
         return;
     }
+    x.zero();
 #pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = c + j < cols ? load_as_float(row + c + j) : 0.0f;
+    for (int j = 0; j < 8; ++j)
+        if (c + j < cols) x.set(j, row + c + j);
+}
+
+// Largest magnitude of the eight.
+template <class T>
+__device__ __forceinline__ uint32_t max_of_eight(const Eight<T> &x)
+{
+    auto m = Eight<T>::max_of(Eight<T>::max_of(x.mags(0), x.mags(1)), Eight<T>::max_of(x.mags(2), x.mags(3)));
+    return umax(Eight<T>::first(m), Eight<T>::second(m));
+}
+
+// The eight times inv, as eight bytes.
+template <class T>
+__device__ __forceinline__ uint2 eight_bytes(const Eight<T> &x, float inv)
+{
+    const float2 f = make_float2(inv, inv);
+    const float2 a = __fmul2_rn(x.pair(0), f), b = __fmul2_rn(x.pair(1), f), c = __fmul2_rn(x.pair(2), f),
+                 d = __fmul2_rn(x.pair(3), f);
+    return make_uint2(to_e4m3x4(a.x, a.y, b.x, b.y), to_e4m3x4(c.x, c.y, d.x, d.y));
+}
+
+// Maxima over the 16 lanes of a half warp of N values each (N = 8 or 4), one
+// of them per lane in the end: halves of the values are traded with the lanes
+// 8, 4, ... away, so that this takes N shuffles instead of 4 N, and the two
+// divisions of a scale are done once per value instead of by all 16 lanes.
+// Lane l of the half holds value l / (16 / N).
+template <int N>
+__device__ __forceinline__ uint32_t max_over_half(uint32_t (&m)[N], int lane)
+{
+    int d = 8;
+#pragma unroll
+    for (int n = N; n > 1; n /= 2, d /= 2) {
+        const bool upper = (lane & d) != 0;
+#pragma unroll
+        for (int i = 0; i < n / 2; ++i) {
+            const uint32_t keep = upper ? m[i + n / 2] : m[i], give = upper ? m[i] : m[i + n / 2];
+            m[i] = umax(keep, __shfl_xor_sync(0xffffffffu, give, d));
+        }
+    }
+#pragma unroll
+    for (; d > 0; d /= 2) m[0] = umax(m[0], __shfl_xor_sync(0xffffffffu, m[0], d));
+    return m[0];
 }
 
 // ---------------------------------------------------------------------------
@@ -98,36 +173,27 @@ quantize_rows_kernel(int64_t rows, int64_t cols, const T *__restrict__ src, int6
     const int64_t b0 = (int64_t)blockIdx.y * kBlocksPerCta;
     const int64_t r0 = (int64_t)blockIdx.x * kRowsPerCta;
     // Warp w: rows 2w and 2w + 1, each half of the warp blocks half and half + 2.
-    float v[4][8];
+    Eight<T> v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int64_t r = r0 + 2 * warp + (i >> 1), b = b0 + half + 2 * (i & 1);
         int64_t from = -1;
         if (r < rows) from = gather ? (int64_t)gather[r] : r;
-        if (from >= 0 && from < src_rows && b < nb) {
-            load_row<8>(src + from * ld, b * kBlock + 8 * l, cols, vec != 0, v[i]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
-        }
+        if (from >= 0 && from < src_rows && b < nb)
+            load_row<T>(src + from * ld, b * kBlock + 8 * l, cols, vec != 0, v[i]);
+        else
+            v[i].zero();
     }
+    uint32_t m[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i] = max_of_eight(v[i]);
+    const Scale s = scale_of(max_over_half<4>(m, lane));       // of block l / 4
+    if ((l & 3) == 0) tile[half + 2 * ((l >> 2) & 1)][2 * warp + (l >> 3)] = s.scale;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int64_t r = r0 + 2 * warp + (i >> 1), b = b0 + half + 2 * (i & 1);
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = umax(m, magnitude(v[i][j]));
-#pragma unroll
-        for (int d = 8; d; d /= 2) m = umax(m, __shfl_xor_sync(0xffffffffu, m, d));
-        const Scale s = scale_of(m);
-        const int64_t c = b * kBlock + 8 * l;
-        if (r < rows && c < cols) {
-            uint2 o;
-            o.x = to_e4m3x4(v[i][0] * s.inv, v[i][1] * s.inv, v[i][2] * s.inv, v[i][3] * s.inv);
-            o.y = to_e4m3x4(v[i][4] * s.inv, v[i][5] * s.inv, v[i][6] * s.inv, v[i][7] * s.inv);
-            *reinterpret_cast<uint2 *>(q + r * ldq + c) = o;
-        }
-        if (l == 0) tile[half + 2 * (i & 1)][2 * warp + (i >> 1)] = s.scale;
+        const int64_t r = r0 + 2 * warp + (i >> 1), c = (b0 + half + 2 * (i & 1)) * kBlock + 8 * l;
+        const float inv = __shfl_sync(0xffffffffu, s.inv, (lane & 16) | (4 * i));
+        if (r < rows && c < cols) *reinterpret_cast<uint2 *>(q + r * ldq + c) = eight_bytes(v[i], inv);
     }
     __syncthreads();
     if (threadIdx.x < kBlocksPerCta * kRowsPerCta) {
@@ -142,7 +208,7 @@ quantize_rows_kernel(int64_t rows, int64_t cols, const T *__restrict__ src, int6
 // row form (8 bytes of each of its rows), the column form and the block form.
 // Transposed output goes through shared memory: column c's 128 bytes are one
 // row there, its 8-byte pieces permuted by XOR with c / 8 against bank
-// conflicts.
+// conflicts. Each scale's divisions are done by one thread.
 struct TileArgs {
     int64_t rows, cols;
     const void *src;
@@ -164,20 +230,25 @@ struct TileArgs {
 };
 
 template <class T, bool BLOCKS>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2)
 quantize_tiles_kernel(const TileArgs a)
 {
     __shared__ uint32_t red[8][128];
+    __shared__ float4 inv_of[32];                     // 448 / a of the 128 columns
     __shared__ uint4 turned[128 * 8];
-    __shared__ int table[kMaxGroups + 2];
+    __shared__ int table[BLOCKS ? 1 : kMaxGroups + 2], begins[BLOCKS ? 1 : kMaxGroups], ends[BLOCKS ? 1 : kMaxGroups];
     const int x = threadIdx.x & 15, y = threadIdx.x >> 4, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (!BLOCKS && a.groups > 0) {
-        // table[g] = blocks of the groups before g.
+        // table[g] = blocks of the groups before g; group g's rows are
+        // [begins[g], ends[g]), held to the rows there are.
+        const int rows = (int)a.rows;
         for (int g = threadIdx.x; g < a.groups; g += 256) {
-            int64_t lo = a.offsets[g], hi = a.offsets[g + 1];
-            lo = lo < 0 ? 0 : lo > a.rows ? a.rows : lo;
-            hi = hi < lo ? lo : hi > a.rows ? a.rows : hi;
-            table[g] = (int)((hi - lo + kBlock - 1) / kBlock);
+            const int o0 = a.offsets[g], o1 = a.offsets[g + 1];
+            const int lo = o0 < 0 ? 0 : o0 > rows ? rows : o0;
+            const int hi = o1 < lo ? lo : o1 > rows ? rows : o1;
+            begins[g] = lo;
+            ends[g] = hi;
+            table[g] = (hi - lo + kBlock - 1) / kBlock;
         }
         __syncthreads();
         if (warp == 0) {
@@ -199,9 +270,11 @@ quantize_tiles_kernel(const TileArgs a)
         }
         __syncthreads();
     }
-    const int64_t per = a.row_blocks * a.col_blocks;
-    for (int64_t t = blockIdx.x; t < per * a.batch; t += gridDim.x) {
-        const int64_t e = t / per, rb = (t % per) / a.col_blocks, cb = (t % per) % a.col_blocks;
+    const uint32_t col_blocks = (uint32_t)a.col_blocks, per = (uint32_t)a.row_blocks * col_blocks;
+    const uint32_t tiles = per * (uint32_t)a.batch;
+    for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const uint32_t in = BLOCKS ? t % per : t, row_block = in / col_blocks;
+        const int64_t e = BLOCKS ? t / per : 0, rb = row_block, cb = in - row_block * col_blocks;
         // Rows [r0, r1) of this tile.
         int64_t r0 = rb * kBlock, r1 = r0 + kBlock < a.rows ? r0 + kBlock : a.rows;
         if (!BLOCKS && a.groups > 0) {
@@ -216,60 +289,48 @@ quantize_tiles_kernel(const TileArgs a)
                     else
                         hi = mid - 1;
                 }
-                int64_t g0 = a.offsets[lo], g1 = a.offsets[lo + 1];
-                g0 = g0 < 0 ? 0 : g0 > a.rows ? a.rows : g0;
-                g1 = g1 < g0 ? g0 : g1 > a.rows ? a.rows : g1;
-                r0 = g0 + (rb - table[lo]) * kBlock;
-                r1 = r0 + kBlock < g1 ? r0 + kBlock : g1;
+                r0 = begins[lo] + (rb - table[lo]) * kBlock;
+                r1 = r0 + kBlock < ends[lo] ? r0 + kBlock : ends[lo];
             }
         }
         const T *src = static_cast<const T *>(a.src) + e * a.stride_src;
         const int64_t c = cb * kBlock + 8 * x;
-        float v[8][8];
+        Eight<T> v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int64_t r = r0 + 8 * y + i;
             int64_t from = -1;
             if (r < r1) from = a.gather ? (int64_t)a.gather[r] : r;
-            if (from >= 0 && from < a.src_rows) {
-                load_row<8>(src + from * a.ld, c, a.cols, a.vec != 0, v[i]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
-            }
+            if (from >= 0 && from < a.src_rows)
+                load_row<T>(src + from * a.ld, c, a.cols, a.vec != 0, v[i]);
+            else
+                v[i].zero();
         }
         if (!BLOCKS && a.q) {
             // Row form: a row's 128 columns are the 16 lanes of a half warp.
+            uint32_t m[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m[i] = max_of_eight(v[i]);
+            const Scale s = scale_of(max_over_half<8>(m, lane));   // of row x / 2
+            if ((x & 1) == 0 && r0 + 8 * y + (x >> 1) < r1) a.scales[cb * a.lds + r0 + 8 * y + (x >> 1)] = s.scale;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                uint32_t m = 0;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) m = umax(m, magnitude(v[i][j]));
-#pragma unroll
-                for (int d = 8; d; d /= 2) m = umax(m, __shfl_xor_sync(0xffffffffu, m, d));
-                const Scale s = scale_of(m);
                 const int64_t r = r0 + 8 * y + i;
-                if (r < r1) {
-                    if (c < a.cols) {
-                        uint2 o;
-                        o.x = to_e4m3x4(v[i][0] * s.inv, v[i][1] * s.inv, v[i][2] * s.inv, v[i][3] * s.inv);
-                        o.y = to_e4m3x4(v[i][4] * s.inv, v[i][5] * s.inv, v[i][6] * s.inv, v[i][7] * s.inv);
-                        *reinterpret_cast<uint2 *>(a.q + r * a.ldq + c) = o;
-                    }
-                    if (x == 0) a.scales[cb * a.lds + r] = s.scale;
-                }
+                const float inv = __shfl_sync(0xffffffffu, s.inv, (lane & 16) | (2 * i));
+                if (r < r1 && c < a.cols) *reinterpret_cast<uint2 *>(a.q + r * a.ldq + c) = eight_bytes(v[i], inv);
             }
         }
         // Columns' (or the block's) largest magnitudes.
         uint32_t m[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            m[j] = 0;
+        for (int j = 0; j < 4; ++j) {
+            typename Eight<T>::Mags p = Eight<T>::none();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m[j] = umax(m[j], magnitude(v[i][j]));
-            m[j] = umax(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
+            for (int i = 0; i < 8; ++i) p = Eight<T>::max_of(p, v[i].mags(j));
+            m[2 * j] = Eight<T>::first(p);
+            m[2 * j + 1] = Eight<T>::second(p);
         }
-        Scale s[8];
+        float inv[8];
         if (BLOCKS) {
             uint32_t all = 0;
 #pragma unroll
@@ -280,55 +341,59 @@ quantize_tiles_kernel(const TileArgs a)
             __syncthreads();
 #pragma unroll
             for (int w = 0; w < 8; ++w) all = umax(all, red[w][0]);
-            s[0] = scale_of(all);
+            const Scale s = scale_of(all);
 #pragma unroll
-            for (int j = 1; j < 8; ++j) s[j] = s[0];
+            for (int j = 0; j < 8; ++j) inv[j] = s.inv;
             if (threadIdx.x == 0) {
                 if (a.q)
-                    a.scales[e * a.stride_s + rb * a.lds + cb] = s[0].scale;
+                    a.scales[e * a.stride_s + rb * a.lds + cb] = s.scale;
                 else
-                    a.scales_t[e * a.stride_st + cb * a.ldst + rb] = s[0].scale;
+                    a.scales_t[e * a.stride_st + cb * a.ldst + rb] = s.scale;
             }
             if (a.q) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int64_t r = r0 + 8 * y + i;
-                    if (r < r1 && c < a.cols) {
-                        uint2 o;
-                        o.x = to_e4m3x4(v[i][0] * s[0].inv, v[i][1] * s[0].inv, v[i][2] * s[0].inv, v[i][3] * s[0].inv);
-                        o.y = to_e4m3x4(v[i][4] * s[0].inv, v[i][5] * s[0].inv, v[i][6] * s[0].inv, v[i][7] * s[0].inv);
-                        *reinterpret_cast<uint2 *>(a.q + e * a.stride_q + r * a.ldq + c) = o;
-                    }
+                    if (r < r1 && c < a.cols)
+                        *reinterpret_cast<uint2 *>(a.q + e * a.stride_q + r * a.ldq + c) = eight_bytes(v[i], s.inv);
                 }
                 continue;
             }
         } else {
-            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) m[j] = umax(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
+            // The last tile's reads of `red` and `turned` are behind the barriers that ended it.
             if (lane < 16) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) red[warp][8 * x + j] = m[j];
+                *reinterpret_cast<uint4 *>(&red[warp][8 * x]) = make_uint4(m[0], m[1], m[2], m[3]);
+                *reinterpret_cast<uint4 *>(&red[warp][8 * x + 4]) = make_uint4(m[4], m[5], m[6], m[7]);
             }
             __syncthreads();
+            if (threadIdx.x < 128) {
+                uint32_t all = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-#pragma unroll
-                for (int w = 0; w < 8; ++w) m[j] = umax(m[j], red[w][8 * x + j]);
-                s[j] = scale_of(m[j]);
+                for (int w = 0; w < 8; ++w) all = umax(all, red[w][threadIdx.x]);
+                const Scale s = scale_of(all);
+                reinterpret_cast<float *>(inv_of)[threadIdx.x] = s.inv;
+                const int64_t col = cb * kBlock + threadIdx.x;
+                if (col < a.cols) a.scales_t[rb * a.ldst + col] = s.scale;
             }
-            if (y == 0) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (c + j < a.cols) a.scales_t[rb * a.ldst + c + j] = s[j].scale;
-            }
+            __syncthreads();
+            const float4 lo = inv_of[2 * x], hi = inv_of[2 * x + 1];
+            inv[0] = lo.x, inv[1] = lo.y, inv[2] = lo.z, inv[3] = lo.w;
+            inv[4] = hi.x, inv[5] = hi.y, inv[6] = hi.z, inv[7] = hi.w;
         }
         // Turn the tile: 8 bytes of each of this thread's columns.
         uint2 *const pieces = reinterpret_cast<uint2 *>(turned);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            uint2 o;
-            o.x = to_e4m3x4(v[0][j] * s[j].inv, v[1][j] * s[j].inv, v[2][j] * s[j].inv, v[3][j] * s[j].inv);
-            o.y = to_e4m3x4(v[4][j] * s[j].inv, v[5][j] * s[j].inv, v[6][j] * s[j].inv, v[7][j] * s[j].inv);
-            pieces[(8 * x + j) * 16 + (y ^ x)] = o;
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = make_float2(inv[2 * j], inv[2 * j + 1]);
+            float2 p[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[i] = __fmul2_rn(v[i].pair(j), f);
+            pieces[(8 * x + 2 * j) * 16 + (y ^ x)] =
+                make_uint2(to_e4m3x4(p[0].x, p[1].x, p[2].x, p[3].x), to_e4m3x4(p[4].x, p[5].x, p[6].x, p[7].x));
+            pieces[(8 * x + 2 * j + 1) * 16 + (y ^ x)] =
+                make_uint2(to_e4m3x4(p[0].y, p[1].y, p[2].y, p[3].y), to_e4m3x4(p[4].y, p[5].y, p[6].y, p[7].y));
         }
         __syncthreads();
         const int64_t end = BLOCKS ? a.rows : a.row_blocks * kBlock;   // length of a transposed row
@@ -358,7 +423,9 @@ template <class T, bool BLOCKS>
 cudaError_t launch_tiles(TileArgs &a, int num_sms, cudaStream_t stream)
 {
     a.vec = vec_ok(static_cast<const T *>(a.src), a.ld, a.batch > 1 ? a.stride_src : 0);
-    const int64_t tiles = a.row_blocks * a.col_blocks * a.batch, most = (int64_t)num_sms * 2;
+    // Tiles are counted in 32 bits (2^31 of them would be 2^45 values).
+    if ((__int128)a.row_blocks * a.col_blocks * a.batch > INT32_MAX) return cudaErrorInvalidValue;
+    const int64_t tiles = a.row_blocks * a.col_blocks * a.batch, most = (int64_t)num_sms * (sizeof(T) == 2 ? 3 : 2);
     quantize_tiles_kernel<T, BLOCKS><<<(unsigned)(tiles < most ? tiles : most), 256, 0, stream>>>(a);
     return cudaGetLastError();
 }
