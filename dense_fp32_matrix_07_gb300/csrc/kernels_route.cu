@@ -9,6 +9,9 @@
 // order like the floats; 0 stands for "not eligible" (a logit or key that is
 // -infinity or NaN).
 #include "experts.cuh"
+#include "ptx.cuh"
+
+#include <atomic>
 
 namespace sgemm_gb300 {
 
@@ -40,122 +43,197 @@ __device__ __forceinline__ float warp_sum(float x)
     return x;
 }
 
+// Sum over groups of L neighbouring lanes.
+template <int L>
+__device__ __forceinline__ float lanes_sum(float x)
+{
+#pragma unroll
+    for (int d = L / 2; d; d /= 2) x += __shfl_xor_sync(0xffffffffu, x, d);
+    return x;
+}
+
 __device__ __forceinline__ float sigmoid(float l) { return __fdiv_rn(1.0f, 1.0f + expf(-l)); }
 
 // exp(l - m); 1 where both are the same infinity.
 __device__ __forceinline__ float exp_below(float l, float m) { return l == m ? 1.0f : expf(l - m); }
 
+// Four neighbouring values.
+__device__ __forceinline__ void load4(const float *p, float *v)
+{
+    const float4 x = *reinterpret_cast<const float4 *>(p);
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+}
+
+__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float *v)
+{
+    const uint2 x = *reinterpret_cast<const uint2 *>(p);
+    v[0] = __uint_as_float(x.x << 16), v[1] = __uint_as_float(x.x & 0xffff0000u);
+    v[2] = __uint_as_float(x.y << 16), v[3] = __uint_as_float(x.y & 0xffff0000u);
+}
+
 constexpr int kRouteWarps = 8;
 
-// One warp per token; lane j holds experts j, j + 32, ...: NPER of them.
-template <class T, int NPER>
+// L lanes per token, each with NPER logits: runs of four, 4 L apart. Bound by
+// instructions (about 450 per warp of 128 experts and 8 rounds), not by the
+// logits' bytes. Fewer lanes with more logits each need fewer instructions a
+// token, but a longer chain of them: 8 lanes of 16 took 12.0 us for 16383
+// tokens and 11.8 us for 8 of them, 32 lanes of 4 take 10.7 us and 6.0 us.
+template <class T, int L, int NPER>
 __global__ void __launch_bounds__(kRouteWarps * 32)
-route_kernel(int64_t tokens, int E, const T *__restrict__ logits, int64_t ld, const float *__restrict__ bias,
+route_kernel(int64_t tokens, int E, const T *__restrict__ logits, int64_t ld, int vec, const float *__restrict__ bias,
              int use_sigmoid, int groups, int kept, int two, int k, int renorm, float scale,
              float *__restrict__ weights, int32_t *__restrict__ indices)
 {
-    extern __shared__ uint32_t group_keys[];      // E per warp, where groups are ranked
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
-    if (t >= tokens) return;
+    constexpr int TOKENS = kRouteWarps * 32 / L;  // of this CTA
+    extern __shared__ uint32_t group_keys[];      // E per token, where groups are ranked
+    __shared__ uint32_t ranks[TOKENS][32];
+    __shared__ int chosen[TOKENS][kMaxTop];
+    const int slot = threadIdx.x / L, sub = threadIdx.x % L;
+    const int64_t t0 = (int64_t)blockIdx.x * TOKENS + slot;
+    const bool there = t0 < tokens;
+    const int64_t t = there ? t0 : tokens - 1;    // lanes without a token go along and store nothing
     const T *row = logits + t * ld;
     float l[NPER];
 #pragma unroll
-    for (int i = 0; i < NPER; ++i) {
-        const int e = lane + 32 * i;
-        l[i] = e < E ? load_as_float(row + e) : __uint_as_float(0xff800000u);
+    for (int i = 0; i < NPER; i += 4) {
+        const int e = (i / 4) * (4 * L) + 4 * sub;
+        if (vec && e + 4 <= E) {
+            load4(row + e, l + i);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) l[i + j] = e + j < E ? load_as_float(row + e + j) : __uint_as_float(0xff800000u);
+        }
     }
-    // Softmax statistics over the eligible logits.
+    auto expert = [&](int i) { return (i / 4) * (4 * L) + 4 * sub + (i & 3); };
+    // Softmax statistics over the eligible logits. Renormalised weights of
+    // experts chosen by their logits need none: the whole row's sum cancels.
+    const bool by_score = bias != nullptr || two;
     float m = 0.0f, sum = 1.0f;
-    if (!use_sigmoid) {
+    if (!use_sigmoid && (by_score || !renorm)) {
         uint32_t best = 0;
 #pragma unroll
         for (int i = 0; i < NPER; ++i) best = max(best, key_of(l[i]));
-        best = __reduce_max_sync(0xffffffffu, best);
-        if (best) {
-            m = unordered(best);
-            sum = 0.0f;
 #pragma unroll
-            for (int i = 0; i < NPER; ++i)
-                if (key_of(l[i])) sum += exp_below(l[i], m);
-            sum = warp_sum(sum);
-        }
+        for (int d = L / 2; d; d /= 2) best = max(best, __shfl_xor_sync(0xffffffffu, best, d));
+        m = best ? unordered(best) : 0.0f;
+        sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NPER; ++i)
+            if (key_of(l[i])) sum += exp_below(l[i], m);
+        sum = lanes_sum<L>(sum);
+        if (!best) sum = 1.0f;
     }
     auto score = [&](float x) { return use_sigmoid ? sigmoid(x) : __fdiv_rn(exp_below(x, m), sum); };
-    const bool by_score = bias != nullptr || two;
     uint32_t key[NPER];
 #pragma unroll
     for (int i = 0; i < NPER; ++i) {
         key[i] = key_of(l[i]);
         if (by_score && key[i]) {
             float x = score(l[i]);
-            if (bias) x += bias[lane + 32 * i];
+            if (bias) x += bias[expert(i)];
             key[i] = key_of(x);
         }
     }
     if (kept < groups) {
         const int size = E / groups;
-        uint32_t *const mine = group_keys + warp * E;
+        uint32_t *const mine = group_keys + slot * E;
 #pragma unroll
         for (int i = 0; i < NPER; ++i)
-            if (lane + 32 * i < E) mine[lane + 32 * i] = key[i];
+            if (expert(i) < E) mine[expert(i)] = key[i];
         __syncwarp();
-        // `per` lanes (a power of two) scan each group.
+        // `per` lanes (a power of two) scan each group, L / per groups at a time.
         int per = 1;
-        while (2 * per * groups <= 32) per *= 2;
-        const int g = lane / per, sub = lane % per;
-        uint32_t b1 = 0, b2 = 0;
-        if (g < groups)
-            for (int j = sub; j < size; j += per) {
-                const uint32_t x = mine[g * size + j];
-                b2 = max(b2, min(b1, x));
-                b1 = max(b1, x);
+        while (2 * per * groups <= L) per *= 2;
+        for (int g0 = 0; g0 < groups; g0 += L / per) {
+            const int g = g0 + sub / per;
+            uint32_t b1 = 0, b2 = 0;
+            if (g < groups)
+                for (int j = sub % per; j < size; j += per) {
+                    const uint32_t x = mine[g * size + j];
+                    b2 = max(b2, min(b1, x));
+                    b1 = max(b1, x);
+                }
+            for (int d = 1; d < per; d *= 2) {
+                const uint32_t o1 = __shfl_xor_sync(0xffffffffu, b1, d), o2 = __shfl_xor_sync(0xffffffffu, b2, d);
+                b2 = max(max(b2, o2), min(b1, o1));
+                b1 = max(b1, o1);
             }
-        for (int d = 1; d < per; d *= 2) {
-            const uint32_t o1 = __shfl_xor_sync(0xffffffffu, b1, d), o2 = __shfl_xor_sync(0xffffffffu, b2, d);
-            b2 = max(max(b2, o2), min(b1, o1));
-            b1 = max(b1, o1);
+            // A group's rank; with `two` a group of fewer than two eligible
+            // experts comes last.
+            if (g < groups && sub % per == 0)
+                ranks[slot][g] = !two ? b1 : b2 ? key_of(unordered(b1) + unordered(b2)) : 0u;
         }
-        // A group's rank; with `two` a group of fewer than two eligible
-        // experts comes last.
-        uint32_t rank = b1;
-        if (two) rank = b2 ? key_of(unordered(b1) + unordered(b2)) : 0u;
-        int before = 0;
-        for (int o = 0; o < groups; ++o) {
-            const uint32_t other = __shfl_sync(0xffffffffu, rank, o * per);
-            before += (other > rank || (other == rank && o < g)) ? 1 : 0;
+        __syncwarp();
+        uint32_t keep = 0;
+        for (int g = sub; g < groups; g += L) {
+            const uint32_t rank = ranks[slot][g];
+            int before = 0;
+            for (int o = 0; o < groups; ++o) {
+                const uint32_t other = ranks[slot][o];
+                before += (other > rank || (other == rank && o < g)) ? 1 : 0;
+            }
+            if (before < kept) keep |= 1u << g;
         }
-        const uint32_t ballot = __ballot_sync(0xffffffffu, g < groups && before < kept);
 #pragma unroll
-        for (int i = 0; i < NPER; ++i) {
-            const int e = lane + 32 * i;
-            if (e < E && !((ballot >> ((e / size) * per)) & 1u)) key[i] = 0;
-        }
+        for (int d = L / 2; d; d /= 2) keep |= __shfl_xor_sync(0xffffffffu, keep, d);
+#pragma unroll
+        for (int i = 0; i < NPER; ++i)
+            if (expert(i) < E && !((keep >> (expert(i) / size)) & 1u)) key[i] = 0;
     }
     // k times the largest key, the lowest expert first among equals.
-    int chosen = -1;                              // lane j: the expert of slot j
     for (int j = 0; j < k; ++j) {
-        uint32_t best = 0;
-        int at = 0;
+        uint32_t best = key[NPER - 1];
+        int at = NPER - 1;
 #pragma unroll
-        for (int i = NPER - 1; i >= 0; --i)
+        for (int i = NPER - 2; i >= 0; --i)
             if (key[i] >= best) best = key[i], at = i;
-        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-        if (top == 0) break;
-        const int e = (int)__reduce_min_sync(0xffffffffu, best == top ? (uint32_t)(lane + 32 * at) : 0xffffffffu);
-        if (lane == j) chosen = e;
+        int e = expert(at);
+        if constexpr (L == 32) {
+            const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+            e = (int)__reduce_min_sync(0xffffffffu, best == top ? (uint32_t)e : 0xffffffffu);
+            best = top;
+        } else {
+#pragma unroll
+            for (int d = L / 2; d; d /= 2) {
+                const uint32_t other = __shfl_xor_sync(0xffffffffu, best, d);
+                const int oe = __shfl_xor_sync(0xffffffffu, e, d);
+                if (other > best || (other == best && oe < e)) best = other, e = oe;
+            }
+        }
 #pragma unroll
         for (int i = 0; i < NPER; ++i)
-            if (lane + 32 * i == e) key[i] = 0;
+            if (expert(i) == e) key[i] = 0;
+        if (sub == 0) chosen[slot][j] = best ? e : -1;
     }
-    float w = chosen >= 0 ? score(load_as_float(row + chosen)) : 0.0f;
-    if (renorm) {
-        const float total = warp_sum(w);
-        w = total > 0.0f ? __fdiv_rn(w, total) : 0.0f;
+    __syncwarp();
+    // Without the row's statistics the first choice has the largest logit, and
+    // the sum is that of the chosen.
+    const bool plain = !use_sigmoid && !by_score && renorm;
+    if (plain) m = chosen[slot][0] >= 0 ? load_as_float(row + chosen[slot][0]) : 0.0f;
+    constexpr int HELD = kMaxTop / L;             // slots per lane
+    int e[HELD];
+    float w[HELD], total = 0.0f;
+#pragma unroll
+    for (int h = 0; h < HELD; ++h) {
+        const int j = sub + h * L;
+        e[h] = j < k ? chosen[slot][j] : -1;
+        w[h] = 0.0f;
+        if (e[h] >= 0) {
+            const float x = load_as_float(row + e[h]);
+            w[h] = plain ? exp_below(x, m) : score(x);
+        }
+        total += w[h];
     }
-    if (lane < k) {
-        weights[t * k + lane] = w * scale;
-        indices[t * k + lane] = chosen;
+    if (renorm) total = lanes_sum<L>(total);
+    if (!there) return;
+#pragma unroll
+    for (int h = 0; h < HELD; ++h) {
+        const int j = sub + h * L;
+        if (j < k) {
+            if (renorm) w[h] = total > 0.0f ? __fdiv_rn(w[h], total) : 0.0f;
+            weights[t * k + j] = w[h] * scale;
+            indices[t * k + j] = e[h];
+        }
     }
 }
 
@@ -169,10 +247,21 @@ route_kernel(int64_t tokens, int E, const T *__restrict__ logits, int64_t ld, co
 // Only the second needs the whole row of logits; the others read the chosen
 // ones and write a row of zeros with k values in it.
 template <class T>
+__device__ __forceinline__ void zero_row(T *out, int E, int vec, int lane)
+{
+    constexpr int N = 16 / (int)sizeof(T);
+    if (vec) {
+        for (int i = lane * N; i < E; i += 32 * N) *reinterpret_cast<uint4 *>(out + i) = make_uint4(0, 0, 0, 0);
+    } else {
+        for (int i = lane; i < E; i += 32) store_from_float(out + i, 0.0f);
+    }
+}
+
+template <class T>
 __global__ void __launch_bounds__(kRouteWarps * 32)
 route_backward_kernel(int64_t tokens, int E, const T *__restrict__ logits, int64_t ld, int use_sigmoid, int k,
                       int renorm, float scale, const int32_t *__restrict__ indices,
-                      const float *__restrict__ grad_w, T *__restrict__ grad, int64_t ld_g)
+                      const float *__restrict__ grad_w, T *__restrict__ grad, int64_t ld_g, int vec)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
@@ -201,7 +290,7 @@ route_backward_kernel(int64_t tokens, int E, const T *__restrict__ logits, int64
             d = 0.0f;
             if (e >= 0 && D > 0.0f) d = scale / D * (g - mean / D) * (s * sigmoid(-l));
         }
-        for (int i = lane; i < E; i += 32) store_from_float(out + i, 0.0f);
+        zero_row(out, E, vec, lane);
     } else if (renorm) {
         float m = e >= 0 ? l : __uint_as_float(0xff800000u);
 #pragma unroll
@@ -211,7 +300,7 @@ route_backward_kernel(int64_t tokens, int E, const T *__restrict__ logits, int64
         const float w = total > 0.0f ? x / total : 0.0f;
         const float mean = warp_sum(w * g);
         d = scale * w * (g - mean);
-        for (int i = lane; i < E; i += 32) store_from_float(out + i, 0.0f);
+        zero_row(out, E, vec, lane);
     } else {
         uint32_t best = 0;
         for (int i = lane; i < E; i += 32) best = max(best, key_of(load_as_float(row + i)));
@@ -244,14 +333,21 @@ route_backward_kernel(int64_t tokens, int E, const T *__restrict__ logits, int64
 // warps before), and each warp walks its part again, 32 pairs at a time,
 // ranking equal experts within the 32 by their lane. Nothing depends on the
 // order in which threads run.
-constexpr int kDispatchThreads = 1024, kDispatchWarps = 32;
+//
+// Up to 131072 pairs (where the device takes clusters of 16; else 65536) the
+// blocks are one cluster, which reads its neighbours' counts from their shared
+// memory: one launch, no scratch. Beyond that 128 blocks run behind a launch
+// that leaves every block's counts in scratch: what bounds large sorts is the
+// scattered writes of token_of, about one a cycle and SM.
+constexpr int kDispatchThreads = 1024, kDispatchWarps = 32, kDispatchHeld = 8, kDispatchCluster = 16;
+constexpr int64_t kDispatchRun = 32 * kDispatchWarps * kDispatchHeld;   // pairs a block can hold in registers
 
 struct DispatchArgs {
     int64_t n, run;                 // pairs, and pairs per block (a multiple of 1024)
     int k, E;
     const int32_t *indices;
     int32_t *offsets, *row_of, *token_of;
-    int32_t *counts;                // [block][E], with more than one block
+    int32_t *counts;                // [block][E], with blocks that are no cluster
     int blocks;
 };
 
@@ -266,56 +362,112 @@ __device__ __forceinline__ uint32_t same_expert(int e, int bits)
     return same;
 }
 
+// The expert of pair i, E where it has none.
 __device__ __forceinline__ int valid_expert(const DispatchArgs &a, int64_t i)
 {
-    if (i >= a.n) return -1;
+    if (i >= a.n) return a.E;
     const int e = a.indices[i];
-    return e >= 0 && e < a.E ? e : -1;
+    return e >= 0 && e < a.E ? e : a.E;
 }
 
 __global__ void __launch_bounds__(kDispatchThreads)
 dispatch_count_kernel(const DispatchArgs a)
 {
     extern __shared__ int hist[];
+    ptx::grid_launch_dependents();                // the placing kernel's blocks read their pairs meanwhile
     for (int e = threadIdx.x; e < a.E; e += kDispatchThreads) hist[e] = 0;
     __syncthreads();
     const int64_t i0 = (int64_t)blockIdx.x * a.run, i1 = i0 + a.run < a.n ? i0 + a.run : a.n;
     for (int64_t i = i0 + threadIdx.x; i < i1; i += kDispatchThreads) {
         const int e = valid_expert(a, i);
-        if (e >= 0) atomicAdd(&hist[e], 1);
+        if (e < a.E) atomicAdd(&hist[e], 1);
     }
     __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += kDispatchThreads) a.counts[(int64_t)blockIdx.x * a.E + e] = hist[e];
 }
 
+// HELD: the warp's part of the run stays in registers between the two walks.
+template <bool HELD>
 __global__ void __launch_bounds__(kDispatchThreads)
 dispatch_place_kernel(const DispatchArgs a)
 {
     extern __shared__ int next[];                 // [warp][E]: counts, then the next row of each expert
     __shared__ int sums[kDispatchWarps];
+    __shared__ int totals[kMaxExperts], earlier[kMaxExperts];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t part = a.run / kDispatchWarps, i0 = (int64_t)blockIdx.x * a.run + warp * part;
+    const int steps = (int)(part / 32);
+    int held[HELD ? kDispatchHeld : 1];
+    if constexpr (HELD) {
+#pragma unroll
+        for (int j = 0; j < kDispatchHeld; ++j) held[j] = j < steps ? valid_expert(a, i0 + 32 * j + lane) : a.E;
+    }
     for (int i = threadIdx.x; i < kDispatchWarps * a.E; i += kDispatchThreads) next[i] = 0;
     __syncthreads();
-    const int64_t part = a.run / kDispatchWarps;
-    const int64_t i0 = (int64_t)blockIdx.x * a.run + warp * part;
     int *const mine = next + warp * a.E;
-    for (int64_t i = i0 + lane; i < i0 + part && i < a.n; i += 32) {
-        const int e = valid_expert(a, i);
-        if (e >= 0) atomicAdd(&mine[e], 1);
+    if constexpr (HELD) {
+#pragma unroll
+        for (int j = 0; j < kDispatchHeld; ++j)
+            if (held[j] < a.E) atomicAdd(&mine[held[j]], 1);
+    } else {
+        for (int j = 0; j < steps; ++j) {
+            const int e = valid_expert(a, i0 + 32 * j + lane);
+            if (e < a.E) atomicAdd(&mine[e], 1);
+        }
     }
     __syncthreads();
     // Thread e: expert e (E <= 1024).
     const int e = threadIdx.x;
-    int total = 0, before = 0;
+    int total = 0, before = 0, of_warp[kDispatchWarps];
     if (e < a.E) {
-        if (a.blocks > 1) {
-            for (int b = 0; b < a.blocks; ++b) {
-                const int c = a.counts[(int64_t)b * a.E + e];
-                total += c;
-                before += b < (int)blockIdx.x ? c : 0;
+#pragma unroll
+        for (int w = 0; w < kDispatchWarps; ++w) of_warp[w] = next[w * a.E + e];
+#pragma unroll
+        for (int w = 0; w < kDispatchWarps; ++w) total += of_warp[w];
+    }
+    if (a.counts) {
+        // Sums over the blocks: 1024 / (E rounded up to a power of two) threads
+        // share an expert.
+        ptx::grid_dependency_wait();
+        int width = 32;
+        while (width < a.E) width *= 2;
+        const int x = threadIdx.x % width, share = threadIdx.x / width, shares = kDispatchThreads / width;
+        const int b0 = a.blocks * share / shares, b1 = a.blocks * (share + 1) / shares;
+        int all_of = 0, before_of = 0;
+        if (x < a.E) {
+#pragma unroll 16
+            for (int b = b0; b < b1; ++b) {
+                const int c = __ldcg(a.counts + (int64_t)b * a.E + x);
+                all_of += c;
+                before_of += b < (int)blockIdx.x ? c : 0;
             }
-        } else {
-            for (int w = 0; w < kDispatchWarps; ++w) total += next[w * a.E + e];
+        }
+        totals[threadIdx.x] = all_of;
+        earlier[threadIdx.x] = before_of;
+        __syncthreads();
+        total = 0;
+        if (e < a.E)
+            for (int s = 0; s < shares; ++s) {
+                total += totals[s * width + e];
+                before += earlier[s * width + e];
+            }
+    } else if (a.blocks > 1) {
+        // The blocks of the cluster trade their counts.
+        if (e < a.E) totals[e] = total;
+        ptx::cluster_sync_all();
+        if (e < a.E) {
+            total = 0;
+#pragma unroll 8
+            for (int b = 0; b < a.blocks; ++b) {
+                int of_block;
+                asm volatile("{\n\t.reg .b32 ra;\n\tmapa.shared::cluster.u32 ra, %1, %2;\n\t"
+                             "ld.shared::cluster.s32 %0, [ra];\n\t}"
+                             : "=r"(of_block)
+                             : "r"(ptx::smem_addr(&totals[e])), "r"(b)
+                             : "memory");
+                total += of_block;
+                before += b < (int)blockIdx.x ? of_block : 0;
+            }
         }
     }
     // Exclusive prefix sum of `total` over the experts.
@@ -327,69 +479,86 @@ dispatch_place_kernel(const DispatchArgs a)
     }
     if (lane == 31) sums[warp] = sum;
     __syncthreads();
-    int base = 0;
-    for (int w = 0; w < warp; ++w) base += sums[w];
+    const int others = sums[lane];
+    const int base = __reduce_add_sync(0xffffffffu, lane < warp ? others : 0);
+    const int all = __reduce_add_sync(0xffffffffu, others);
     const int first = base + sum - total;
     if (e < a.E) {
         int at = first + before;
+#pragma unroll
         for (int w = 0; w < kDispatchWarps; ++w) {
-            const int c = next[w * a.E + e];
             next[w * a.E + e] = at;
-            at += c;
+            at += of_warp[w];
         }
         if (blockIdx.x == 0) a.offsets[e] = first;
     }
-    int all = 0;
-    for (int w = 0; w < kDispatchWarps; ++w) all += sums[w];
     if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[a.E] = all;
     __syncthreads();
     const int bits = 32 - __clz(a.E);             // E itself marks "no expert"
-    for (int64_t b = i0; b < i0 + part && b < a.n; b += 32) {
-        const int64_t i = b + lane;
-        const int x = valid_expert(a, i), as = x < 0 ? a.E : x;
-        const uint32_t same = same_expert(as, bits);
+    auto place = [&](int64_t i, int x) {
+        const uint32_t same = same_expert(x, bits);
         const int rank = __popc(same & ((1u << lane) - 1u));
         int at = -1;
-        if (x >= 0) at = mine[x] + rank;
+        if (x < a.E) at = mine[x] + rank;
         __syncwarp();
-        if (x >= 0 && rank == 0) mine[x] += __popc(same);
+        if (x < a.E && rank == 0) mine[x] += __popc(same);
         __syncwarp();
         if (i < a.n) a.row_of[i] = at;
         if (at >= 0) a.token_of[at] = (int32_t)(i / a.k);
+    };
+    if constexpr (HELD) {
+#pragma unroll
+        for (int j = 0; j < kDispatchHeld; ++j)
+            if (j < steps) place(i0 + 32 * j + lane, held[j]);
+    } else {
+        for (int j = 0; j < steps; ++j) place(i0 + 32 * j + lane, valid_expert(a, i0 + 32 * j + lane));
     }
     // Rows that no pair has.
     for (int64_t r = all + (int64_t)blockIdx.x * kDispatchThreads + threadIdx.x; r < a.n;
          r += (int64_t)gridDim.x * kDispatchThreads)
         a.token_of[r] = -1;
+    // No block leaves while another may read its counts.
+    if (!a.counts && a.blocks > 1) ptx::cluster_sync_all();
 }
 
-// Blocks of a dispatch: one up to 16384 pairs (512 per warp), at most 128.
+// Largest cluster that every device of this process so far takes.
+std::atomic<int> g_dispatch_cluster{kDispatchCluster};
+
+// One block up to 4096 pairs (128 per warp), then a cluster of 8, then the
+// largest cluster (the last blocks of either may have nothing), then 128.
+int64_t dispatch_blocks(int64_t n)
+{
+    const int most = g_dispatch_cluster.load();
+    return n <= 4096 ? 1 : n <= 16384 ? 8 : n <= most * kDispatchRun ? most : 128;
+}
+
+bool dispatch_clustered(int64_t n) { return n <= g_dispatch_cluster.load() * kDispatchRun; }
+
 int64_t dispatch_run(int64_t n)
 {
-    if (n <= 16384) return n > 0 ? (n + 1023) / 1024 * 1024 : 1024;
-    int64_t run = (n + 127) / 128;
-    run = (run + 1023) / 1024 * 1024;
-    return run < 4096 ? 4096 : run;
+    const int64_t blocks = dispatch_blocks(n), run = (n + blocks - 1) / blocks;
+    return run > 0 ? (run + 1023) / 1024 * 1024 : 1024;
 }
 
 template <class T>
 cudaError_t route_of(const RouteArgs &r, float *weights, int32_t *indices, cudaStream_t stream)
 {
-    const unsigned grid = (unsigned)((r.T + kRouteWarps - 1) / kRouteWarps);
-    const size_t smem = r.kept < r.groups ? (size_t)kRouteWarps * r.E * 4 : 0;
     const T *l = static_cast<const T *>(r.logits);
-    auto go = [&](auto kernel) {
-        kernel<<<grid, kRouteWarps * 32, smem, stream>>>(r.T, r.E, l, r.ld, r.bias, r.sigmoid, r.groups, r.kept, r.two,
-                                                         r.k, r.renorm, r.scale, weights, indices);
+    // Runs of four logits in one load.
+    const int vec = (reinterpret_cast<uintptr_t>(l) % (4 * sizeof(T)) == 0 && r.ld % 4 == 0) ? 1 : 0;
+    auto go = [&](auto kernel, int lanes) {
+        const int per_cta = kRouteWarps * 32 / lanes;
+        const size_t smem = r.kept < r.groups ? (size_t)per_cta * r.E * 4 : 0;
+        kernel<<<(unsigned)((r.T + per_cta - 1) / per_cta), kRouteWarps * 32, smem, stream>>>(
+            r.T, r.E, l, r.ld, vec, r.bias, r.sigmoid, r.groups, r.kept, r.two, r.k, r.renorm, r.scale, weights, indices);
         return cudaGetLastError();
     };
-    const int per = (r.E + 31) / 32;
-    if (per <= 1) return go(route_kernel<T, 1>);
-    if (per <= 2) return go(route_kernel<T, 2>);
-    if (per <= 4) return go(route_kernel<T, 4>);
-    if (per <= 8) return go(route_kernel<T, 8>);
-    if (per <= 16) return go(route_kernel<T, 16>);
-    return go(route_kernel<T, 32>);
+    if (r.E <= 32) return go(route_kernel<T, 8, 4>, 8);
+    if (r.E <= 64) return go(route_kernel<T, 16, 4>, 16);
+    if (r.E <= 128) return go(route_kernel<T, 32, 4>, 32);
+    if (r.E <= 256) return go(route_kernel<T, 32, 8>, 32);
+    if (r.E <= 512) return go(route_kernel<T, 32, 16>, 32);
+    return go(route_kernel<T, 32, 32>, 32);
 }
 
 }  // namespace
@@ -403,27 +572,51 @@ cudaError_t launch_route_backward(const RouteArgs &r, const int32_t *indices, co
                                   int64_t ld_g, int, cudaStream_t stream)
 {
     const unsigned grid = (unsigned)((r.T + kRouteWarps - 1) / kRouteWarps);
+    const int64_t per16 = r.bf16 ? 8 : 4;
+    const int vec = (reinterpret_cast<uintptr_t>(grad_logits) % 16 == 0 && ld_g % per16 == 0 && r.E % per16 == 0) ? 1 : 0;
     if (r.bf16)
         route_backward_kernel<<<grid, kRouteWarps * 32, 0, stream>>>(
             r.T, r.E, static_cast<const __nv_bfloat16 *>(r.logits), r.ld, r.sigmoid, r.k, r.renorm, r.scale, indices,
-            grad_w, static_cast<__nv_bfloat16 *>(grad_logits), ld_g);
+            grad_w, static_cast<__nv_bfloat16 *>(grad_logits), ld_g, vec);
     else
         route_backward_kernel<<<grid, kRouteWarps * 32, 0, stream>>>(
             r.T, r.E, static_cast<const float *>(r.logits), r.ld, r.sigmoid, r.k, r.renorm, r.scale, indices, grad_w,
-            static_cast<float *>(grad_logits), ld_g);
+            static_cast<float *>(grad_logits), ld_g, vec);
     return cudaGetLastError();
 }
 
 size_t dispatch_scratch_bytes(int64_t n, int E)
 {
-    const int64_t run = dispatch_run(n), blocks = (n + run - 1) / run;
-    return blocks > 1 ? (size_t)(blocks * E) * 4 : 0;
+    return dispatch_clustered(n) ? 0 : (size_t)(dispatch_blocks(n) * E) * 4;
 }
 
 cudaError_t prepare_route()
 {
-    return cudaFuncSetAttribute(dispatch_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kDispatchWarps * kMaxExperts * 4);
+    const int smem = kDispatchWarps * kMaxExperts * 4;
+    cudaError_t e = cudaFuncSetAttribute(dispatch_place_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(dispatch_place_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(dispatch_place_kernel<true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    // Clusters of 16 where the device can hold one at the largest size.
+    cudaLaunchConfig_t lc = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = kDispatchCluster;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    lc.attrs = &attr;
+    lc.numAttrs = 1;
+    lc.gridDim = dim3(kDispatchCluster);
+    lc.blockDim = dim3(kDispatchThreads);
+    lc.dynamicSmemBytes = smem;
+    int clusters = 0;
+    if (cudaOccupancyMaxActiveClusters(&clusters, dispatch_place_kernel<true>, &lc) != cudaSuccess || clusters < 1) {
+        cudaGetLastError();
+        g_dispatch_cluster.store(8);
+    }
+    return cudaSuccess;
 }
 
 cudaError_t launch_dispatch(int64_t T, int k, int E, const int32_t *indices, int32_t *offsets, int32_t *row_of,
@@ -439,15 +632,31 @@ cudaError_t launch_dispatch(int64_t T, int k, int E, const int32_t *indices, int
     a.row_of = row_of;
     a.token_of = token_of;
     a.counts = static_cast<int32_t *>(scratch);
-    a.blocks = (int)((a.n + a.run - 1) / a.run);
-    if (a.blocks < 1) a.blocks = 1;
-    if (a.blocks > 1) {
+    a.blocks = (int)dispatch_blocks(a.n);
+    cudaLaunchConfig_t lc = {};
+    cudaLaunchAttribute attr;
+    if (scratch) {
         dispatch_count_kernel<<<a.blocks, kDispatchThreads, (size_t)E * 4, stream>>>(a);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        lc.numAttrs = 1;
+    } else {
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = (unsigned)a.blocks;
+        attr.val.clusterDim.y = 1;
+        attr.val.clusterDim.z = 1;
+        lc.numAttrs = a.blocks > 1 ? 1 : 0;
     }
-    dispatch_place_kernel<<<a.blocks, kDispatchThreads, (size_t)kDispatchWarps * E * 4, stream>>>(a);
-    return cudaGetLastError();
+    lc.attrs = &attr;
+    lc.gridDim = dim3((unsigned)a.blocks);
+    lc.blockDim = dim3(kDispatchThreads);
+    lc.dynamicSmemBytes = (size_t)kDispatchWarps * E * 4;
+    lc.stream = stream;
+    const cudaError_t e = a.run <= kDispatchRun ? cudaLaunchKernelEx(&lc, dispatch_place_kernel<true>, a)
+                                                : cudaLaunchKernelEx(&lc, dispatch_place_kernel<false>, a);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace sgemm_gb300

@@ -539,7 +539,9 @@ def test_route_with_infinite_logits(cuda_device):
 
 
 @pytest.mark.parametrize("T,k,E", [(0, 4, 8), (1, 1, 1), (7, 6, 64), (100, 8, 256), (2047, 8, 60), (2049, 8, 1024),
-                                   (5000, 7, 128), (70000, 8, 16)])
+                                   (5000, 7, 128), (70000, 8, 16), (4096, 1, 33), (4097, 1, 33), (16384, 8, 256),
+                                   (16385, 8, 64),
+                                   (16384, 1, 9), (16385, 1, 9)])
 def test_dispatch(cuda_device, T, k, E):
     rng = np.random.RandomState(T + E)
     idx = rng.randint(-1, E + 1, (T, k)) if T % 2 else np.minimum(rng.geometric(0.05, (T, k)) - 1, E - 1)
@@ -555,7 +557,7 @@ def test_dispatch(cuda_device, T, k, E):
 
 
 def test_dispatch_reports_a_failed_allocation(cuda_device):
-    T, k, E = 5000, 7, 128                           # more than one block: counts in scratch
+    T, k, E = 20000, 7, 128                          # more pairs than a cluster holds: counts in scratch
     di = torch.zeros(T, k, dtype=torch.int32, device="cuda")
     out = [torch.full((n,), 99, dtype=torch.int32, device="cuda") for n in (E + 1, T * k, T * k)]
     ok(sg.sgemm_test_fail_next_allocs(1))
