@@ -32,10 +32,10 @@
 // shared memory first. A tile may read rows past its group's end: they are
 // the next group's, or zero fill, and are never stored.
 //
-// Few tiles: `split` CTAs of a cluster share a tile's K blocks. Each leaves
-// its partial sums in its own shared memory, and after a cluster barrier CTA
-// r adds columns r, r + split, ... over the CTAs in rank order: the result
-// does not depend on timing.
+// Few tiles: `split` CTAs of a cluster share a tile's K blocks. Each sends its
+// partial sums of column j to the shared memory of CTA j % split, and after a
+// cluster barrier that CTA adds the parts in rank order: the result does not
+// depend on timing.
 //
 // Every wait is bounded; a role that gives up sets the device error word and
 // goes to the teardown, which drains copies and MMAs.
@@ -363,15 +363,12 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar)
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank)
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, uint32_t rank, float v)
 {
-    float v;
-    asm volatile("{\n\t.reg .b32 ra;\n\tmapa.shared::cluster.u32 ra, %1, %2;\n\t"
-                 "ld.shared::cluster.f32 %0, [ra];\n\t}"
-                 : "=f"(v)
-                 : "r"(addr), "r"(rank)
+    asm volatile("{\n\t.reg .b32 ra;\n\tmapa.shared::cluster.u32 ra, %0, %1;\n\t"
+                 "st.shared::cluster.f32 [ra], %2;\n\t}" ::"r"(addr),
+                 "r"(rank), "f"(v)
                  : "memory");
-    return v;
 }
 
 __device__ __forceinline__ float ld_shared_f32(uint32_t addr)
@@ -379,11 +376,6 @@ __device__ __forceinline__ float ld_shared_f32(uint32_t addr)
     float v;
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
-}
-
-__device__ __forceinline__ void st_shared_f32(uint32_t addr, float v)
-{
-    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 __device__ __forceinline__ void st_shared_u32x4(uint32_t addr, uint4 v)
@@ -443,6 +435,10 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
         return;
     }
 
+    if (warp == 2 && lane == 0) {
+        ptx::prefetch_tensormap(&mapP);
+        ptx::prefetch_tensormap(&mapQ);
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             ptx::mbar_init(full_bar(s), 1);
@@ -464,33 +460,40 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
         for (int g = threadIdx.x; g < p.groups; g += Cfg::THREADS) {
             int lo, hi;
             group_range(p.offsets, g, rows, lo, hi);
-            table[g] = (int)(((int64_t)hi - lo + unit - 1) / unit);
+            table[g] = (int)(((uint32_t)(hi - lo) + (uint32_t)unit - 1) / (uint32_t)unit);
         }
         __syncthreads();
         if (warp == 0) {
-            int64_t carry = 0;
+            // Offsets that are not a partition may sum to anything: no entry
+            // passes what the kernel can walk. (A group has at most 2^27
+            // tiles, so 32 of them and a carry held to 2^27 stay below 2^32.)
+            const uint32_t most = p.mode == kFp8GroupK ? (uint32_t)p.nk
+                                                       : (uint32_t)(INT32_MAX / p.weight_tiles - 2 * kRaster);
+            const uint32_t held = most < (1u << 27) ? most : 1u << 27;
+            uint32_t carry = 0;
             for (int g0 = 0; g0 < p.groups; g0 += 32) {
                 const int g = g0 + lane;
-                const int64_t mine = g < p.groups ? table[g] : 0;
-                int64_t sum = mine;
+                const uint32_t mine = g < p.groups ? table[g] : 0;
+                uint32_t sum = mine < held ? mine : held;
 #pragma unroll
                 for (int d = 1; d < 32; d *= 2) {
-                    const int64_t up = __shfl_up_sync(0xffffffffu, sum, d);
-                    if (lane >= d) sum += up;
+                    const uint32_t up = __shfl_up_sync(0xffffffffu, sum, d);
+                    if (lane >= d) sum = sum + up < held ? sum + up : held;
                 }
-                // Offsets that are not a partition may sum to anything: no
-                // entry passes what the kernel can walk.
-                const int64_t most = p.mode == kFp8GroupK ? p.nk : INT32_MAX / p.weight_tiles - 2 * kRaster;
-                const int64_t before = carry + sum - mine;
-                if (g < p.groups) table[g] = (int)(before < most ? before : most);
-                carry += __shfl_sync(0xffffffffu, sum, 31);
-                if (g0 + 32 >= p.groups && lane == 0) table[p.groups] = (int)(carry < most ? carry : most);
+                const uint32_t end = carry + sum < held ? carry + sum : held;
+                const uint32_t before = __shfl_up_sync(0xffffffffu, end, 1);
+                if (g < p.groups) table[g] = (int)(lane == 0 ? carry : before);
+                carry = __shfl_sync(0xffffffffu, end, 31);
+                if (g0 + 32 >= p.groups && lane == 0) table[p.groups] = (int)carry;
             }
         }
     }
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
+    // The CTAs of a split tile write into each other's shared memory in the
+    // end: each says that it has begun, and waits for the others before that.
+    if (Cfg::CAN_SPLIT && split > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     const uint32_t taddr = *reinterpret_cast<uint32_t *>(smem_raw + (tmem_slot - raw));
 
     const uint32_t t_first = blockIdx.x / split, t_step = gridDim.x / split;
@@ -505,10 +508,6 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
     if (warp == 0) {
         // ------------------------------ TMA producer ------------------------------
         const uint32_t on = elect_one();
-        if (on) {
-            ptx::prefetch_tensormap(&mapP);
-            ptx::prefetch_tensormap(&mapQ);
-        }
         const uint64_t policy = ptx::policy_evict_last();
         uint32_t it = 0;
         bool ok = true;
@@ -625,6 +624,7 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
         const int row = 32 * q + lane;                    // lane of tensor memory
         const uint32_t lanes = taddr + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * CW);
         const float *const slots = reinterpret_cast<const float *>(smem_raw + (base - raw) + Cfg::OFF_SCALES);
+        if (Cfg::CAN_SPLIT && split > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         if constexpr (Cfg::EPI_REGS > 0) ptx::setmaxnreg_inc<Cfg::EPI_REGS>();
         uint32_t it = 0, batch = 0;
         bool ok = true;
@@ -732,18 +732,34 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
             if constexpr (SWAP) {
                 // Lane = row of B (column of C), column = row of A.
                 if (split == 1) {
-                    const int n = w.b_row + row;
+                    const int n = w.b_row + row, m0 = w.a_row + half * CW;
+                    const int rows = n < p.N ? w.a_end - m0 : 0;
+                    const int64_t at = c_base + (int64_t)m0 * p.ldc + n;
+                    if (p.c_bf16 && p.beta == 0.0f) {
+                        __nv_bfloat16 *c = static_cast<__nv_bfloat16 *>(p.C) + at;
 #pragma unroll
-                    for (int j = 0; j < CW; ++j) {
-                        const int m = w.a_row + half * CW + j;
-                        if (n < p.N && m < w.a_end)
-                            store_c(p, c_base + (int64_t)m * p.ldc + n, (j & 1) ? acc[j / 2].y : acc[j / 2].x);
+                        for (int j = 0; j < CW; ++j, c += p.ldc)
+                            if (j < rows) *c = __float2bfloat16_rn((j & 1) ? acc[j / 2].y : acc[j / 2].x);
+                    } else if (p.beta == 0.0f) {
+                        float *c = static_cast<float *>(p.C) + at;
+#pragma unroll
+                        for (int j = 0; j < CW; ++j, c += p.ldc)
+                            if (j < rows) *c = (j & 1) ? acc[j / 2].y : acc[j / 2].x;
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < CW; ++j)
+                            if (j < rows) store_c(p, at + j * p.ldc, (j & 1) ? acc[j / 2].y : acc[j / 2].x);
                     }
                 } else {
-                    const uint32_t part = base + Cfg::OFF_PARTIAL;
+                    // To the CTA that adds column j over the cluster: j % split.
+                    const int per = BN / split, shift = __ffs(split) - 1;
+                    const uint32_t mine = base + Cfg::OFF_PARTIAL + 4 * (rank * per * 128 + row);
 #pragma unroll
-                    for (int j = 0; j < CW; ++j)
-                        st_shared_f32(part + 4 * ((half * CW + j) * 128 + row), (j & 1) ? acc[j / 2].y : acc[j / 2].x);
+                    for (int j = 0; j < CW; ++j) {
+                        const int col = half * CW + j;
+                        st_cluster_f32(mine + 4 * 128 * (col >> shift), (uint32_t)(col & (split - 1)),
+                                       (j & 1) ? acc[j / 2].y : acc[j / 2].x);
+                    }
                 }
             } else {
                 // Lane = row of A; 128 bytes of each of 32 rows at a time go
@@ -816,30 +832,34 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
     }
 
     // ------------------------------ teardown ------------------------------
-    __syncthreads();
     if constexpr (Cfg::CAN_SPLIT) {
         if (split > 1) {
-            // One tile per cluster: every CTA's partial sums are in its
-            // shared memory. CTA `rank` adds every split-th column of the
-            // tile over the CTAs in rank order.
+            __syncwarp();
+            if (warp < 4) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+            // One tile per cluster. Its columns' parts are here, one set per
+            // CTA of the cluster; this CTA adds columns rank, rank + split, ..
+            // in rank order. Nothing reaches into another CTA after this
+            // barrier.
             ptx::cluster_sync_all();
             if (t_first < tiles) {
                 const Fp8Item w = fp8_item<Cfg>(p, table, t_first, rank);
                 const int64_t c_base = p.mode == kFp8GroupK ? w.group * p.stride_c : 0;
                 const uint32_t part = base + Cfg::OFF_PARTIAL;
-                for (int i = threadIdx.x; i < (BN / split) * 128; i += Cfg::THREADS) {
-                    const int col = (i >> 7) * split + rank, l = i & 127;
-                    const int m = w.a_row + col, n = w.b_row + l;
+                const int per = BN / split;
+                for (int i = threadIdx.x; i < per * 128; i += Cfg::THREADS) {
+                    const int m = w.a_row + (i >> 7) * split + rank, n = w.b_row + (i & 127);
                     if (m < w.a_end && n < p.N) {
                         float v = 0.0f;
-                        for (int r = 0; r < split; ++r) v += ld_cluster_f32(part + 4 * (col * 128 + l), (uint32_t)r);
+#pragma unroll
+                        for (int r = 0; r < 8; ++r)
+                            if (r < split) v += ld_shared_f32(part + 4 * (r * per * 128 + i));
                         store_c(p, c_base + (int64_t)m * p.ldc + n, v);
                     }
                 }
             }
-            ptx::cluster_sync_all();
         }
     }
+    __syncthreads();
     if (warp == 1) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(taddr, Cfg::TMEM_COLS);
@@ -872,7 +892,6 @@ cudaError_t encode_fp8(CUtensorMap *map, const uint8_t *ptr, int64_t rows, int64
 
 using Wide256 = Fp8Cfg<256, false>;
 using Wide128 = Fp8Cfg<128, false>;
-using Swap128 = Fp8Cfg<128, true>;
 using Swap64 = Fp8Cfg<64, true>;
 using Swap32 = Fp8Cfg<32, true>;
 using Swap16 = Fp8Cfg<16, true>;
@@ -962,26 +981,41 @@ cudaError_t launch_cfg(const Fp8Args &g, const Fp8Plan &plan, cudaStream_t strea
 
 }  // namespace
 
+// Which kernel, by sizes (152 SMs, N = K = 4096 or 64 experts of 2048 x 2048;
+// us):
+//   rows of A per group up to 16, 32, 64: as many columns, B on the lanes. 16
+//   rows 10.1; 64 rows 12.5, on 128 x 128 tiles 17.6.
+//   65 to 128 rows: 128 x 128 tiles with A on the lanes where they fill half
+//   the SMs (128 x 16384: 22.1 against 26.5; 8000 rows over the experts 75.6
+//   against 97.2), else 64 columns with split tiles (128 x 4096: 14.6 against
+//   17.6).
+//   More: 128 x 256 tiles, unless 128 x 128 ones take fewer waves of CTAs by
+//   more than the quarter that they are slower per value.
 Fp8Plan plan_fp8(const Fp8Args &g)
 {
-    Fp8Plan p{256, false, 1, 0};
-    const int64_t nk = ceil_div(g.K, kBlock);
-    // Rows of A per group (all rows of a dense product).
+    const int64_t nk = ceil_div(g.K, kBlock), sms = g.num_sms;
     const int64_t per = g.mode == kFp8GroupRows ? ceil_div(g.M, g.groups) : g.M;
-    if (g.mode != kFp8GroupK && per <= 128) {
+    // Tiles of tt rows of A by wt of B; for groups of rows, at most.
+    auto tiles_of = [&](int64_t tt, int64_t wt) {
+        const int64_t hit = g.groups < g.M ? g.groups : g.M;
+        const int64_t tokens = g.mode == kFp8GroupRows ? g.M / tt + hit : ceil_div(g.M, tt);
+        return tokens * ceil_div(g.N, wt) * (g.mode == kFp8GroupK ? g.groups : 1);
+    };
+    Fp8Plan p{256, false, 1, 0};
+    if (g.mode != kFp8GroupK && per <= 64) {
         p.swap = true;
-        p.cols = per <= 16 ? 16 : per <= 32 ? 32 : per <= 64 ? 64 : 128;
-    } else if (ceil_div(g.M, 128) * ceil_div(g.N, 256) * (g.mode == kFp8GroupK ? g.groups : 1) < g.num_sms) {
+        p.cols = per <= 16 ? 16 : per <= 32 ? 32 : 64;
+    } else if (g.mode != kFp8GroupK && per <= 128) {
+        p.swap = 2 * tiles_of(128, 128) < sms;
+        p.cols = p.swap ? 64 : 128;
+    } else if (4 * ceil_div(tiles_of(128, 256), sms) > 3 * ceil_div(tiles_of(128, 128), sms)) {
         p.cols = 128;
     }
-    const int tt = p.swap ? p.cols : 128, wt = p.swap ? 128 : p.cols;
-    const int64_t groups_hit = g.mode == kFp8GroupRows ? (g.groups < g.M ? g.groups : g.M) : 0;
-    int64_t tiles = (g.mode == kFp8GroupRows ? g.M / tt + groups_hit : ceil_div(g.M, tt)) * ceil_div(g.N, wt);
-    if (g.mode == kFp8GroupK) tiles *= g.groups;
+    const int64_t tiles = p.swap ? tiles_of(p.cols, 128) : tiles_of(128, p.cols);
     // Few tiles: clusters of 2, 4 or 8 CTAs share each tile's K blocks.
-    if (p.swap && p.cols <= 64)
-        while (p.split < 8 && tiles * p.split * 2 <= g.num_sms && nk >= p.split * 4) p.split *= 2;
-    const int64_t most = g.num_sms / p.split * p.split;
+    if (p.swap)
+        while (p.split < 8 && tiles * p.split * 2 <= sms && nk >= p.split * 4) p.split *= 2;
+    const int64_t most = sms / p.split * p.split;
     p.grid = tiles * p.split < most ? tiles * p.split : most;
     return p;
 }
@@ -990,7 +1024,6 @@ cudaError_t prepare_fp8()
 {
     cudaError_t e = prepare_cfg<Wide256>();
     if (e == cudaSuccess) e = prepare_cfg<Wide128>();
-    if (e == cudaSuccess) e = prepare_cfg<Swap128>();
     if (e == cudaSuccess) e = prepare_cfg<Swap64>();
     if (e == cudaSuccess) e = prepare_cfg<Swap32>();
     if (e == cudaSuccess) e = prepare_cfg<Swap16>();
@@ -1001,12 +1034,9 @@ cudaError_t launch_fp8(const Fp8Args &g, cudaStream_t stream)
 {
     const Fp8Plan p = plan_fp8(g);
     if (!p.swap) return p.cols == 256 ? launch_cfg<Wide256>(g, p, stream) : launch_cfg<Wide128>(g, p, stream);
-    switch (p.cols) {
-    case 16: return launch_cfg<Swap16>(g, p, stream);
-    case 32: return launch_cfg<Swap32>(g, p, stream);
-    case 64: return launch_cfg<Swap64>(g, p, stream);
-    default: return launch_cfg<Swap128>(g, p, stream);
-    }
+    return p.cols == 16   ? launch_cfg<Swap16>(g, p, stream)
+           : p.cols == 32 ? launch_cfg<Swap32>(g, p, stream)
+                          : launch_cfg<Swap64>(g, p, stream);
 }
 
 }  // namespace sgemm_gb300
