@@ -378,6 +378,13 @@ __device__ __forceinline__ float ld_shared_f32(uint32_t addr)
     return v;
 }
 
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ void st_shared_u32x4(uint32_t addr, uint4 v)
 {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -792,19 +799,38 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
                         }
                         return;
                     }
-#pragma unroll 8
-                    for (int i = 0; i < cols; ++i) {
-                        const int e = 32 * i + lane, r = e / cols, c = e % cols, byte = c * size;
-                        const uint32_t a = st + 128 * r + 16 * ((byte >> 4) ^ (r & 7)) + (byte & 15);
-                        if (row0 + r < w.a_end && col0 + c < p.N) {
-                            const int64_t at = c_base + (int64_t)(row0 + r) * p.ldc + col0 + c;
-                            if (cols == 64) {
-                                uint16_t x;
-                                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(a) : "memory");
-                                static_cast<uint16_t *>(p.C)[at] = x;
+                    // Rows that are not whole aligned pieces: lane by lane, eight
+                    // rows read before the first is stored.
+                    const int64_t at = c_base + (int64_t)row0 * p.ldc + col0;
+                    const int rows = w.a_end - row0;
+#pragma unroll 1
+                    for (int r0 = 0; r0 < 32; r0 += 8) {
+                        uint32_t x[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            x[i] = ld_shared_u32(st + 128 * (r0 + i) + 16 * ((lane >> 2) ^ i) + 4 * (lane & 3));
+                        if (cols == 32) {
+                            // Lane: column.
+                            if (p.beta == 0.0f) {
+                                float *c = static_cast<float *>(p.C) + at + r0 * p.ldc + lane;
+#pragma unroll
+                                for (int i = 0; i < 8; ++i, c += p.ldc)
+                                    if (r0 + i < rows && col0 + lane < p.N) *c = __uint_as_float(x[i]);
                             } else {
-                                store_c(p, at, ld_shared_f32(a));
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    if (r0 + i < rows && col0 + lane < p.N)
+                                        store_c(p, at + (r0 + i) * p.ldc + lane, __uint_as_float(x[i]));
                             }
+                        } else {
+                            // Lane: columns 2 lane and 2 lane + 1.
+                            uint16_t *c = static_cast<uint16_t *>(p.C) + at + r0 * p.ldc + 2 * lane;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i, c += p.ldc)
+                                if (r0 + i < rows) {
+                                    if (col0 + 2 * lane < p.N) c[0] = (uint16_t)x[i];
+                                    if (col0 + 2 * lane + 1 < p.N) c[1] = (uint16_t)(x[i] >> 16);
+                                }
                         }
                     }
                 };
