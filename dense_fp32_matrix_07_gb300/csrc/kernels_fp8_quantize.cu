@@ -62,11 +62,12 @@ struct Eight<float> {
     __device__ __forceinline__ float2 pair(int j) const { return make_float2(v[2 * j], v[2 * j + 1]); }
     // Magnitude bits of pair j, as one or two numbers packed for max_of().
     __device__ __forceinline__ uint2 mags(int j) const { return make_uint2(magnitude(v[2 * j]), magnitude(v[2 * j + 1])); }
-    static __device__ __forceinline__ uint2 max_of(uint2 a, uint2 b) { return make_uint2(umax(a.x, b.x), umax(a.y, b.y)); }
-    static __device__ __forceinline__ uint2 none() { return make_uint2(0, 0); }
+    static __device__ __forceinline__ uint2 max_of(uint2 a, uint2 b, uint2 c)
+    {
+        return make_uint2(__vimax3_u32(a.x, b.x, c.x), __vimax3_u32(a.y, b.y, c.y));
+    }
     static __device__ __forceinline__ uint32_t first(uint2 m) { return m.x; }
     static __device__ __forceinline__ uint32_t second(uint2 m) { return m.y; }
-    using Mags = uint2;
 };
 
 template <>
@@ -92,11 +93,9 @@ struct Eight<__nv_bfloat16> {
         return make_float2(__uint_as_float(v[j] << 16), __uint_as_float(v[j] & 0xffff0000u));
     }
     __device__ __forceinline__ uint32_t mags(int j) const { return v[j] & 0x7fff7fffu; }
-    static __device__ __forceinline__ uint32_t max_of(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
-    static __device__ __forceinline__ uint32_t none() { return 0; }
+    static __device__ __forceinline__ uint32_t max_of(uint32_t a, uint32_t b, uint32_t c) { return __vimax3_u16x2(a, b, c); }
     static __device__ __forceinline__ uint32_t first(uint32_t m) { return m << 16; }
     static __device__ __forceinline__ uint32_t second(uint32_t m) { return m & 0xffff0000u; }
-    using Mags = uint32_t;
 };
 
 // Values c .. c + 7 of a row of `cols`, zeros past its end.
@@ -117,7 +116,7 @@ __device__ __forceinline__ void load_row(const T *row, int64_t c, int64_t cols, 
 template <class T>
 __device__ __forceinline__ uint32_t max_of_eight(const Eight<T> &x)
 {
-    auto m = Eight<T>::max_of(Eight<T>::max_of(x.mags(0), x.mags(1)), Eight<T>::max_of(x.mags(2), x.mags(3)));
+    const auto last = x.mags(3), m = Eight<T>::max_of(Eight<T>::max_of(x.mags(0), x.mags(1), x.mags(2)), last, last);
     return umax(Eight<T>::first(m), Eight<T>::second(m));
 }
 
@@ -230,7 +229,7 @@ struct TileArgs {
 };
 
 template <class T, bool BLOCKS>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2)
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2)
 quantize_tiles_kernel(const TileArgs a)
 {
     __shared__ uint32_t red[8][128];
@@ -295,16 +294,28 @@ quantize_tiles_kernel(const TileArgs a)
         }
         const T *src = static_cast<const T *>(a.src) + e * a.stride_src;
         const int64_t c = cb * kBlock + 8 * x;
+        const int64_t ry = r0 + 8 * y;               // this thread's first row
+        const int n = (int)(r1 - ry);                // its rows: those below n
         Eight<T> v[8];
+        if (!a.gather && a.vec && c + 8 <= a.cols) {
+            const T *p = src + ry * a.ld + c;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int64_t r = r0 + 8 * y + i;
-            int64_t from = -1;
-            if (r < r1) from = a.gather ? (int64_t)a.gather[r] : r;
-            if (from >= 0 && from < a.src_rows)
-                load_row<T>(src + from * a.ld, c, a.cols, a.vec != 0, v[i]);
-            else
-                v[i].zero();
+            for (int i = 0; i < 8; ++i, p += a.ld) {
+                if (i < n)
+                    v[i].load(p);
+                else
+                    v[i].zero();
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                int64_t from = -1;
+                if (i < n) from = a.gather ? (int64_t)a.gather[ry + i] : ry + i;
+                if (from >= 0 && from < a.src_rows)
+                    load_row<T>(src + from * a.ld, c, a.cols, a.vec != 0, v[i]);
+                else
+                    v[i].zero();
+            }
         }
         if (!BLOCKS && a.q) {
             // Row form: a row's 128 columns are the 16 lanes of a half warp.
@@ -312,21 +323,24 @@ quantize_tiles_kernel(const TileArgs a)
 #pragma unroll
             for (int i = 0; i < 8; ++i) m[i] = max_of_eight(v[i]);
             const Scale s = scale_of(max_over_half<8>(m, lane));   // of row x / 2
-            if ((x & 1) == 0 && r0 + 8 * y + (x >> 1) < r1) a.scales[cb * a.lds + r0 + 8 * y + (x >> 1)] = s.scale;
+            if ((x & 1) == 0 && (x >> 1) < n) a.scales[cb * a.lds + ry + (x >> 1)] = s.scale;
+            uint8_t *q = a.q + ry * a.ldq + c;
+            const int nq = c < a.cols ? n : 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int64_t r = r0 + 8 * y + i;
+            for (int i = 0; i < 8; ++i, q += a.ldq) {
                 const float inv = __shfl_sync(0xffffffffu, s.inv, (lane & 16) | (2 * i));
-                if (r < r1 && c < a.cols) *reinterpret_cast<uint2 *>(a.q + r * a.ldq + c) = eight_bytes(v[i], inv);
+                if (i < nq) *reinterpret_cast<uint2 *>(q) = eight_bytes(v[i], inv);
             }
         }
         // Columns' (or the block's) largest magnitudes.
         uint32_t m[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            typename Eight<T>::Mags p = Eight<T>::none();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) p = Eight<T>::max_of(p, v[i].mags(j));
+            auto p = Eight<T>::max_of(v[0].mags(j), v[1].mags(j), v[2].mags(j));
+            p = Eight<T>::max_of(p, v[3].mags(j), v[4].mags(j));
+            p = Eight<T>::max_of(p, v[5].mags(j), v[6].mags(j));
+            const auto last = v[7].mags(j);
+            p = Eight<T>::max_of(p, last, last);
             m[2 * j] = Eight<T>::first(p);
             m[2 * j + 1] = Eight<T>::second(p);
         }
@@ -351,12 +365,11 @@ quantize_tiles_kernel(const TileArgs a)
                     a.scales_t[e * a.stride_st + cb * a.ldst + rb] = s.scale;
             }
             if (a.q) {
+                uint8_t *q = a.q + e * a.stride_q + ry * a.ldq + c;
+                const int nq = c < a.cols ? n : 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int64_t r = r0 + 8 * y + i;
-                    if (r < r1 && c < a.cols)
-                        *reinterpret_cast<uint2 *>(a.q + e * a.stride_q + r * a.ldq + c) = eight_bytes(v[i], s.inv);
-                }
+                for (int i = 0; i < 8; ++i, q += a.ldq)
+                    if (i < nq) *reinterpret_cast<uint2 *>(q) = eight_bytes(v[i], s.inv);
                 continue;
             }
         } else {
@@ -397,14 +410,20 @@ quantize_tiles_kernel(const TileArgs a)
         }
         __syncthreads();
         const int64_t end = BLOCKS ? a.rows : a.row_blocks * kBlock;   // length of a transposed row
+        {
+            // This thread: piece threadIdx.x % 8 of columns threadIdx.x / 8 + 32 i.
+            const int piece = threadIdx.x & 7, col0 = threadIdx.x >> 3;
+            const int64_t r = rb * kBlock + 16 * piece;
+            const int left = r < end ? (int)(a.cols - cb * kBlock < kBlock ? a.cols - cb * kBlock : kBlock) - col0 : 0;
+            uint8_t *q = a.qt + e * a.stride_qt + (cb * kBlock + col0) * a.ldqt + r;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int n = threadIdx.x + 256 * i, col = n >> 3, piece = n & 7, cx = col >> 3;
-            // Pieces 2p and 2p + 1 of the column lie side by side, swapped for odd cx.
-            uint4 o = turned[col * 8 + (piece ^ (cx >> 1))];
-            if (cx & 1) o = make_uint4(o.z, o.w, o.x, o.y);
-            const int64_t cc = cb * kBlock + col, r = rb * kBlock + 16 * piece;
-            if (cc < a.cols && r < end) *reinterpret_cast<uint4 *>(a.qt + e * a.stride_qt + cc * a.ldqt + r) = o;
+            for (int i = 0; i < 4; ++i, q += 32 * a.ldqt) {
+                const int col = col0 + 32 * i, cx = col >> 3;
+                // Pieces 2p and 2p + 1 of the column lie side by side, swapped for odd cx.
+                uint4 o = turned[col * 8 + (piece ^ (cx >> 1))];
+                if (cx & 1) o = make_uint4(o.z, o.w, o.x, o.y);
+                if (32 * i < left) *reinterpret_cast<uint4 *>(q) = o;
+            }
         }
         __syncthreads();
     }
@@ -425,7 +444,7 @@ cudaError_t launch_tiles(TileArgs &a, int num_sms, cudaStream_t stream)
     a.vec = vec_ok(static_cast<const T *>(a.src), a.ld, a.batch > 1 ? a.stride_src : 0);
     // Tiles are counted in 32 bits (2^31 of them would be 2^45 values).
     if ((__int128)a.row_blocks * a.col_blocks * a.batch > INT32_MAX) return cudaErrorInvalidValue;
-    const int64_t tiles = a.row_blocks * a.col_blocks * a.batch, most = (int64_t)num_sms * (sizeof(T) == 2 ? 3 : 2);
+    const int64_t tiles = a.row_blocks * a.col_blocks * a.batch, most = (int64_t)num_sms * (sizeof(T) == 2 ? 4 : 2);
     quantize_tiles_kernel<T, BLOCKS><<<(unsigned)(tiles < most ? tiles : most), 256, 0, stream>>>(a);
     return cudaGetLastError();
 }
