@@ -63,6 +63,8 @@ class SgemmError(RuntimeError):
 def load(rebuild: bool = False):
     """Build (if needed) and load the library; raises if either fails."""
     global _lib
+    if _lib is not None and not rebuild:
+        return _lib
     with _lock:
         if _lib is None or rebuild:
             path = _build.build(force=rebuild)
