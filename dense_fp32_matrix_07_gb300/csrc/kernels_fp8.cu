@@ -15,11 +15,14 @@
 //               block (128-byte swizzle), full/empty barrier per stage;
 //   warp 1      TMEM owner and MMA issuer: 4 MMAs (K 32 each) per block into
 //               one of NBUF accumulators, then a commit that frees the stage
-//               and one that hands the accumulator on;
-//   warps 2, 3  scales: asynchronous 4-byte copies into a ring of their own,
-//               since rows of scales start at any address;
+//               and hands the accumulator on;
+//   warps 2, 3  scales of the accumulator's columns, where each has its own:
+//               asynchronous 4-byte copies into a ring, since rows of scales
+//               start at any address;
 //   warps 4..   promotion and epilogue: warp 4 + i reads lanes 32 (i % 4) ..
-//               of accumulator columns (i / 4) * CW ..
+//               of accumulator columns (i / 4) * CW ..; its lanes' scales (and
+//               the one that its columns share) it fetches itself, two K
+//               blocks ahead (through the ring they cost 165 cycles a block).
 //
 // The 128 lanes of tensor memory hold rows of A and the columns rows of B
 // ("wide"), or, where there are few rows of A, the other way round ("swap"):
@@ -71,10 +74,10 @@ struct Fp8Cfg {
     static constexpr int THREADS = 128 + 32 * EPI_WARPS;
     // Registers move from the first four warps to the eight that hold up to
     // 128 sums per thread: 168 * 384 at launch, 72 * 128 + 216 * 256 (or
-    // 104 * 128 + 200 * 256) after.
-    static constexpr int EPI_REGS = BN == 256 ? 216 : BN == 128 ? 200 : 0;
+    // 88 * 128 + 208 * 256) after.
+    static constexpr int EPI_REGS = BN == 256 ? 216 : BN == 128 ? 208 : 0;
     static constexpr int SDEPTH = BN == 256 ? 4 : 6;         // ring of scales
-    static constexpr int SLOT = kScaleBatch * (128 + BN);    // floats of one slot
+    static constexpr int SLOT = kScaleBatch * BN;            // floats of one slot
     static constexpr bool CAN_SPLIT = SWAP && BN <= 64;
     static constexpr int STAGING = SWAP ? 0 : EPI_WARPS * kStaging;
     static constexpr int PARTIAL = CAN_SPLIT ? BN * 128 * 4 : 0;
@@ -403,9 +406,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// ROWS_FORM: B's scales are per row. LANES_SCALED: every lane of the
-// accumulator has a scale of its own, else all share one; COLS_SCALED: the
-// same of the columns (shared: by the CW columns of a warp).
+// ROWS_FORM: B's scales are per row. COLS_SCALED: every column of the
+// accumulator has a scale of its own, else the CW columns of a warp share one.
 template <class Cfg, bool ROWS_FORM>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
 fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_constant__ CUtensorMap mapQ,
@@ -414,7 +416,6 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
     constexpr int BN = Cfg::BN, STAGES = Cfg::STAGES, NBUF = Cfg::NBUF, SD = Cfg::SDEPTH, CW = Cfg::CW;
     constexpr int CHUNK = Cfg::CHUNK;
     constexpr bool SWAP = Cfg::SWAP;
-    constexpr bool LANES_SCALED = ROWS_FORM || !SWAP;
     constexpr bool COLS_SCALED = ROWS_FORM || SWAP;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
@@ -510,7 +511,7 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
     if (split > 1 && tiles > t_step) tiles = t_step;   // a split grid has one tile per cluster
 
     if constexpr (Cfg::EPI_REGS > 0) {
-        if (warp < 4) ptx::setmaxnreg_dec<BN == 256 ? 72 : 104>();
+        if (warp < 4) ptx::setmaxnreg_dec<BN == 256 ? 72 : 88>();
     }
     if (warp == 0) {
         // ------------------------------ TMA producer ------------------------------
@@ -554,9 +555,8 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
             const Fp8Item w = fp8_item<Cfg>(p, table, t, rank);
             for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
                 const int s = (int)(it % STAGES), b = (int)(it % NBUF);
-                if (!__builtin_expect(__all_sync(0xffffffffu, early) != 0, 1) &&
-                    (!ptx::wait_phase_warp(acce_bar(b), ((it / NBUF) & 1) ^ 1) ||
-                     !ptx::wait_phase_warp(full_bar(s), (it / STAGES) & 1))) {
+                const uint32_t full = (it / STAGES) & 1, free = ((it / NBUF) & 1) ^ 1, next = it + 1;
+                if (!FP8_WAIT(mbar_test(full_bar(s), full), full_bar(s), full) || !FP8_WAIT(early, acce_bar(b), free)) {
                     if (lane == 0) atomicOr(p.status, kStatusTimeout);
                     ok = false;
                     break;
@@ -569,9 +569,7 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
                 for (int ks = 0; ks < 4; ++ks)
                     mma_f8_if(on, d, desc_p + off + 2 * ks, desc_q + off + 2 * ks, idesc, ks != 0 ? 1u : 0u);
                 mma_commit_if(on, done_bar(s));
-                const uint32_t next = it + 1;
-                early = mbar_test(acce_bar((int)(next % NBUF)), ((next / NBUF) & 1) ^ 1) &
-                        mbar_test(full_bar((int)(next % STAGES)), (next / STAGES) & 1);
+                early = mbar_test(acce_bar((int)(next % NBUF)), ((next / NBUF) & 1) ^ 1);
             }
         }
         // Everything issued finishes before TMEM is released.
@@ -579,16 +577,15 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
         if (!ptx::wait_phase_warp(drain_bar, 0) && lane == 0) atomicOr(p.status, kStatusTimeout);
     } else if (warp < 4) {
         // ------------------------------ scales ------------------------------
-        // A slot holds the scales of up to kScaleBatch K blocks of one tile:
-        // 128 per block for the lanes (or the first alone where they share
-        // one), then BN per block for the columns (or one per 128 of them).
+        // A slot holds BN scales for each of up to kScaleBatch K blocks of a tile.
         const int th = threadIdx.x - 64;
         uint32_t it = 0;
-        bool ok = true;
+        bool ok = COLS_SCALED;
         for (uint32_t t = t_first; ok && t < tiles; t += t_step) {
             const Fp8Item w = fp8_item<Cfg>(p, table, t, rank);
-            const float *sbg = p.sb + (p.mode == kFp8GroupRows ? w.group * p.stride_sb : 0);
-            constexpr int ta = SWAP ? BN : 128, tb = SWAP ? 128 : BN;
+            const float *src = SWAP ? p.sa : p.sb;
+            const int64_t ld = SWAP ? p.ld_sa : p.ld_sb;
+            const int first = SWAP ? w.a_row : w.b_row, end = SWAP ? w.a_end : p.N;
             for (int k0 = w.kb0; k0 < w.kb1; k0 += kScaleBatch, ++it) {
                 const int s = (int)(it % SD);
                 if (!ptx::wait_phase_warp(sempty_bar(s), ((it / SD) & 1) ^ 1)) {
@@ -597,28 +594,14 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
                     break;
                 }
                 const uint32_t slot = base + Cfg::OFF_SCALES + s * (Cfg::SLOT * 4);
-                const int blocks = w.kb1 - k0 < kScaleBatch ? w.kb1 - k0 : kScaleBatch;
-                for (int j = 0; j < blocks; ++j) {
-                    const int kb = k0 + j;
-                    const uint32_t lanes_at = slot + 4 * (128 * j), cols_at = slot + 4 * (kScaleBatch * 128 + BN * j);
-                    const uint32_t a_at = SWAP ? cols_at : lanes_at, b_at = SWAP ? lanes_at : cols_at;
-                    const float *sa = p.sa + (int64_t)kb * p.ld_sa;
 #pragma unroll
-                    for (int i = th; i < ta; i += 64) {
-                        const bool there = w.a_row + i < w.a_end;
-                        cp_async_4(a_at + 4 * i, there ? sa + w.a_row + i : p.sa, there);
-                    }
-                    if constexpr (ROWS_FORM) {
-                        const float *sb = p.sb + (int64_t)kb * p.ld_sb;
+                for (int j = 0; j < kScaleBatch; ++j) {
+                    if (k0 + j >= w.kb1) break;
+                    const float *sk = src + (int64_t)(k0 + j) * ld;
 #pragma unroll
-                        for (int i = th; i < tb; i += 64) {
-                            const bool there = w.b_row + i < p.N;
-                            cp_async_4(b_at + 4 * i, there ? sb + w.b_row + i : p.sb, there);
-                        }
-                    } else if (th < (tb + 127) / 128) {
-                        const int row = w.b_row + 128 * th;
-                        const bool there = row < p.N;
-                        cp_async_4(b_at + 4 * th, there ? sbg + (int64_t)(row / 128) * p.ld_sb + kb : p.sb, there);
+                    for (int i = th; i < BN; i += 64) {
+                        const bool there = first + i < end;
+                        cp_async_4(slot + 4 * (BN * j + i), there ? sk + first + i : src, there);
                     }
                 }
                 cp_async_arrive(sfull_bar(s));
@@ -635,8 +618,52 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
         if constexpr (Cfg::EPI_REGS > 0) ptx::setmaxnreg_inc<Cfg::EPI_REGS>();
         uint32_t it = 0, batch = 0;
         bool ok = true;
-        for (uint32_t t = t_first; ok && t < tiles; t += t_step) {
+        // Where the next K block's scales are: this lane's, and the one that
+        // this warp's columns share. Past a tile's last block the place stays,
+        // and rows that are not stored read the last one's: loads without
+        // conditions, hence without branches.
+        const float *lane_at = p.sa, *cols_at = p.sb;
+        float lane_next[kScaleBatch], cols_next[kScaleBatch];
+        const int64_t lane_step = !SWAP ? p.ld_sa : ROWS_FORM ? p.ld_sb : 1;
+        auto fetch = [&](int kb, int kb1) {
+#pragma unroll
+            for (int j = 0; j < kScaleBatch; ++j) {
+                lane_next[j] = __ldg(lane_at);
+                if constexpr (!COLS_SCALED) cols_next[j] = __ldg(cols_at);
+                const bool last = kb + j + 1 >= kb1;
+                lane_at += last ? 0 : lane_step;
+                if constexpr (!COLS_SCALED) cols_at += last ? 0 : 1;
+            }
+        };
+        auto start = [&](const Fp8Item &w) {
+            if (w.kb0 >= w.kb1) return;
+            const float *sbg = p.sb + (p.mode == kFp8GroupRows ? w.group * p.stride_sb : 0);
+            if constexpr (!SWAP) {
+                lane_at = p.sa + (int64_t)w.kb0 * p.ld_sa + (w.a_row + row < w.a_end ? w.a_row + row : w.a_end - 1);
+            } else if constexpr (ROWS_FORM) {
+                lane_at = p.sb + (int64_t)w.kb0 * p.ld_sb + (w.b_row + row < p.N ? w.b_row + row : p.N - 1);
+            } else {
+                lane_at = sbg + (int64_t)(w.b_row / 128) * p.ld_sb + w.kb0;
+            }
+            if constexpr (!COLS_SCALED) {
+                const int col = w.b_row + half * CW;
+                cols_at = sbg + (int64_t)((col < p.N ? col : p.N - 1) / 128) * p.ld_sb + w.kb0;
+            }
+            fetch(w.kb0, w.kb1);
+        };
+        // Of a tile the sums' loop keeps its K blocks alone: the store decodes
+        // it again. (Registers: what the store needs, kept through the loop,
+        // spills there and costs a quarter of its speed.)
+        int kb0 = 0, kb1 = 0;
+        auto enter = [&](uint32_t t) {
+            if (t >= tiles) return;
             const Fp8Item w = fp8_item<Cfg>(p, table, t, rank);
+            start(w);
+            kb0 = w.kb0;
+            kb1 = w.kb1;
+        };
+        enter(t_first);
+        for (uint32_t t = t_first; ok && t < tiles; t += t_step) {
             float2 acc[CW / 2];
 #pragma unroll
             for (int j = 0; j < CW / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
@@ -644,34 +671,23 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
             // the next block's first chunk is requested before this block's
             // last one is added.
             uint32_t v[2][CHUNK];
-            float fl = 0.0f, fl_next = 0.0f;
-            const float *cols = nullptr, *cols_next = nullptr;
+            float fl[kScaleBatch] = {};
+            const float *cols = nullptr;                  // the batch's slot, this warp's columns
             // Waits for block i's sums and requests their first chunk.
             auto begin = [&](uint32_t i, uint32_t early, uint32_t (&dst)[CHUNK]) {
                 ok = ok && FP8_WAIT(early, done_bar((int)(i % STAGES)), (i / STAGES) & 1);
                 ptx::tc_fence_after();
                 tmem_ld_chunk<CHUNK>(lanes + (uint32_t)((int)(i % NBUF) * BN), dst);
             };
-            auto batch_test = [&](uint32_t bt) { return mbar_test(sfull_bar((int)(bt % SD)), (bt / SD) & 1); };
-            auto batch_wait = [&](uint32_t bt, uint32_t early) {
-                ok = ok && FP8_WAIT(early, sfull_bar((int)(bt % SD)), (bt / SD) & 1);
-            };
-            // Scales of K block j of a batch: the lane's, and the columns' place.
-            auto scales_of = [&](uint32_t bt, int j, float &f, const float *&at) {
-                const float *slot = slots + (int)(bt % SD) * Cfg::SLOT;
-                at = slot + kScaleBatch * 128 + BN * j + half * CW;
-                f = slot[128 * j + (LANES_SCALED ? row : 0)];
-                if constexpr (!COLS_SCALED) f *= slot[kScaleBatch * 128 + BN * j + (half * CW) / 128];
-            };
-            auto add = [&](int c0, const uint32_t (&x)[CHUNK]) {
-                const float2 f2 = make_float2(fl, fl);
+            auto add = [&](int j0, int c0, const uint32_t (&x)[CHUNK]) {
+                const float2 f2 = make_float2(fl[j0], fl[j0]);
 #pragma unroll
                 for (int j = 0; j < CHUNK; j += 4) {
                     const float2 v0 = make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
                     const float2 v1 = make_float2(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
                     float2 &a0 = acc[(c0 + j) / 2], &a1 = acc[(c0 + j) / 2 + 1];
                     if constexpr (COLS_SCALED) {
-                        const float4 sc = *reinterpret_cast<const float4 *>(cols + c0 + j);
+                        const float4 sc = *reinterpret_cast<const float4 *>(cols + BN * j0 + c0 + j);
                         a0 = __ffma2_rn(__fmul2_rn(v0, f2), make_float2(sc.x, sc.y), a0);
                         a1 = __ffma2_rn(__fmul2_rn(v1, f2), make_float2(sc.z, sc.w), a1);
                     } else {
@@ -685,56 +701,58 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
             // and requests the first chunk of the block after it, if any.
             auto block = [&](auto J, bool more) {
                 constexpr int j = decltype(J)::value;
-                constexpr bool turn = j + 1 == kScaleBatch;   // the next block is another batch's
                 const int b = (int)(it % NBUF);
                 const uint32_t next = it + 1;
-                uint32_t early = 0, early_scales = 0;
+                uint32_t early = 0;
 #pragma unroll
                 for (int c = 0; c < NCH; ++c) {
                     const int at = NCH == 1 ? j & 1 : c & 1;
                     tmem_ld_wait_for<CHUNK>(v[at]);
                     if (c + 1 < NCH) tmem_ld_chunk<CHUNK>(lanes + (uint32_t)(b * BN + (c + 1) * CHUNK), v[at ^ 1]);
-                    if (c == 0) {
-                        early = mbar_test(done_bar((int)(next % STAGES)), (next / STAGES) & 1);
-                        if (turn) early_scales = batch_test(batch + 1);
-                    }
+                    if (c == 0) early = mbar_test(done_bar((int)(next % STAGES)), (next / STAGES) & 1);
                     if (c + 1 == NCH) {
                         // The accumulator is read: the MMA warp may reuse it.
                         ptx::tc_fence_before();
                         mbar_arrive_if(lane == 0, acce_bar(b));
-                        if (more) {
-                            if (turn) batch_wait(batch + 1, early_scales);
-                            scales_of(turn ? batch + 1 : batch, turn ? 0 : j + 1, fl_next, cols_next);
-                            begin(next, early, v[at ^ 1]);
-                        }
+                        if (more) begin(next, early, v[at ^ 1]);
                     }
-                    add(c * CHUNK, v[at]);
+                    add(j, c * CHUNK, v[at]);
                 }
-                fl = fl_next;
-                cols = cols_next;
                 ++it;
             };
             static_assert((NCH == 1 || NCH % 2 == 0) && kScaleBatch == 2, "chunks alternate between two buffers");
             using std::integral_constant;
-            if (w.kb0 < w.kb1) {
-                batch_wait(batch, batch_test(batch));
-                scales_of(batch, 0, fl, cols);
-                begin(it, 0, v[0]);
-            }
-            for (int kb = w.kb0; ok && kb < w.kb1; kb += kScaleBatch) {
-                const int left = w.kb1 - kb;
+            if (kb0 < kb1) begin(it, mbar_test(done_bar((int)(it % STAGES)), (it / STAGES) & 1), v[0]);
+            for (int kb = kb0; ok && kb < kb1; kb += kScaleBatch) {
+                const int left = kb1 - kb;
+#pragma unroll
+                for (int j = 0; j < kScaleBatch; ++j) fl[j] = COLS_SCALED ? lane_next[j] : lane_next[j] * cols_next[j];
+                fetch(kb + kScaleBatch, kb1);
+                if constexpr (COLS_SCALED) {
+                    const int s = (int)(batch % SD);
+                    const uint32_t phase = (batch / SD) & 1;
+                    ok = ok && FP8_WAIT(mbar_test(sfull_bar(s), phase), sfull_bar(s), phase);
+                    cols = slots + s * Cfg::SLOT + half * CW;
+                }
                 if (left >= kScaleBatch) {
                     block(integral_constant<int, 0>{}, true);
                     block(integral_constant<int, 1>{}, left > kScaleBatch);
                 } else {
                     block(integral_constant<int, 0>{}, false);
                 }
-                __syncwarp();
-                mbar_arrive_if(lane == 0, sempty_bar((int)(batch % SD)));
-                ++batch;
+                if constexpr (COLS_SCALED) {
+                    __syncwarp();
+                    mbar_arrive_if(lane == 0, sempty_bar((int)(batch % SD)));
+                    ++batch;
+                }
             }
             if (!ok && lane == 0) atomicOr(p.status, kStatusTimeout);
             if (!ok && split == 1) break;
+            // The next tile's first scales are on their way while this one is stored.
+            enter(t + t_step);
+            uint32_t stored = t;
+            asm volatile("" : "+r"(stored));              // not to be kept from before the loop
+            const Fp8Item w = fp8_item<Cfg>(p, table, stored, rank);
             const int64_t c_base = p.mode == kFp8GroupK ? w.group * p.stride_c : 0;
             if constexpr (SWAP) {
                 // Lane = row of B (column of C), column = row of A.
