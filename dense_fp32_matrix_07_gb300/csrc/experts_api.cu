@@ -10,6 +10,9 @@ namespace {
 
 // Largest row, column or token count: tile arithmetic stays below 2^31.
 constexpr int64_t kMaxSize = (int64_t(1) << 31) - 1024;
+// Most columns of a row quantised by sgemm_fp8_quantize_rows() or summed by
+// sgemm_combine(): a grid has 65535 blocks of 256 along its second dimension.
+constexpr int64_t kMaxCols = 65535 * 256;
 
 bool bad_size(int64_t n) { return n < 0; }
 bool too_large(int64_t n) { return n > kMaxSize; }
@@ -91,7 +94,7 @@ int sgemm_fp8_quantize_rows(int64_t rows, int64_t cols, const void *src, int typ
     if (ld < cols || lds < rows || !scales || bad_fp8(q, ldq, cols)) return SGEMM_ERR_INVALID_VALUE;
     if (!gather && src_rows < rows) return SGEMM_ERR_INVALID_VALUE;
     if (!src && src_rows > 0) return SGEMM_ERR_INVALID_VALUE;
-    if (too_large(rows) || too_large(cols) || too_large(src_rows)) return SGEMM_ERR_OVERFLOW;
+    if (too_large(rows) || cols > kMaxCols || too_large(src_rows)) return SGEMM_ERR_OVERFLOW;
     const Region out[] = {{q, span(rows, cols, ldq, 1)}, {scales, span(ceil_div(cols, kBlock), rows, lds, 4)}};
     const Region in[] = {{src, span(src_rows, cols, ld, type_size(type))}, {gather, gather ? rows * 4 : 0}};
     int rc = check_regions(out, in);
@@ -378,7 +381,7 @@ int sgemm_combine(int64_t T, int k, int64_t cols, int64_t rows, const void *Y, i
         return SGEMM_ERR_INVALID_VALUE;
     if (T == 0 || cols == 0) return SGEMM_OK;
     if ((!Y && rows > 0) || !row_of || !out || ldy < cols || ld_out < cols) return SGEMM_ERR_INVALID_VALUE;
-    if (too_large(T) || too_large(cols) || too_large(rows)) return SGEMM_ERR_OVERFLOW;
+    if (too_large(T) || cols > kMaxCols || too_large(rows)) return SGEMM_ERR_OVERFLOW;
     const int64_t size = type_size(type);
     const Region o[] = {{out, span(T, cols, ld_out, size)}};
     const Region in[] = {{Y, span(rows, cols, ldy, size)}, {row_of, span(T, k, k, 4)}, {weights, weights ? span(T, k, k, 4) : 0}};

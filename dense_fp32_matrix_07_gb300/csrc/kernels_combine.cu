@@ -5,7 +5,11 @@
 //
 // Without weights (w = 1) the sum is also the gradient of gathering rows for
 // their experts. A slot whose row is outside [0, rows) adds nothing. Sums are
-// in FP32, in slot order. Bound by memory: Y, out and dout once.
+// in FP32, in slot order. Bound by memory: Y, out and dout once. Measured on
+// one GB300, 8191 tokens of 6 rows of 2048 bfloat16: the sum 42.5 us (5.5
+// TB/s), its gradients 78 us (5.6 TB/s). Requesting four or eight rows before
+// the first is added took 72 us and more; two rows at a time in the gradients
+// changed nothing.
 #include "experts.cuh"
 
 namespace sgemm_gb300 {
@@ -18,7 +22,8 @@ struct alignas(sizeof(T) * N) Pack {
     T v[N];
 };
 
-// One thread per N columns of a token: blockDim.x columns' threads, blockDim.y tokens.
+// One thread per N columns of a token: blockDim.x columns' threads, blockDim.y
+// tokens (16 tokens of a decode step: 6 us, launch and one chain of loads).
 template <class T, int N>
 __global__ void __launch_bounds__(256)
 combine_kernel(int64_t tokens, int k, int64_t cols, int64_t rows, const T *__restrict__ Y, int64_t ldy,

@@ -42,6 +42,22 @@
 //
 // Every wait is bounded; a role that gives up sets the device error word and
 // goes to the teardown, which drains copies and MMAs.
+//
+// What bounds it, and what it measured (one GB300):
+//   16384 x 4096 x 4096, blocks form: 225 us, 2.44 PFLOP/s, 1.28 times the
+//   measured bf16 rate. MMAs alone would take 512 cycles a K block (N = 256)
+//   and run beside the reads of tensor memory at full rate; a round through
+//   commit, barrier, read, add and release takes about 1450, of which two
+//   accumulators hide half. 4096 x 4096 x 4096 with scales per row of both
+//   operands: 99 us (two operations per element and a read of the columns'
+//   scales from shared memory).
+//   16 x 4096 x 4096: 10.1 us, most of it launch, set-up and the two
+//   barriers of a split tile; 48 experts of 2048 x 2048 on 2 rows each:
+//   38.8 us, 5.2 TB/s of weights.
+// Not taken: pairs of CTAs on 256 x 256 tiles (cta_group::2; 433 us: the
+// round goes through two SMs), two accumulators of 128 columns with barriers
+// of their own (285 us), waits that poll without a pause (241 to 304 us: they
+// take issue slots from the warps that add).
 #include "common.cuh"
 #include "experts.cuh"
 #include "ptx.cuh"
@@ -65,12 +81,14 @@ struct Fp8Cfg {
     static constexpr int P_TILE = 128 * ROW_BYTES;           // lanes' operand
     static constexpr int Q_TILE = BN * ROW_BYTES;            // columns' operand
     static constexpr int STAGE_BYTES = P_TILE + Q_TILE;
-    static constexpr int STAGES = BN == 256 ? 3 : BN == 128 ? 5 : 7;
+    static constexpr int STAGES = BN == 256 ? 3 : BN == 128 ? 5 : 7;   // 3 or 4 of 48 KB: the same time
     static constexpr int NBUF = BN == 256 ? 2 : 4;           // accumulators in tensor memory
     static constexpr int TMEM_COLS = NBUF * BN < 32 ? 32 : NBUF * BN;
     static constexpr int EPI_WARPS = BN >= 128 ? 8 : 4;
     static constexpr int CW = BN / (EPI_WARPS / 4);          // columns per epilogue warp
-    static constexpr int CHUNK = CW < 32 || BN == 256 ? 16 : 32;   // columns per tcgen05.ld
+    // Columns per tcgen05.ld, of which two are in flight: 32 of them beside
+    // 128 sums spill (302 us against 240 for 16 at 16384 x 4096 x 4096).
+    static constexpr int CHUNK = CW < 32 || BN == 256 ? 16 : 32;
     static constexpr int THREADS = 128 + 32 * EPI_WARPS;
     // Registers move from the first four warps to the eight that hold up to
     // 128 sums per thread: 168 * 384 at launch, 72 * 128 + 216 * 256 (or
@@ -78,7 +96,7 @@ struct Fp8Cfg {
     static constexpr int EPI_REGS = BN == 256 ? 216 : BN == 128 ? 208 : 0;
     static constexpr int SDEPTH = BN == 256 ? 4 : 6;         // ring of scales
     static constexpr int SLOT = kScaleBatch * BN;            // floats of one slot
-    static constexpr bool CAN_SPLIT = SWAP && BN <= 64;
+    static constexpr bool CAN_SPLIT = SWAP;
     static constexpr int STAGING = SWAP ? 0 : EPI_WARPS * kStaging;
     static constexpr int PARTIAL = CAN_SPLIT ? BN * 128 * 4 : 0;
     static constexpr int NUM_BARS = 2 * STAGES + NBUF + 2 * SDEPTH + 1;

@@ -6,8 +6,12 @@
 //
 // A block with a NaN gets a NaN scale and NaN values; one with an infinity an
 // infinite scale, zeros for its finite values and NaN for the infinity.
-// All forms are bound by memory: each value is read once and written as one
-// byte per form.
+// Each value is read once and written as one byte per form. Measured on one
+// GB300: 16383 x 4096 bfloat16 values along rows 36.4 us (5.5 TB/s: memory);
+// along rows and, transposed, along 16 groups of rows 55 us (5.0 TB/s),
+// bound by instructions as much as by memory (about 700 per warp and tile:
+// conversions, and two products, two maxima per value); 8192 x 4096 in 128 x
+// 128 blocks and their transposes 40 us for the two calls.
 #include "experts.cuh"
 
 #include <cuda_fp8.h>

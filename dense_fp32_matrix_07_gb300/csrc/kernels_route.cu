@@ -17,8 +17,7 @@ namespace sgemm_gb300 {
 
 namespace {
 
-// Floats as unsigned integers in the same order; every number above
-// -infinity maps above kNoKey.
+// Floats as unsigned integers in the same order; every number maps above 0.
 __device__ __forceinline__ uint32_t ordered(float x)
 {
     const uint32_t b = __float_as_uint(x);
@@ -245,7 +244,9 @@ route_kernel(int64_t tokens, int E, const T *__restrict__ logits, int64_t ld, in
 //   sigmoid:               dl_j = c g_j s_j (1 - s_j)
 // with 1 - s taken as sigmoid(-l), which keeps its digits where s is near 1.
 // Only the second needs the whole row of logits; the others read the chosen
-// ones and write a row of zeros with k values in it.
+// ones and write a row of zeros with k values in it. One warp per token;
+// bound by instructions and the latency of its three dependent loads (16383
+// tokens of 128 experts: 7.0 us, 1.2 us of bytes).
 template <class T>
 __device__ __forceinline__ void zero_row(T *out, int E, int vec, int lane)
 {
@@ -338,7 +339,10 @@ route_backward_kernel(int64_t tokens, int E, const T *__restrict__ logits, int64
 // blocks are one cluster, which reads its neighbours' counts from their shared
 // memory: one launch, no scratch. Beyond that 128 blocks run behind a launch
 // that leaves every block's counts in scratch: what bounds large sorts is the
-// scattered writes of token_of, about one a cycle and SM.
+// scattered writes of token_of, about one a cycle and SM. Measured: 48 pairs
+// 5.4 us; 131064 pairs of 128 experts 12.6 us (128 blocks behind a counting
+// launch: 12.4 us in two launches and an allocation, which cost the host more
+// than the first; 8 blocks: 18 us).
 constexpr int kDispatchThreads = 1024, kDispatchWarps = 32, kDispatchHeld = 8, kDispatchCluster = 16;
 constexpr int64_t kDispatchRun = 32 * kDispatchWarps * kDispatchHeld;   // pairs a block can hold in registers
 

@@ -11,6 +11,9 @@
  * depends on the order in which threads run: the same inputs give the same
  * bits. Only sgemm_dispatch() takes scratch (from the library's pool).
  *
+ * Sizes go up to 2^31 - 1024 (sgemm_fp8_quantize_rows() and sgemm_combine():
+ * 2^24 - 256 columns); larger ones return SGEMM_ERR_OVERFLOW.
+ *
  * Types of matrices: SGEMM_F32 (float), SGEMM_BF16 (bfloat16). Row-major, any
  * leading dimension and alignment, except the 8-bit ones: q, A and B lie on
  * 16-byte boundaries with leading dimensions (and batch strides) that are

@@ -41,7 +41,7 @@ ROWS = dict(rows=10, cols=200, src=P[0], type=BF16, ld=200, gather=0, src_rows=1
     (dict(q=0), BAD), (dict(q=P[1] + 8), BAD), (dict(ldq=200), BAD), (dict(ldq=192), BAD), (dict(scales=0), BAD),
     (dict(lds=9), BAD), (dict(src_rows=9), BAD), (dict(q=P[0]), BAD), (dict(scales=P[1]), BAD),
     (dict(rows=2 ** 31, src_rows=2 ** 31, lds=2 ** 31), OVER), (dict(ld=2 ** 62), OVER),
-    (dict(rows=0), OK), (dict(cols=0), OK),
+    (dict(cols=2 ** 24, ld=2 ** 24, ldq=2 ** 24), OVER), (dict(rows=0), OK), (dict(cols=0), OK),
 ])
 def test_quantize_rows_refusals(change, code):
     assert call("sgemm_fp8_quantize_rows", ROWS, **change) == code
@@ -160,6 +160,7 @@ COMBINE = dict(T=10, k=6, cols=64, rows=60, Y=P[0], type=BF16, ldy=64, row_of=P[
 @pytest.mark.parametrize("change,code", [
     (dict(k=0), BAD), (dict(k=33), BAD), (dict(Y=0), BAD), (dict(row_of=0), BAD), (dict(out=0), BAD), (dict(ldy=63), BAD),
     (dict(ld_out=63), BAD), (dict(out=P[0]), BAD), (dict(rows=-1), BAD), (dict(T=0), OK), (dict(cols=0), OK),
+    (dict(cols=2 ** 24, ldy=2 ** 24, ld_out=2 ** 24), OVER),
 ])
 def test_combine_refusals(change, code):
     assert call("sgemm_combine", COMBINE, **change) == code
@@ -186,6 +187,12 @@ def test_plan_refusals_and_empty():
 
 
 def test_plan_puts_few_rows_on_the_columns():
+    # 65 to 128 rows: split tiles of 64 columns while 128 x 128 ones would leave half the SMs idle.
+    assert sg.sgemm_fp8_plan(sg.SGEMM_FP8_DENSE, 1, 128, 4096, 4096, 152)[1:4] == (64, 1, 2)
+    assert sg.sgemm_fp8_plan(sg.SGEMM_FP8_DENSE, 1, 128, 16384, 4096, 152)[1:4] == (128, 0, 1)
+    # More: by waves of CTAs (1024 rows: one wave of 256-column tiles; 512 rows: one of either).
+    assert sg.sgemm_fp8_plan(sg.SGEMM_FP8_DENSE, 1, 1024, 4096, 4096, 152)[1:3] == (256, 0)
+    assert sg.sgemm_fp8_plan(sg.SGEMM_FP8_DENSE, 1, 512, 4096, 4096, 152)[1:3] == (128, 0)
     for M, cols in ((1, 16), (16, 16), (17, 32), (33, 64)):
         rc, c, swap, split, grid = sg.sgemm_fp8_plan(sg.SGEMM_FP8_DENSE, 1, M, 4096, 4096, 152)
         assert (rc, c, swap) == (OK, cols, 1) and grid <= 152 and grid % split == 0
