@@ -44,20 +44,22 @@
 // goes to the teardown, which drains copies and MMAs.
 //
 // What bounds it, and what it measured (one GB300):
-//   16384 x 4096 x 4096, blocks form: 225 us, 2.44 PFLOP/s, 1.28 times the
+//   16384 x 4096 x 4096, blocks form: 219 us, 2.51 PFLOP/s, 1.31 times the
 //   measured bf16 rate. MMAs alone would take 512 cycles a K block (N = 256)
 //   and run beside the reads of tensor memory at full rate; a round through
 //   commit, barrier, read, add and release takes about 1450, of which two
 //   accumulators hide half. 4096 x 4096 x 4096 with scales per row of both
-//   operands: 99 us (two operations per element and a read of the columns'
+//   operands: 97 us (two operations per element and a read of the columns'
 //   scales from shared memory).
 //   16 x 4096 x 4096: 10.1 us, most of it launch, set-up and the two
 //   barriers of a split tile; 48 experts of 2048 x 2048 on 2 rows each:
 //   38.8 us, 5.2 TB/s of weights.
 // Not taken: pairs of CTAs on 256 x 256 tiles (cta_group::2; 433 us: the
 // round goes through two SMs), two accumulators of 128 columns with barriers
-// of their own (285 us), waits that poll without a pause (241 to 304 us: they
-// take issue slots from the warps that add).
+// of their own (285 us), C stored from the registers (225 us; gradients of
+// 16 experts' 2048 x 2048 weights from 16383 rows 132 us for 124: the warps
+// that add held a tile 1100 cycles a piece), waits that poll without a pause
+// (241 to 304 us: they take issue slots from the warps that add).
 #include "common.cuh"
 #include "experts.cuh"
 #include "ptx.cuh"
@@ -71,7 +73,7 @@ namespace sgemm_gb300 {
 namespace {
 
 constexpr int kScaleBatch = 2;   // K blocks whose scales are handed over together
-constexpr int kStaging = 4096;   // bytes an epilogue warp turns its tile through: 128 of each of 32 rows
+constexpr int kStaging = 4096;   // a piece of a tile on its way to C: 128 bytes of each of a warp's 32 rows
 
 template <int BN_, bool SWAP_>
 struct Fp8Cfg {
@@ -81,7 +83,7 @@ struct Fp8Cfg {
     static constexpr int P_TILE = 128 * ROW_BYTES;           // lanes' operand
     static constexpr int Q_TILE = BN * ROW_BYTES;            // columns' operand
     static constexpr int STAGE_BYTES = P_TILE + Q_TILE;
-    static constexpr int STAGES = BN == 256 ? 3 : BN == 128 ? 5 : 7;   // 3 or 4 of 48 KB: the same time
+    static constexpr int STAGES = BN == 256 ? 3 : BN == 128 ? 4 : 7;   // more of 48 or 32 KB: the same time
     static constexpr int NBUF = BN == 256 ? 2 : 4;           // accumulators in tensor memory
     static constexpr int TMEM_COLS = NBUF * BN < 32 ? 32 : NBUF * BN;
     static constexpr int EPI_WARPS = BN >= 128 ? 8 : 4;
@@ -92,12 +94,12 @@ struct Fp8Cfg {
     static constexpr int THREADS = 128 + 32 * EPI_WARPS;
     // Registers move from the first four warps to the eight that hold up to
     // 128 sums per thread: 168 * 384 at launch, 72 * 128 + 216 * 256 (or
-    // 88 * 128 + 208 * 256) after.
+    // 88 * 128 + 208 * 256) after: the splits with the fewest spills.
     static constexpr int EPI_REGS = BN == 256 ? 216 : BN == 128 ? 208 : 0;
     static constexpr int SDEPTH = BN == 256 ? 4 : 6;         // ring of scales
     static constexpr int SLOT = kScaleBatch * BN;            // floats of one slot
     static constexpr bool CAN_SPLIT = SWAP;
-    static constexpr int STAGING = SWAP ? 0 : EPI_WARPS * kStaging;
+    static constexpr int STAGING = SWAP ? 0 : EPI_WARPS * 2 * kStaging;
     static constexpr int PARTIAL = CAN_SPLIT ? BN * 128 * 4 : 0;
     static constexpr int NUM_BARS = 2 * STAGES + NBUF + 2 * SDEPTH + 1;
     static constexpr int OFF_STAGING = STAGES * STAGE_BYTES;
@@ -145,7 +147,8 @@ struct Fp8Params {
     float beta;
     void *C;
     int64_t ldc, stride_c;
-    int c_bf16, vec_c;
+    int c_bf16;
+    int tma_c;                   // mapC holds C (whole 16-byte pieces, beta 0)
     unsigned int *status;
 };
 
@@ -418,6 +421,16 @@ __device__ __forceinline__ uint4 ld_shared_u32x4(uint32_t addr)
     return v;
 }
 
+// A box in shared memory (128-byte swizzle) to its place in C, asynchronously,
+// as part of the thread's next bulk group.
+__device__ __forceinline__ void tma_store(const CUtensorMap *map, uint32_t src, int32_t x, int32_t y, int32_t z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(src)
+                 : "memory");
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
 {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -429,7 +442,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
 template <class Cfg, bool ROWS_FORM>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
 fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_constant__ CUtensorMap mapQ,
-                   const __grid_constant__ Fp8Params p)
+                   const __grid_constant__ CUtensorMap mapC, const __grid_constant__ Fp8Params p)
 {
     constexpr int BN = Cfg::BN, STAGES = Cfg::STAGES, NBUF = Cfg::NBUF, SD = Cfg::SDEPTH, CW = Cfg::CW;
     constexpr int CHUNK = Cfg::CHUNK;
@@ -806,37 +819,53 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
                 }
             } else {
                 // Lane = row of A; 128 bytes of each of 32 rows at a time go
-                // through shared memory, so that a warp's stores cover whole
-                // 128-byte pieces of 4 rows instead of 16 bytes of 32.
-                const uint32_t st = base + Cfg::OFF_STAGING + ew * kStaging;
+                // through shared memory and leave by TMA, while the next piece
+                // is written beside them and the next tile begun. Rows that
+                // end inside the 32 at the next group's first, columns that
+                // end inside the 128 bytes (TMA stores whole 16 bytes), and C
+                // that TMA cannot address or that is read, are stored by the
+                // lanes.
                 const int row0 = w.a_row + 32 * q;
-                // Writes 128 bytes of columns from col0 on: 32 floats, or 64 bfloat16.
-                auto flush = [&](const uint32_t (&u)[32], int cols, int col0) {
-                    const int size = 128 / cols;
+                const bool whole_rows = p.mode != kFp8GroupRows || row0 + 32 <= w.a_end;
+                // Writes 128 bytes of the warp's columns from h on: 32 floats, or 64 bfloat16.
+                auto flush = [&](const uint32_t (&u)[32], int cols, int h) {
+                    const int col0 = w.b_row + half * CW + h, place = (h / cols) & 1;
+                    const uint32_t st = base + Cfg::OFF_STAGING + (2 * ew + place) * kStaging;
+                    const bool pieces = p.tma_c && col0 + cols <= p.N, whole = pieces && whole_rows;
+                    // The piece that was last here has left: the one before the
+                    // last, or the last where a tile has only one.
+                    if (lane == 0) {
+                        if (cols < CW) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                        else asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    }
                     __syncwarp();
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
                         st_shared_u32x4(st + 128 * lane + 16 * (c ^ (lane & 7)),
                                         make_uint4(u[4 * c], u[4 * c + 1], u[4 * c + 2], u[4 * c + 3]));
+                    if (whole) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
-                    if (p.vec_c && p.beta == 0.0f && col0 + cols <= p.N) {
-                        uint4 x[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int r = 4 * i + (lane >> 3), c = lane & 7;
-                            x[i] = ld_shared_u32x4(st + 128 * r + 16 * (c ^ (r & 7)));
-                        }
+                    if (lane == 0) {
+                        if (whole && row0 < w.a_end)
+                            tma_store(&mapC, st, col0, row0, p.mode == kFp8GroupK ? w.group : 0);
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");   // one group per piece, if empty
+                    }
+                    if (whole) return;
+                    if (pieces) {
+                        // 16 bytes per lane, of four rows at a time.
+                        const int size = 128 / cols;
                         uint8_t *dst = static_cast<uint8_t *>(p.C) +
                                        (c_base + (int64_t)(row0 + (lane >> 3)) * p.ldc + col0) * size + 16 * (lane & 7);
-#pragma unroll
+#pragma unroll 4
                         for (int i = 0; i < 8; ++i) {
-                            if (row0 + 4 * i + (lane >> 3) < w.a_end) *reinterpret_cast<uint4 *>(dst) = x[i];
+                            const int r = 4 * i + (lane >> 3), c = lane & 7;
+                            if (row0 + r < w.a_end)
+                                *reinterpret_cast<uint4 *>(dst) = ld_shared_u32x4(st + 128 * r + 16 * (c ^ (r & 7)));
                             dst += 4 * p.ldc * size;
                         }
                         return;
                     }
-                    // Rows that are not whole aligned pieces: lane by lane, eight
-                    // rows read before the first is stored.
+                    // Lane by lane, eight rows read before the first is stored.
                     const int64_t at = c_base + (int64_t)row0 * p.ldc + col0;
                     const int rows = w.a_end - row0;
 #pragma unroll 1
@@ -870,14 +899,13 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
                         }
                     }
                 };
-                const int col_base = w.b_row + half * CW;
                 uint32_t u[32];
                 if (p.c_bf16 && p.beta == 0.0f) {
 #pragma unroll
                     for (int h = 0; h < CW; h += 64) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) u[j] = pack_bf16(acc[h / 2 + j].x, acc[h / 2 + j].y);
-                        flush(u, 64, col_base + h);
+                        flush(u, 64, h);
                     }
                 } else {
 #pragma unroll
@@ -885,11 +913,13 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             u[j] = __float_as_uint((j & 1) ? acc[h / 2 + j / 2].y : acc[h / 2 + j / 2].x);
-                        flush(u, 32, col_base + h);
+                        flush(u, 32, h);
                     }
                 }
             }
         }
+        if (!SWAP && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
         ptx::tc_fence_before();
     }
 
@@ -928,10 +958,7 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
     }
 }
 
-// Tensor map of an 8-bit operand: `rows` rows of K bytes, `groups` of them
-// `stride` bytes apart, in boxes of one K block by box_rows rows.
-cudaError_t encode_fp8(CUtensorMap *map, const uint8_t *ptr, int64_t rows, int64_t k, int64_t ld, int64_t groups,
-                       int64_t stride, int box_rows)
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
 {
     static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
         void *fnp = nullptr;
@@ -941,6 +968,15 @@ cudaError_t encode_fp8(CUtensorMap *map, const uint8_t *ptr, int64_t rows, int64
             fnp = nullptr;
         return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fnp);
     }();
+    return encode;
+}
+
+// Tensor map of an 8-bit operand: `rows` rows of K bytes, `groups` of them
+// `stride` bytes apart, in boxes of one K block by box_rows rows.
+cudaError_t encode_fp8(CUtensorMap *map, const uint8_t *ptr, int64_t rows, int64_t k, int64_t ld, int64_t groups,
+                       int64_t stride, int box_rows)
+{
+    const auto encode = tensor_map_encoder();
     if (!encode) return cudaErrorNotSupported;
     const cuuint64_t dims[3] = {(cuuint64_t)k, (cuuint64_t)rows, (cuuint64_t)groups};
     const cuuint64_t strides[2] = {(cuuint64_t)ld, (cuuint64_t)stride};
@@ -949,6 +985,23 @@ cudaError_t encode_fp8(CUtensorMap *map, const uint8_t *ptr, int64_t rows, int64
     const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t *>(ptr), dims, strides, box,
                               elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Tensor map of C (of all groups' under grouped K), in boxes of 128 bytes by
+// the 32 rows of an epilogue warp.
+cudaError_t encode_c(CUtensorMap *map, const Fp8Args &g)
+{
+    const auto encode = tensor_map_encoder();
+    if (!encode) return cudaErrorNotSupported;
+    const int64_t size = g.c_bf16 ? 2 : 4, many = g.mode == kFp8GroupK ? g.groups : 1;
+    const cuuint64_t dims[3] = {(cuuint64_t)g.N, (cuuint64_t)g.M, (cuuint64_t)many};
+    const cuuint64_t strides[2] = {(cuuint64_t)(g.ldc * size), (cuuint64_t)((many > 1 ? g.stride_c : g.M * g.ldc) * size)};
+    const cuuint32_t box[3] = {(cuuint32_t)(128 / size), 32, 1};
+    const cuuint32_t elem[3] = {1, 1, 1};
+    const CUresult r = encode(map, g.c_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, g.C,
+                              dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -1015,12 +1068,14 @@ cudaError_t launch_cfg(const Fp8Args &g, const Fp8Plan &plan, cudaStream_t strea
     p.ldc = g.ldc;
     p.stride_c = g.stride_c;
     p.c_bf16 = g.c_bf16;
-    const int64_t per16 = g.c_bf16 ? 8 : 4;
-    p.vec_c = ((reinterpret_cast<uintptr_t>(g.C) & 15u) == 0 && g.ldc % per16 == 0 &&
-               (g.mode != kFp8GroupK || g.stride_c % per16 == 0)) ? 1 : 0;
     p.status = g.status;
     CUtensorMap &mp = Cfg::SWAP ? map_b : map_a, &mq = Cfg::SWAP ? map_a : map_b;
-    void *args[] = {&mp, &mq, &p};
+    CUtensorMap map_c = map_a;                        // any valid one where C goes without
+    const int64_t per16 = g.c_bf16 ? 8 : 4;
+    if (!Cfg::SWAP && g.beta == 0.0f && (reinterpret_cast<uintptr_t>(g.C) & 15u) == 0 && g.ldc % per16 == 0 &&
+        (g.mode != kFp8GroupK || g.stride_c % per16 == 0))
+        p.tma_c = encode_c(&map_c, g) == cudaSuccess ? 1 : 0;
+    void *args[] = {&mp, &mq, &map_c, &p};
     const void *fn = g.rows_form ? reinterpret_cast<const void *>(fp8_product_kernel<Cfg, true>)
                                  : reinterpret_cast<const void *>(fp8_product_kernel<Cfg, false>);
     cudaLaunchConfig_t lc = {};
