@@ -16,9 +16,11 @@
 //   warp 1      TMEM owner and MMA issuer: 4 MMAs (K 32 each) per block into
 //               one of NBUF accumulators, then a commit that frees the stage
 //               and hands the accumulator on;
-//   warps 2, 3  scales of the accumulator's columns, where each has its own:
-//               asynchronous 4-byte copies into a ring, since rows of scales
-//               start at any address;
+//   warps 2, 3  warp 2 finds the CTA's tiles, up to four ahead, for all (found
+//               by each role, a tile cost the adding warps 2000 cycles); both
+//               copy the scales of the accumulator's columns, where each has
+//               its own: asynchronous 4-byte copies into a ring, since rows of
+//               scales start at any address;
 //   warps 4..   promotion and epilogue: warp 4 + i reads lanes 32 (i % 4) ..
 //               of accumulator columns (i / 4) * CW ..; its lanes' scales (and
 //               the one that its columns share) it fetches itself, two K
@@ -73,6 +75,8 @@ namespace sgemm_gb300 {
 namespace {
 
 constexpr int kScaleBatch = 2;   // K blocks whose scales are handed over together
+constexpr int kItems = 4;        // tiles found ahead of their sums
+constexpr int kItemBytes = 32;
 constexpr int kStaging = 4096;   // a piece of a tile on its way to C: 128 bytes of each of a warp's 32 rows
 
 template <int BN_, bool SWAP_>
@@ -101,11 +105,12 @@ struct Fp8Cfg {
     static constexpr bool CAN_SPLIT = SWAP;
     static constexpr int STAGING = SWAP ? 0 : EPI_WARPS * 2 * kStaging;
     static constexpr int PARTIAL = CAN_SPLIT ? BN * 128 * 4 : 0;
-    static constexpr int NUM_BARS = 2 * STAGES + NBUF + 2 * SDEPTH + 1;
+    static constexpr int NUM_BARS = 2 * STAGES + NBUF + 2 * SDEPTH + 2 * kItems + 1;
     static constexpr int OFF_STAGING = STAGES * STAGE_BYTES;
     static constexpr int OFF_PARTIAL = OFF_STAGING + STAGING;
     static constexpr int OFF_SCALES = OFF_PARTIAL + PARTIAL;
-    static constexpr int OFF_TABLE = OFF_SCALES + SDEPTH * SLOT * 4;
+    static constexpr int OFF_ITEMS = OFF_SCALES + SDEPTH * SLOT * 4;
+    static constexpr int OFF_TABLE = OFF_ITEMS + kItems * kItemBytes;
     static constexpr int OFF_BARS = OFF_TABLE + (kMaxGroups + 2) * 4;
     static constexpr int SMEM_BYTES = 1024 + OFF_BARS + NUM_BARS * 8 + 16;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
@@ -153,9 +158,9 @@ struct Fp8Params {
 };
 
 // One tile: its group, first row of A and of B, the end of its rows of A,
-// and its K blocks.
+// its K blocks, and whether the CTA has another after it.
 struct Fp8Item {
-    int group, a_row, a_end, b_row, kb0, kb1;
+    int group, a_row, a_end, b_row, kb0, kb1, more;
 };
 
 __device__ __forceinline__ int clamp_to(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
@@ -181,6 +186,28 @@ __device__ __forceinline__ int find_group(const int *table, int groups, int x)
     return lo;
 }
 
+// An item on its way through shared memory.
+__device__ __forceinline__ void store_item(uint32_t at, const Fp8Item &w)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w.group), "r"(w.a_row), "r"(w.a_end), "r"(w.b_row)
+                 : "memory");
+    asm volatile("st.shared.v4.u32 [%0+16], {%1,%2,%3,%3};" ::"r"(at), "r"(w.kb0), "r"(w.kb1), "r"(w.more) : "memory");
+}
+
+__device__ __forceinline__ Fp8Item load_item(uint32_t at)
+{
+    Fp8Item w;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w.group), "=r"(w.a_row), "=r"(w.a_end), "=r"(w.b_row)
+                 : "r"(at)
+                 : "memory");
+    asm volatile("{\n\t.reg .u32 x;\n\tld.shared.v4.u32 {%0,%1,%2,x}, [%3+16];\n\t}"
+                 : "=r"(w.kb0), "=r"(w.kb1), "=r"(w.more)
+                 : "r"(at)
+                 : "memory");
+    return w;
+}
+
 constexpr int kRaster = 16;   // token tiles walked together, so that a wave of CTAs shares both operands in L2
 
 template <class Cfg>
@@ -189,7 +216,7 @@ __device__ __forceinline__ Fp8Item fp8_item(const Fp8Params &p, const int *table
     constexpr int TT = Cfg::SWAP ? Cfg::BN : 128;    // rows of A per tile
     constexpr int WT = Cfg::SWAP ? 128 : Cfg::BN;    // rows of B per tile
     Fp8Item it;
-    it.group = 0;
+    it.group = it.more = 0;
     int tokens = p.token_tiles;
     if (p.mode == kFp8GroupRows) tokens = table[p.groups];
     if (p.mode == kFp8GroupK) {
@@ -461,7 +488,9 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
     auto acce_bar = [&](int b) { return bars + 8u * (2 * STAGES + b); };
     auto sfull_bar = [&](int s) { return bars + 8u * (2 * STAGES + NBUF + s); };
     auto sempty_bar = [&](int s) { return bars + 8u * (2 * STAGES + NBUF + SD + s); };
-    const uint32_t drain_bar = bars + 8u * (2 * STAGES + NBUF + 2 * SD);
+    auto ifull_bar = [&](uint32_t i) { return bars + 8u * (2 * STAGES + NBUF + 2 * SD + i); };
+    auto iempty_bar = [&](uint32_t i) { return bars + 8u * (2 * STAGES + NBUF + 2 * SD + kItems + i); };
+    const uint32_t drain_bar = bars + 8u * (2 * STAGES + NBUF + 2 * SD + 2 * kItems);
     const uint32_t tmem_slot = bars + 8u * Cfg::NUM_BARS;
     auto scale_slot = [&](int s) { return base + Cfg::OFF_SCALES + s * (Cfg::SLOT * 4); };
 
@@ -477,6 +506,7 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
     if (warp == 2 && lane == 0) {
         ptx::prefetch_tensormap(&mapP);
         ptx::prefetch_tensormap(&mapQ);
+        if (!SWAP && p.tma_c) ptx::prefetch_tensormap(&mapC);
     }
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -487,6 +517,12 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
         for (int s = 0; s < SD; ++s) {
             ptx::mbar_init(sfull_bar(s), 64);
             ptx::mbar_init(sempty_bar(s), Cfg::EPI_WARPS);
+        }
+        for (int i = 0; i < kItems; ++i) {
+            // Read by the producer, the MMA issuer, the warps that store and,
+            // where columns have scales, warp 3.
+            ptx::mbar_init(ifull_bar(i), 1);
+            ptx::mbar_init(iempty_bar(i), Cfg::EPI_WARPS + (COLS_SCALED ? 3 : 2));
         }
         ptx::mbar_init(drain_bar, 1);
         ptx::mbar_init_fence();
@@ -541,6 +577,17 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
                                                                                      : p.token_tiles * p.groups);
     if (split > 1 && tiles > t_step) tiles = t_step;   // a split grid has one tile per cluster
 
+    // The CTA's nth tile, once warp 2 has found it; not to be read after done_with().
+    auto item_at = [&](uint32_t n) { return base + Cfg::OFF_ITEMS + (n % kItems) * kItemBytes; };
+    auto item_there = [&](uint32_t n) {
+        const uint32_t bar = ifull_bar(n % kItems), phase = (n / kItems) & 1;
+        return FP8_WAIT(mbar_test(bar, phase), bar, phase);
+    };
+    auto done_with = [&](uint32_t n) {
+        __syncwarp();
+        mbar_arrive_if(lane == 0, iempty_bar(n % kItems));
+    };
+
     if constexpr (Cfg::EPI_REGS > 0) {
         if (warp < 4) ptx::setmaxnreg_dec<BN == 256 ? 72 : 88>();
     }
@@ -548,10 +595,15 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
         // ------------------------------ TMA producer ------------------------------
         const uint32_t on = elect_one();
         const uint64_t policy = ptx::policy_evict_last();
-        uint32_t it = 0;
+        uint32_t it = 0, n = 0;
         bool ok = true;
-        for (uint32_t t = t_first; ok && t < tiles; t += t_step) {
-            const Fp8Item w = fp8_item<Cfg>(p, table, t, rank);
+        for (uint32_t t = t_first; ok && t < tiles; t += t_step, ++n) {
+            if (!item_there(n)) {
+                if (lane == 0) atomicOr(p.status, kStatusTimeout);
+                break;
+            }
+            const Fp8Item w = load_item(item_at(n));
+            done_with(n);
             const int z = p.mode == kFp8GroupRows ? w.group : 0;
             for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
                 const int s = (int)(it % STAGES);
@@ -580,10 +632,15 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
         const uint64_t desc_p = ptx::sdesc_kmajor(stage_p(0), Cfg::ROW_BYTES);
         const uint64_t desc_q = ptx::sdesc_kmajor(stage_q(0), Cfg::ROW_BYTES);
         const uint32_t on = elect_one();
-        uint32_t it = 0, early = 0;
+        uint32_t it = 0, early = 0, n = 0;
         bool ok = true;
-        for (uint32_t t = t_first; ok && t < tiles; t += t_step) {
-            const Fp8Item w = fp8_item<Cfg>(p, table, t, rank);
+        for (uint32_t t = t_first; ok && t < tiles; t += t_step, ++n) {
+            if (!item_there(n)) {
+                if (lane == 0) atomicOr(p.status, kStatusTimeout);
+                break;
+            }
+            const Fp8Item w = load_item(item_at(n));
+            done_with(n);
             for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
                 const int s = (int)(it % STAGES), b = (int)(it % NBUF);
                 const uint32_t full = (it / STAGES) & 1, free = ((it / NBUF) & 1) ^ 1, next = it + 1;
@@ -607,13 +664,36 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
         mma_commit_if(on, drain_bar);
         if (!ptx::wait_phase_warp(drain_bar, 0) && lane == 0) atomicOr(p.status, kStatusTimeout);
     } else if (warp < 4) {
-        // ------------------------------ scales ------------------------------
-        // A slot holds BN scales for each of up to kScaleBatch K blocks of a tile.
+        // -------------------------- tiles and scales --------------------------
+        // Warp 2 finds the tiles, ahead of the others. A slot of the scales
+        // holds BN of them for each of up to kScaleBatch K blocks of a tile.
         const int th = threadIdx.x - 64;
-        uint32_t it = 0;
-        bool ok = COLS_SCALED;
-        for (uint32_t t = t_first; ok && t < tiles; t += t_step) {
-            const Fp8Item w = fp8_item<Cfg>(p, table, t, rank);
+        uint32_t it = 0, n = 0;
+        bool ok = COLS_SCALED || warp == 2;
+        for (uint32_t t = t_first; ok && t < tiles; t += t_step, ++n) {
+            Fp8Item w;
+            if (warp == 2) {
+                w = fp8_item<Cfg>(p, table, t, rank);
+                w.more = t + t_step < tiles;
+                // The place is free when the tile kItems before is stored; a
+                // wait's limit is far above the time of 2^16 K blocks.
+                const uint32_t bar = iempty_bar(n % kItems), phase = ((n / kItems) & 1) ^ 1;
+                ok = ptx::wait_phase_warp(bar, phase);
+                for (int k = p.nk >> 16; !ok && k > 0; --k) ok = ptx::wait_phase_warp(bar, phase);
+                if (ok && lane == 0) store_item(item_at(n), w);
+                mbar_arrive_if(ok && lane == 0, ifull_bar(n % kItems));
+            } else {
+                ok = item_there(n);
+                if (ok) {
+                    w = load_item(item_at(n));
+                    done_with(n);
+                }
+            }
+            if (!ok) {
+                if (lane == 0) atomicOr(p.status, kStatusTimeout);
+                break;
+            }
+            if (!COLS_SCALED) continue;
             const float *src = SWAP ? p.sa : p.sb;
             const int64_t ld = SWAP ? p.ld_sa : p.ld_sb;
             const int first = SWAP ? w.a_row : w.b_row, end = SWAP ? w.a_end : p.N;
@@ -647,7 +727,7 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
         const float *const slots = reinterpret_cast<const float *>(smem_raw + (base - raw) + Cfg::OFF_SCALES);
         if (Cfg::CAN_SPLIT && split > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         if constexpr (Cfg::EPI_REGS > 0) ptx::setmaxnreg_inc<Cfg::EPI_REGS>();
-        uint32_t it = 0, batch = 0;
+        uint32_t it = 0, batch = 0, n = 0;
         bool ok = true;
         // Where the next K block's scales are: this lane's, and the one that
         // this warp's columns share. Past a tile's last block the place stays,
@@ -682,19 +762,24 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
             }
             fetch(w.kb0, w.kb1);
         };
-        // Of a tile the sums' loop keeps its K blocks alone: the store decodes
+        // Of a tile the sums' loop keeps its K blocks alone: the store reads
         // it again. (Registers: what the store needs, kept through the loop,
         // spills there and costs a quarter of its speed.)
         int kb0 = 0, kb1 = 0;
-        auto enter = [&](uint32_t t) {
-            if (t >= tiles) return;
-            const Fp8Item w = fp8_item<Cfg>(p, table, t, rank);
+        auto enter = [&](uint32_t i) {
+            if (!item_there(i)) {
+                if (lane == 0) atomicOr(p.status, kStatusTimeout);
+                ok = false;
+                return;
+            }
+            const Fp8Item w = load_item(item_at(i));
             start(w);
             kb0 = w.kb0;
             kb1 = w.kb1;
         };
-        enter(t_first);
-        for (uint32_t t = t_first; ok && t < tiles; t += t_step) {
+        bool more = t_first < tiles;
+        if (more) enter(0);
+        for (; ok && more; ++n) {
             float2 acc[CW / 2];
 #pragma unroll
             for (int j = 0; j < CW / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
@@ -780,10 +865,10 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
             if (!ok && lane == 0) atomicOr(p.status, kStatusTimeout);
             if (!ok && split == 1) break;
             // The next tile's first scales are on their way while this one is stored.
-            enter(t + t_step);
-            uint32_t stored = t;
-            asm volatile("" : "+r"(stored));              // not to be kept from before the loop
-            const Fp8Item w = fp8_item<Cfg>(p, table, stored, rank);
+            more = ld_shared_u32(item_at(n) + 24) != 0;
+            if (more) enter(n + 1);
+            const Fp8Item w = load_item(item_at(n));
+            done_with(n);
             const int64_t c_base = p.mode == kFp8GroupK ? w.group * p.stride_c : 0;
             if constexpr (SWAP) {
                 // Lane = row of B (column of C), column = row of A.
