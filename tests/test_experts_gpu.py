@@ -289,6 +289,89 @@ def test_grouped_k(cuda_device, name, MN):
             check_product(C[e], want * (1 + beta), S * (1 + beta) + 1e-30, padded // 128 + 2, False)
 
 
+def small_integers(rows, cols, generator):
+    return torch.randint(-3, 4, (rows, cols), generator=generator, device="cuda").float().to(FP8)
+
+
+def powers_of_two(rows, cols, generator):
+    return 2.0 ** torch.randint(0, 2, (rows, cols), generator=generator, device="cuda").float()
+
+
+def spread(s, cols, rows=1):
+    """Scales of blocks of `rows` x 128 values, one per value of `cols` columns."""
+    return s.repeat_interleave(128, 1)[:, :cols].repeat_interleave(rows, 0).double()
+
+
+@pytest.mark.parametrize("counts", [[5, 0, 160, 31, 33, 300, 1, 700], [32, 64, 0, 95, 129, 1, 1300], [700, 900]], ids=str)
+@pytest.mark.parametrize("N", [256, 328, 1000])
+@pytest.mark.parametrize("ctype", [sg.SGEMM_F32, sg.SGEMM_BF16], ids=["f32", "bf16"])
+def test_groups_that_end_inside_pieces_of_an_aligned_c(cuda_device, counts, N, ctype):
+    """Integers (sums below 9 * 4 * 200 < 2^24): exact, or rounded once."""
+    E, K, R = len(counts), 200, sum(counts) + 40
+    g = torch.Generator(device="cuda").manual_seed(N + E)
+    off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32).cuda()
+    nk, nb = 2, -(-N // 128)
+    A, B = small_integers(R, 208, g), small_integers(E * N, 208, g)
+    sa, sb = powers_of_two(nk, R, g), powers_of_two(E * nb, nk, g)
+    C = Guarded(R, N, ref.up(N, 8) + 8, TYPES[ctype])
+    ok(sg.sgemm_fp8_grouped(E, off.data_ptr(), R, N, K, A.data_ptr(), 208, sa.data_ptr(), R, B.data_ptr(), 208, N * 208,
+                            sb.data_ptr(), nk, nb * nk, 0.0, C.ptr, ctype, C.ld, stream()))
+    finish()
+    a = A[:, :K].double() * spread(sa.t(), K)
+    for e in range(E):
+        lo, hi = int(off[e]), int(off[e + 1])
+        b = B[e * N:(e + 1) * N, :K].double() * spread(sb[e * nb:(e + 1) * nb], K, 128)[:N]
+        assert torch.equal(C.view()[lo:hi], (a[lo:hi] @ b.t()).to(TYPES[ctype]))
+    assert bool((C.view()[int(off[-1]):] == 77.0).all()), "rows of no group were written"
+    assert C.outside_untouched()
+
+
+@pytest.mark.parametrize("form", [sg.SGEMM_SCALE_BLOCKS, sg.SGEMM_SCALE_ROWS], ids=["blocks", "rows"])
+@pytest.mark.parametrize("shape", [(20000, 1500, 130), (40, 65000, 250)], ids=lambda s: "x".join(map(str, s)))
+def test_many_tiles_per_cta(cuda_device, shape, form):
+    M, N, K = shape
+    g = torch.Generator(device="cuda").manual_seed(M)
+    nk, nb, ld = -(-K // 128), -(-N // 128), ref.up(K, 16)
+    A, B = small_integers(M, ld, g), small_integers(N, ld, g)
+    sa = powers_of_two(nk, M, g)
+    sb = powers_of_two(nb, nk, g) if form == sg.SGEMM_SCALE_BLOCKS else powers_of_two(nk, N, g)
+    b = spread(sb, K, 128)[:N] if form == sg.SGEMM_SCALE_BLOCKS else spread(sb.t(), K)
+    C = Guarded(M, N, ref.up(N, 8), torch.float32)
+    ok(sg.sgemm_fp8(form, M, N, K, A.data_ptr(), ld, sa.data_ptr(), M, B.data_ptr(), ld, sb.data_ptr(), sb.shape[1], 0.0,
+                    C.ptr, sg.SGEMM_F32, C.ld, stream()))
+    finish()
+    want = (A[:, :K].double() * spread(sa.t(), K)) @ (B[:, :K].double() * b).t()
+    assert torch.equal(C.view().double(), want)
+    assert C.outside_untouched()
+
+
+@pytest.mark.parametrize("MN", [(512, 512), (300, 1030)], ids=["512x512", "300x1030"])
+def test_many_groups_of_k_most_of_them_short_or_empty(cuda_device, MN):
+    """Several tiles per CTA, runs of them without a single K block."""
+    M, N = MN
+    g = torch.Generator(device="cuda").manual_seed(M)
+    counts = [(0, 0, 0, 0, 0, 200, 1, 0, 128, 0, 0, 129, 0, 0, 0, 0)[e % 16] for e in range(112)]
+    E, R = len(counts), sum(counts)
+    off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32).cuda()
+    padded = ref.up(R + 127 * min(R, E), 128)
+    A, B = (torch.zeros(rows, padded, dtype=FP8, device="cuda") for rows in (M, N))
+    begin, at = [], 0
+    for n in counts:
+        begin.append(at)
+        A[:, at:at + n] = small_integers(M, n, g)
+        B[:, at:at + n] = small_integers(N, n, g)
+        at += ref.up(n, 128)
+    sa, sb = powers_of_two(padded // 128, M, g), powers_of_two(padded // 128, N, g)
+    C = Guarded(E * M, N, ref.up(N, 4), torch.float32)
+    ok(sg.sgemm_fp8_grouped_k(E, off.data_ptr(), padded, M, N, A.data_ptr(), padded, sa.data_ptr(), M, B.data_ptr(),
+                              padded, sb.data_ptr(), N, 0.0, C.ptr, sg.SGEMM_F32, C.ld, M * C.ld, stream()))
+    finish()
+    a, b = (q.double() * spread(s.t(), padded) for q, s in ((A, sa), (B, sb)))
+    for e, (at, n) in enumerate(zip(begin, counts)):
+        assert torch.equal(C.view()[e * M:(e + 1) * M].double(), a[:, at:at + n] @ b[:, at:at + n].t()), e
+    assert C.outside_untouched()
+
+
 def test_group_offsets_out_of_range_stay_in_bounds(cuda_device):
     """Offsets that are no partition are held to the rows there are."""
     R, N, K, E = 40, 128, 128, 4
