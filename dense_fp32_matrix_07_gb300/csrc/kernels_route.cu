@@ -56,6 +56,16 @@ __device__ __forceinline__ float sigmoid(float l) { return __fdiv_rn(1.0f, 1.0f 
 // exp(l - m); 1 where both are the same infinity.
 __device__ __forceinline__ float exp_below(float l, float m) { return l == m ? 1.0f : expf(l - m); }
 
+// The score of logit l over exp(min(m, 0)) (sigmoid) or, but for the sum over
+// the row, over exp(m) (softmax): between 1/2 and 1 for l = m, so that the
+// ratios of chosen scores keep range and digits where the scores themselves
+// are below 2^-126. For m >= 0 the sigmoid is the score itself.
+__device__ __forceinline__ float relative_score(float l, float m, int use_sigmoid)
+{
+    if (!use_sigmoid) return exp_below(l, m);
+    return __fdiv_rn(exp_below(fminf(l, 0.0f), fminf(m, 0.0f)), 1.0f + expf(-fabsf(l)));
+}
+
 // Four neighbouring values.
 __device__ __forceinline__ void load4(const float *p, float *v)
 {
@@ -240,9 +250,10 @@ route_kernel(int64_t tokens, int E, const T *__restrict__ logits, int64_t ld, in
 // experts, g_j the gradient of slot j and c the scale:
 //   softmax, renormalised: dl_j = w_j (g_j - sum_S w_i g_i / c), w_j = c e_j / sum_S e   (j in S)
 //   softmax:               dl_i = c p_i (g_i [i in S] - sum_S p_j g_j)                   (every i)
-//   sigmoid, renormalised: dl_j = c / D (g_j - sum_S g_i s_i / D) s_j (1 - s_j), D = sum_S s
+//   sigmoid, renormalised: dl_j = w_j (g_j - sum_S w_i g_i / c) (1 - s_j), w_j = c s_j / sum_S s
 //   sigmoid:               dl_j = c g_j s_j (1 - s_j)
-// with 1 - s taken as sigmoid(-l), which keeps its digits where s is near 1.
+// with 1 - s taken as sigmoid(-l), which keeps its digits where s is near 1,
+// and the weights from scores relative to the largest chosen one.
 // Only the second needs the whole row of logits; the others read the chosen
 // ones and write a row of zeros with k values in it. One warp per token;
 // bound by instructions and the latency of its three dependent loads (16383
@@ -280,27 +291,20 @@ route_backward_kernel(int64_t tokens, int E, const T *__restrict__ logits, int64
         }
     }
     float d = 0.0f;
-    if (use_sigmoid) {
-        if (e >= 0) {
-            const float s = sigmoid(l), slope = s * sigmoid(-l);
-            d = scale * g * slope;
-        }
-        if (renorm) {
-            const float s = e >= 0 ? sigmoid(l) : 0.0f;
-            const float D = warp_sum(s), mean = warp_sum(s * g);
-            d = 0.0f;
-            if (e >= 0 && D > 0.0f) d = scale / D * (g - mean / D) * (s * sigmoid(-l));
-        }
-        zero_row(out, E, vec, lane);
-    } else if (renorm) {
-        float m = e >= 0 ? l : __uint_as_float(0xff800000u);
+    if (renorm) {
+        const float least = __uint_as_float(0xff800000u);
+        float m = e >= 0 ? l : least;
 #pragma unroll
         for (int o = 16; o; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float x = e >= 0 ? exp_below(l, m) : 0.0f;
+        const float x = e >= 0 && l != least ? relative_score(l, m, use_sigmoid) : 0.0f;
         const float total = warp_sum(x);
         const float w = total > 0.0f ? x / total : 0.0f;
         const float mean = warp_sum(w * g);
         d = scale * w * (g - mean);
+        if (use_sigmoid) d *= sigmoid(-l);
+        zero_row(out, E, vec, lane);
+    } else if (use_sigmoid) {
+        if (e >= 0) d = scale * g * (sigmoid(l) * sigmoid(-l));
         zero_row(out, E, vec, lane);
     } else {
         uint32_t best = 0;
