@@ -42,12 +42,20 @@ __device__ __forceinline__ float warp_sum(float x)
     return x;
 }
 
-// Sum over groups of L neighbouring lanes.
+// Sum and maximum over groups of L neighbouring lanes.
 template <int L>
 __device__ __forceinline__ float lanes_sum(float x)
 {
 #pragma unroll
     for (int d = L / 2; d; d /= 2) x += __shfl_xor_sync(0xffffffffu, x, d);
+    return x;
+}
+
+template <int L>
+__device__ __forceinline__ float lanes_max(float x)
+{
+#pragma unroll
+    for (int d = L / 2; d; d /= 2) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
     return x;
 }
 
@@ -114,8 +122,8 @@ route_kernel(int64_t tokens, int E, const T *__restrict__ logits, int64_t ld, in
         }
     }
     auto expert = [&](int i) { return (i / 4) * (4 * L) + 4 * sub + (i & 3); };
-    // Softmax statistics over the eligible logits. Renormalised weights of
-    // experts chosen by their logits need none: the whole row's sum cancels.
+    // Softmax statistics over the eligible logits, for keys and weights that
+    // are scores. Renormalised weights need none: the row's sum cancels.
     const bool by_score = bias != nullptr || two;
     float m = 0.0f, sum = 1.0f;
     if (!use_sigmoid && (by_score || !renorm)) {
@@ -215,22 +223,28 @@ route_kernel(int64_t tokens, int E, const T *__restrict__ logits, int64_t ld, in
         if (sub == 0) chosen[slot][j] = best ? e : -1;
     }
     __syncwarp();
-    // Without the row's statistics the first choice has the largest logit, and
-    // the sum is that of the chosen.
-    const bool plain = !use_sigmoid && !by_score && renorm;
-    if (plain) m = chosen[slot][0] >= 0 ? load_as_float(row + chosen[slot][0]) : 0.0f;
     constexpr int HELD = kMaxTop / L;             // slots per lane
     int e[HELD];
-    float w[HELD], total = 0.0f;
+    float x[HELD], w[HELD], total = 0.0f;
 #pragma unroll
     for (int h = 0; h < HELD; ++h) {
         const int j = sub + h * L;
         e[h] = j < k ? chosen[slot][j] : -1;
-        w[h] = 0.0f;
-        if (e[h] >= 0) {
-            const float x = load_as_float(row + e[h]);
-            w[h] = plain ? exp_below(x, m) : score(x);
-        }
+        x[h] = e[h] >= 0 ? load_as_float(row + e[h]) : __uint_as_float(0xff800000u);
+    }
+    // Renormalised softmax weights are ratios of the chosen scores: taken
+    // relative to the largest of these, not of the row, which a bias may have
+    // passed over.
+    const bool chosen_only = renorm && !use_sigmoid;
+    if (chosen_only) {
+        m = x[0];
+#pragma unroll
+        for (int h = 1; h < HELD; ++h) m = fmaxf(m, x[h]);
+        m = lanes_max<L>(m);
+    }
+#pragma unroll
+    for (int h = 0; h < HELD; ++h) {
+        w[h] = e[h] < 0 ? 0.0f : chosen_only ? relative_score(x[h], m, 0) : score(x[h]);
         total += w[h];
     }
     if (renorm) total = lanes_sum<L>(total);
@@ -294,8 +308,7 @@ route_backward_kernel(int64_t tokens, int E, const T *__restrict__ logits, int64
     if (renorm) {
         const float least = __uint_as_float(0xff800000u);
         float m = e >= 0 ? l : least;
-#pragma unroll
-        for (int o = 16; o; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        m = lanes_max<32>(m);
         const float x = e >= 0 && l != least ? relative_score(l, m, use_sigmoid) : 0.0f;
         const float total = warp_sum(x);
         const float w = total > 0.0f ? x / total : 0.0f;

@@ -86,3 +86,38 @@ def test_sigmoid_gradient_of_very_small_scores(cuda_device, k, scale):
     np.put_along_axis(bound, indices, scale * w * 2 * np.abs(g).max() * (tolerance(k) + 85 * 2.0 ** -23), 1)
     assert np.isfinite(got).all()
     assert np.all(np.abs(got - want) <= bound + 1e-38), np.abs(got - want).max()
+
+
+def forward(l, kind, bias, k, scale):
+    """The library's renormalised weights and choice for logits l (T, E)."""
+    T, E = l.shape
+    dl, db = torch.tensor(l).cuda(), torch.tensor(bias).cuda() if bias is not None else None
+    w, ix = torch.empty(T, k, device="cuda"), torch.empty(T, k, dtype=torch.int32, device="cuda")
+    ok(sg.sgemm_route(T, E, dl.data_ptr(), sg.SGEMM_F32, E, db.data_ptr() if bias is not None else 0, kind, 1, 1, 0, k, 1,
+                      scale, w.data_ptr(), ix.data_ptr(), stream()))
+    finish()
+    return w.cpu().numpy().astype(np.float64), ix.cpu().numpy()
+
+
+@pytest.mark.parametrize("E", [8, 64, 128, 512])
+def test_softmax_weights_of_a_biased_choice_far_below_the_best(cuda_device, E):
+    """A bias chooses experts whose scores are denormal or zero in 32 bits; the gradient is that of these weights."""
+    k, scale = 3, 2.0
+    chosen = np.array([[-100.0, -101.0, -102.5], [-104.0, -105.0, -103.0], [-300.0, -301.0, -302.0],
+                       [-1.0, -2.0, -3.0], [-86.0, -88.0, -90.0]], np.float32)
+    T = len(chosen)
+    l = np.full((T, E), -9.0, np.float32)
+    l[:, 0], l[:, 1:4] = 0.0, chosen
+    bias = np.zeros(E, np.float32)
+    bias[1:4] = 9.0, 7.0, 5.0
+    w, ix = forward(l, SOFTMAX, bias, k, scale)
+    assert (ix == [1, 2, 3]).all()
+    want = scale * shares(chosen, SOFTMAX)
+    assert np.all(np.abs(w - want) <= tolerance(k) * want), np.abs(w / want - 1).max()
+    g = np.random.RandomState(1).randn(T, k).astype(np.float32)
+    d = np.zeros((T, E))
+    d[:, 1:4] = gradient(chosen, SOFTMAX, g, scale)
+    got = backward(l, SOFTMAX, ix, g, scale)
+    bound = np.zeros((T, E))
+    bound[:, 1:4] = want * 2 * np.abs(g).max() * tolerance(k)
+    assert np.all(np.abs(got - d) <= bound)
