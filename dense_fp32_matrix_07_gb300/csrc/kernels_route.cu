@@ -232,11 +232,10 @@ route_kernel(int64_t tokens, int E, const T *__restrict__ logits, int64_t ld, in
         e[h] = j < k ? chosen[slot][j] : -1;
         x[h] = e[h] >= 0 ? load_as_float(row + e[h]) : __uint_as_float(0xff800000u);
     }
-    // Renormalised softmax weights are ratios of the chosen scores: taken
-    // relative to the largest of these, not of the row, which a bias may have
-    // passed over.
-    const bool chosen_only = renorm && !use_sigmoid;
-    if (chosen_only) {
+    // Renormalised weights are ratios of the chosen scores: taken relative to
+    // the largest of these, which a bias may put far below the row's and a row
+    // of very negative logits below what 32 bits hold.
+    if (renorm) {
         m = x[0];
 #pragma unroll
         for (int h = 1; h < HELD; ++h) m = fmaxf(m, x[h]);
@@ -244,7 +243,7 @@ route_kernel(int64_t tokens, int E, const T *__restrict__ logits, int64_t ld, in
     }
 #pragma unroll
     for (int h = 0; h < HELD; ++h) {
-        w[h] = e[h] < 0 ? 0.0f : chosen_only ? relative_score(x[h], m, 0) : score(x[h]);
+        w[h] = e[h] < 0 ? 0.0f : renorm ? relative_score(x[h], m, use_sigmoid) : score(x[h]);
         total += w[h];
     }
     if (renorm) total = lanes_sum<L>(total);

@@ -121,3 +121,21 @@ def test_softmax_weights_of_a_biased_choice_far_below_the_best(cuda_device, E):
     bound = np.zeros((T, E))
     bound[:, 1:4] = want * 2 * np.abs(g).max() * tolerance(k)
     assert np.all(np.abs(got - d) <= bound)
+
+
+@pytest.mark.parametrize("E", [8, 64, 128, 512])
+@pytest.mark.parametrize("biased", [False, True], ids=["by_logit", "biased"])
+def test_sigmoid_weights_of_very_small_scores(cuda_device, E, biased):
+    k, scale = 2, 2.5
+    T = len(LOGITS)
+    l = np.full((T, E), -200.0, np.float32)
+    l[:, 1:3] = LOGITS
+    bias = None
+    if biased:
+        bias = np.zeros(E, np.float32)
+        bias[1:3] = 3.0, 5.0
+    w, ix = forward(l, SIGMOID, bias, k, scale)
+    at = np.take_along_axis(l, ix, 1)
+    assert (np.sort(ix, 1) == [1, 2]).all()
+    want = scale * shares(at, SIGMOID)
+    assert np.all(np.abs(w - want) <= (tolerance(k) + 85 * 2.0 ** -23) * want + 1e-38), np.abs(w / want - 1).max()
