@@ -29,6 +29,13 @@ int64_t span(int64_t rows, int64_t cols, int64_t ld, int64_t size, int64_t batch
     return e > (__int128)INT64_MAX ? -1 : (int64_t)e;
 }
 
+// The same of an 8-bit output: the quantisers store `piece` bytes of a row at a
+// time, the last row's padding with its last values (rows start on 16 bytes).
+int64_t span_fp8(int64_t rows, int64_t cols, int64_t ld, int64_t piece, int64_t batch = 1, int64_t stride = 0)
+{
+    return span(rows, ceil_div(cols, piece) * piece, ld, 1, batch, stride);
+}
+
 struct Region {
     const void *p;
     int64_t bytes;
@@ -95,7 +102,7 @@ int sgemm_fp8_quantize_rows(int64_t rows, int64_t cols, const void *src, int typ
     if (!gather && src_rows < rows) return SGEMM_ERR_INVALID_VALUE;
     if (!src && src_rows > 0) return SGEMM_ERR_INVALID_VALUE;
     if (too_large(rows) || cols > kMaxCols || too_large(src_rows)) return SGEMM_ERR_OVERFLOW;
-    const Region out[] = {{q, span(rows, cols, ldq, 1)}, {scales, span(ceil_div(cols, kBlock), rows, lds, 4)}};
+    const Region out[] = {{q, span_fp8(rows, cols, ldq, 8)}, {scales, span(ceil_div(cols, kBlock), rows, lds, 4)}};
     const Region in[] = {{src, span(src_rows, cols, ld, type_size(type))}, {gather, gather ? rows * 4 : 0}};
     int rc = check_regions(out, in);
     if (rc != SGEMM_OK) return rc;
@@ -120,7 +127,7 @@ int sgemm_fp8_quantize_both(int64_t rows, int64_t cols, const void *src, int typ
     if (too_large(rows) || too_large(cols) || too_large(src_rows) || too_large(padded)) return SGEMM_ERR_OVERFLOW;
     const Region out[] = {{q_t, span(cols, padded, ldq_t, 1)},
                           {scales_t, span(padded / kBlock, cols, lds_t, 4)},
-                          {q, q ? span(rows, cols, ldq, 1) : 0},
+                          {q, q ? span_fp8(rows, cols, ldq, 8) : 0},
                           {scales, q ? span(ceil_div(cols, kBlock), rows, lds, 4) : 0}};
     const Region in[] = {{src, span(src_rows, cols, ld, type_size(type))},
                          {gather, gather ? rows * 4 : 0},
@@ -157,7 +164,8 @@ int sgemm_fp8_quantize_blocks(int64_t rows, int64_t cols, const void *src, int t
     const int64_t q_one = span(qr, qc, ldq, 1), s_one = span(sr, sc, lds, 4);
     if (q_one < 0 || s_one < 0) return SGEMM_ERR_OVERFLOW;
     if (batch > 1 && (stride_q < q_one || stride_q % 16 != 0 || stride_s < s_one / 4)) return SGEMM_ERR_INVALID_VALUE;
-    const Region out[] = {{q, span(qr, qc, ldq, 1, batch, stride_q)}, {scales, span(sr, sc, lds, 4, batch, stride_s)}};
+    const Region out[] = {{q, span_fp8(qr, qc, ldq, transpose ? 16 : 8, batch, stride_q)},
+                          {scales, span(sr, sc, lds, 4, batch, stride_s)}};
     const Region in[] = {{src, span(rows, cols, ld, type_size(type), batch, stride_src)}};
     int rc = check_regions(out, in);
     if (rc != SGEMM_OK) return rc;
