@@ -36,9 +36,13 @@ int64_t span_fp8(int64_t rows, int64_t cols, int64_t ld, int64_t piece, int64_t 
     return span(rows, ceil_div(cols, piece) * piece, ld, 1, batch, stride);
 }
 
+// An array of a call: where it lies, its extent, and the size of its elements.
 struct Region {
     const void *p;
-    int64_t bytes;
+    int64_t bytes, size;
+    template <class T>
+    Region(const T *p, int64_t bytes) : Region(p, bytes, sizeof(T)) {}
+    Region(const void *p, int64_t bytes, int64_t size) : p(p), bytes(bytes), size(size) {}
 };
 
 bool overlap(const Region &a, const Region &b)
@@ -48,8 +52,9 @@ bool overlap(const Region &a, const Region &b)
     return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
 }
 
-// SGEMM_OK, or why an output must not be written: a region that overflows,
-// an output that overlaps an input or another output.
+// SGEMM_OK, or why a call must not run: a region that overflows, elements that
+// do not lie on multiples of their size, an output that overlaps an input or
+// another output.
 template <int NOUT, int NIN>
 int check_regions(const Region (&out)[NOUT], const Region (&in)[NIN])
 {
@@ -57,6 +62,11 @@ int check_regions(const Region (&out)[NOUT], const Region (&in)[NIN])
         if (o.bytes < 0) return SGEMM_ERR_OVERFLOW;
     for (const Region &i : in)
         if (i.bytes < 0) return SGEMM_ERR_OVERFLOW;
+    auto between = [](const Region &r) { return r.bytes > 0 && !aligned(r.p, (uintptr_t)r.size); };
+    for (const Region &o : out)
+        if (between(o)) return SGEMM_ERR_INVALID_VALUE;
+    for (const Region &i : in)
+        if (between(i)) return SGEMM_ERR_INVALID_VALUE;
     for (int a = 0; a < NOUT; ++a) {
         for (int b = 0; b < a; ++b)
             if (overlap(out[a], out[b])) return SGEMM_ERR_INVALID_VALUE;
@@ -103,7 +113,7 @@ int sgemm_fp8_quantize_rows(int64_t rows, int64_t cols, const void *src, int typ
     if (!src && src_rows > 0) return SGEMM_ERR_INVALID_VALUE;
     if (too_large(rows) || cols > kMaxCols || too_large(src_rows)) return SGEMM_ERR_OVERFLOW;
     const Region out[] = {{q, span_fp8(rows, cols, ldq, 8)}, {scales, span(ceil_div(cols, kBlock), rows, lds, 4)}};
-    const Region in[] = {{src, span(src_rows, cols, ld, type_size(type))}, {gather, gather ? rows * 4 : 0}};
+    const Region in[] = {{src, span(src_rows, cols, ld, type_size(type)), type_size(type)}, {gather, gather ? rows * 4 : 0}};
     int rc = check_regions(out, in);
     if (rc != SGEMM_OK) return rc;
     DeviceInfo dev;
@@ -129,7 +139,7 @@ int sgemm_fp8_quantize_both(int64_t rows, int64_t cols, const void *src, int typ
                           {scales_t, span(padded / kBlock, cols, lds_t, 4)},
                           {q, q ? span_fp8(rows, cols, ldq, 8) : 0},
                           {scales, q ? span(ceil_div(cols, kBlock), rows, lds, 4) : 0}};
-    const Region in[] = {{src, span(src_rows, cols, ld, type_size(type))},
+    const Region in[] = {{src, span(src_rows, cols, ld, type_size(type)), type_size(type)},
                          {gather, gather ? rows * 4 : 0},
                          {offsets, offsets ? (groups + 1) * 4 : 0}};
     int rc = check_regions(out, in);
@@ -166,7 +176,7 @@ int sgemm_fp8_quantize_blocks(int64_t rows, int64_t cols, const void *src, int t
     if (batch > 1 && (stride_q < q_one || stride_q % 16 != 0 || stride_s < s_one / 4)) return SGEMM_ERR_INVALID_VALUE;
     const Region out[] = {{q, span_fp8(qr, qc, ldq, transpose ? 16 : 8, batch, stride_q)},
                           {scales, span(sr, sc, lds, 4, batch, stride_s)}};
-    const Region in[] = {{src, span(rows, cols, ld, type_size(type), batch, stride_src)}};
+    const Region in[] = {{src, span(rows, cols, ld, type_size(type), batch, stride_src), type_size(type)}};
     int rc = check_regions(out, in);
     if (rc != SGEMM_OK) return rc;
     DeviceInfo dev;
@@ -190,7 +200,7 @@ int sgemm_fp8(int b_form, int64_t M, int64_t N, int64_t K, const uint8_t *A, int
                   bad_scales(sb, ld_sb, rows_form ? nk : nb, rows_form ? N : nk)))
         return SGEMM_ERR_INVALID_VALUE;
     if (too_large(M) || too_large(N) || too_large(K)) return SGEMM_ERR_OVERFLOW;
-    const Region out[] = {{C, span(M, N, ldc, type_size(c_type))}};
+    const Region out[] = {{C, span(M, N, ldc, type_size(c_type)), type_size(c_type)}};
     const Region in[] = {{A, span(M, K, lda, 1)},
                          {B, span(N, K, ldb, 1)},
                          {sa, span(nk, M, ld_sa, 4)},
@@ -226,7 +236,7 @@ int sgemm_fp8_grouped(int64_t groups, const int32_t *offsets, int64_t rows, int6
     if (b_one < 0 || s_one < 0) return SGEMM_ERR_OVERFLOW;
     if (K > 0 && groups > 1 && (stride_b < b_one || stride_b % 16 != 0 || stride_sb < s_one / 4))
         return SGEMM_ERR_INVALID_VALUE;
-    const Region out[] = {{C, span(rows, N, ldc, type_size(c_type))}};
+    const Region out[] = {{C, span(rows, N, ldc, type_size(c_type)), type_size(c_type)}};
     const Region in[] = {{A, span(rows, K, lda, 1)},
                          {B, span(N, K, ldb, 1, groups, stride_b)},
                          {sa, span(nk, rows, ld_sa, 4)},
@@ -264,7 +274,7 @@ int sgemm_fp8_grouped_k(int64_t groups, const int32_t *offsets, int64_t padded, 
     const int64_t size = type_size(c_type), c_one = span(M, N, ldc, size);
     if (c_one < 0) return SGEMM_ERR_OVERFLOW;
     if (groups > 1 && stride_c < c_one / size) return SGEMM_ERR_INVALID_VALUE;
-    const Region out[] = {{C, span(M, N, ldc, size, groups, stride_c)}};
+    const Region out[] = {{C, span(M, N, ldc, size, groups, stride_c), size}};
     const Region in[] = {{A, span(M, padded, lda, 1)},
                          {B, span(N, padded, ldb, 1)},
                          {sa, span(nk, M, ld_sa, 4)},
@@ -329,7 +339,7 @@ int sgemm_route(int64_t T, int64_t E, const void *logits, int type, int64_t ld, 
     if (T == 0) return SGEMM_OK;
     if (!logits || !weights || !indices) return SGEMM_ERR_INVALID_VALUE;
     const Region out[] = {{weights, span(T, k, k, 4)}, {indices, span(T, k, k, 4)}};
-    const Region in[] = {{logits, span(T, E, ld, type_size(type))}, {bias, bias ? E * 4 : 0}};
+    const Region in[] = {{logits, span(T, E, ld, type_size(type)), type_size(type)}, {bias, bias ? E * 4 : 0}};
     if ((rc = check_regions(out, in)) != SGEMM_OK) return rc;
     DeviceInfo dev;
     if ((rc = device_info(&dev)) != SGEMM_OK) return rc;
@@ -347,8 +357,8 @@ int sgemm_route_backward(int64_t T, int64_t E, const void *logits, int type, int
     if (ld_g < E) return SGEMM_ERR_INVALID_VALUE;
     if (T == 0) return SGEMM_OK;
     if (!logits || !indices || !grad_w || !grad_logits) return SGEMM_ERR_INVALID_VALUE;
-    const Region out[] = {{grad_logits, span(T, E, ld_g, type_size(type))}};
-    const Region in[] = {{logits, span(T, E, ld, type_size(type))},
+    const Region out[] = {{grad_logits, span(T, E, ld_g, type_size(type)), type_size(type)}};
+    const Region in[] = {{logits, span(T, E, ld, type_size(type)), type_size(type)},
                          {indices, span(T, k, k, 4)},
                          {grad_w, span(T, k, k, 4)}};
     if ((rc = check_regions(out, in)) != SGEMM_OK) return rc;
@@ -391,8 +401,10 @@ int sgemm_combine(int64_t T, int k, int64_t cols, int64_t rows, const void *Y, i
     if ((!Y && rows > 0) || !row_of || !out || ldy < cols || ld_out < cols) return SGEMM_ERR_INVALID_VALUE;
     if (too_large(T) || cols > kMaxCols || too_large(rows)) return SGEMM_ERR_OVERFLOW;
     const int64_t size = type_size(type);
-    const Region o[] = {{out, span(T, cols, ld_out, size)}};
-    const Region in[] = {{Y, span(rows, cols, ldy, size)}, {row_of, span(T, k, k, 4)}, {weights, weights ? span(T, k, k, 4) : 0}};
+    const Region o[] = {{out, span(T, cols, ld_out, size), size}};
+    const Region in[] = {{Y, span(rows, cols, ldy, size), size},
+                         {row_of, span(T, k, k, 4)},
+                         {weights, weights ? span(T, k, k, 4) : 0}};
     int rc = check_regions(o, in);
     if (rc != SGEMM_OK) return rc;
     DeviceInfo dev;
@@ -413,9 +425,10 @@ int sgemm_combine_backward(int64_t T, int k, int64_t cols, int64_t rows, const v
     if (grad_w && ((!Y && rows > 0 && cols > 0) || ldy < cols)) return SGEMM_ERR_INVALID_VALUE;
     if (too_large(T) || too_large(cols) || too_large(rows)) return SGEMM_ERR_OVERFLOW;
     const int64_t size = type_size(type);
-    const Region o[] = {{grad_y, grad_y ? span(rows, cols, ld_gy, size) : 0}, {grad_w, grad_w ? span(T, k, k, 4) : 0}};
-    const Region in[] = {{grad_out, span(T, cols, ld_go, size)},
-                         {Y, grad_w ? span(rows, cols, ldy, size) : 0},
+    const Region o[] = {{grad_y, grad_y ? span(rows, cols, ld_gy, size) : 0, size},
+                        {grad_w, grad_w ? span(T, k, k, 4) : 0}};
+    const Region in[] = {{grad_out, span(T, cols, ld_go, size), size},
+                         {Y, grad_w ? span(rows, cols, ldy, size) : 0, size},
                          {row_of, span(T, k, k, 4)},
                          {weights, weights ? span(T, k, k, 4) : 0}};
     int rc = check_regions(o, in);

@@ -15,12 +15,14 @@
  * 2^24 - 256 columns); larger ones return SGEMM_ERR_OVERFLOW.
  *
  * Types of matrices: SGEMM_F32 (float), SGEMM_BF16 (bfloat16). Row-major, any
- * leading dimension and alignment, except the 8-bit ones: q, A and B lie on
- * 16-byte boundaries with leading dimensions (and batch strides) that are
- * multiples of 16, which is what the product's copies need; the bytes between
- * a row's last value and its leading dimension may be written (after the last
- * row's, those to the next multiple of 8, or of 16 in a transposed form: no
- * other matrix of the call may lie there) and are never read as values.
+ * leading dimension and any alignment of whole elements (an array that does not
+ * lie on a multiple of its elements' size is refused), except the 8-bit ones:
+ * q, A and B lie on 16-byte boundaries with leading dimensions (and batch
+ * strides) that are multiples of 16, which is what the product's copies need;
+ * the bytes between a row's last value and its leading dimension may be written
+ * (after the last row's, those to the next multiple of 8, or of 16 in a
+ * transposed form: no other matrix of the call may lie there) and are never
+ * read as values.
  *
  * 8-bit values are e4m3 (largest 448) and share scales by blocks of 128:
  *   rows form     value (r, c) stands for q[r*ldq + c] * scales[(c/128)*lds + r]
