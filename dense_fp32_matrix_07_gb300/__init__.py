@@ -39,7 +39,7 @@ EXPORTED = ("sgemm", "sgemm_ex", "sgemm_check_status", "sgemm_error_string",
 EXPORTED_EXPERTS = ("sgemm_fp8_quantize_rows", "sgemm_fp8_quantize_cols", "sgemm_fp8_quantize_both",
                     "sgemm_fp8_quantize_blocks", "sgemm_fp8", "sgemm_fp8_grouped", "sgemm_fp8_grouped_k",
                     "sgemm_fp8_plan", "sgemm_route", "sgemm_route_backward", "sgemm_dispatch", "sgemm_combine",
-                    "sgemm_combine_backward")
+                    "sgemm_combine_backward", "sgemm_test_fail_next_setups")
 
 # Matrix types, scale forms of B, router scores and product modes of sgemm_experts.h.
 SGEMM_F32, SGEMM_BF16 = 0, 1
@@ -136,6 +136,7 @@ def load(rebuild: bool = False):
                 "sgemm_combine": [_i64, i, _i64, _i64, _vp, i, _i64, _vp, _vp, _vp, _i64, _vp],
                 "sgemm_combine_backward": [_i64, i, _i64, _i64, _vp, i, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp,
                                            _vp],
+                "sgemm_test_fail_next_setups": [i],
             }.items():
                 getattr(lib, name).restype = ctypes.c_int
                 getattr(lib, name).argtypes = args
@@ -360,3 +361,8 @@ def sgemm_combine_backward(T, k, cols, rows, grad_out, type, ld_go, Y, ldy, row_
     """Gradients of sgemm_combine() with respect to Y and the weights."""
     return load().sgemm_combine_backward(T, k, cols, rows, grad_out, type, ld_go, Y, ldy, row_of, weights, grad_y,
                                          ld_gy, grad_w, stream)
+
+
+def sgemm_test_fail_next_setups(n) -> int:
+    """Test hook: the next `n` set-ups of the kernels above are treated as failed (host only)."""
+    return load().sgemm_test_fail_next_setups(n)

@@ -2,6 +2,7 @@
 // tile-configuration selector and kernel dispatch. The exported functions and
 // their contracts are declared in include/sgemm.h.
 #include "../../include/sgemm.h"
+#include "../../include/sgemm_experts.h"
 #include "common.cuh"
 #include "configs.cuh"
 #include "experts.cuh"
@@ -28,6 +29,7 @@ struct DeviceState {
     int num_sms = 0;
     unsigned int *status = nullptr;   // device address of g_status_word
     cudaMemPool_t pool = nullptr;     // scratch for packed operands
+    bool experts_ready = false;       // the kernels of sgemm_experts.h are set up
 };
 
 std::mutex g_mutex;
@@ -55,7 +57,7 @@ int device_state(DeviceState **out)
             cudaGetLastError();
             return SGEMM_ERR_CUDA;
         }
-        if (configs_prepare_device() != cudaSuccess || prepare_fp8() != cudaSuccess || prepare_route() != cudaSuccess) {
+        if (configs_prepare_device() != cudaSuccess) {
             cudaGetLastError();
             return SGEMM_ERR_CUDA;
         }
@@ -118,17 +120,20 @@ int check_sizes(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64
 
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
-// Test hook (sgemm_test_fail_next_allocs): scratch allocations still to fail.
-std::atomic<int> g_fail_allocs{0};
+// Test hooks (sgemm_test_fail_next_allocs, sgemm_test_fail_next_setups):
+// scratch allocations and set-ups of the experts' kernels still to fail.
+std::atomic<int> g_fail_allocs{0}, g_fail_setups{0};
 
 // One pending test failure, if any is left to take.
-bool take_test_alloc_failure()
+bool take_test_failure(std::atomic<int> &left)
 {
-    int n = g_fail_allocs.load();
+    int n = left.load();
     while (n > 0)
-        if (g_fail_allocs.compare_exchange_weak(n, n - 1)) return true;
+        if (left.compare_exchange_weak(n, n - 1)) return true;
     return false;
 }
+
+bool take_test_alloc_failure() { return take_test_failure(g_fail_allocs); }
 
 }  // namespace
 
@@ -138,11 +143,23 @@ cudaError_t device_status_word(unsigned int **out)
     return cudaGetSymbolAddress(reinterpret_cast<void **>(out), g_status_word);
 }
 
+// The experts' operators set their kernels up on their own first call, so that
+// the FP32 products neither wait for them nor fail with them.
 int device_info(DeviceInfo *out)
 {
     DeviceState *dev = nullptr;
     const int rc = device_state(&dev);
     if (rc != SGEMM_OK) return rc;
+    {
+        std::lock_guard<std::mutex> lock(g_mutex);
+        if (!dev->experts_ready) {
+            if (take_test_failure(g_fail_setups) || prepare_fp8() != cudaSuccess || prepare_route() != cudaSuccess) {
+                cudaGetLastError();
+                return SGEMM_ERR_CUDA;
+            }
+            dev->experts_ready = true;
+        }
+    }
     *out = DeviceInfo{dev->status, dev->num_sms, dev->pool};
     return SGEMM_OK;
 }
@@ -544,6 +561,13 @@ int sgemm_test_fail_next_allocs(int n)
 {
     if (n < 0) return SGEMM_ERR_INVALID_VALUE;
     g_fail_allocs.store(n);
+    return SGEMM_OK;
+}
+
+int sgemm_test_fail_next_setups(int n)
+{
+    if (n < 0) return SGEMM_ERR_INVALID_VALUE;
+    g_fail_setups.store(n);
     return SGEMM_OK;
 }
 

@@ -11,6 +11,9 @@
  * depends on the order in which threads run: the same inputs give the same
  * bits. Only sgemm_dispatch() takes scratch (from the library's pool).
  *
+ * The first call of these on a device sets their kernels up, also where
+ * products of sgemm.h have run; a failure of that fails no product there.
+ *
  * Sizes go up to 2^31 - 1024 (sgemm_fp8_quantize_rows() and sgemm_combine():
  * 2^24 - 256 columns); larger ones return SGEMM_ERR_OVERFLOW.
  *
@@ -234,6 +237,16 @@ int sgemm_combine(int64_t T, int k, int64_t cols, int64_t rows, const void *Y, i
 int sgemm_combine_backward(int64_t T, int k, int64_t cols, int64_t rows, const void *grad_out, int type,
                            int64_t ld_go, const void *Y, int64_t ldy, const int32_t *row_of, const float *weights,
                            void *grad_y, int64_t ld_gy, float *grad_w, cudaStream_t stream);
+
+/*
+ * sgemm_test_fail_next_setups — test hook: the next n times that a call above
+ * would set its kernels up on a device (the first call there does) count as
+ * failed: it returns SGEMM_ERR_CUDA with nothing enqueued, and a later call
+ * tries again. The products of sgemm.h do not set these kernels up. n = 0
+ * clears a pending count. Returns SGEMM_OK, or SGEMM_ERR_INVALID_VALUE for
+ * n < 0. Host only; needs no GPU.
+ */
+int sgemm_test_fail_next_setups(int n);
 
 #ifdef __cplusplus
 }
