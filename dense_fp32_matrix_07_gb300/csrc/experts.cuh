@@ -78,7 +78,7 @@ cudaError_t launch_fp8(const Fp8Args &g, cudaStream_t stream);
 
 cudaError_t launch_quantize_rows(int64_t rows, int64_t cols, const void *src, bool bf16, int64_t ld,
                                  const int32_t *gather, int64_t src_rows, uint8_t *q, int64_t ldq, float *scales,
-                                 int64_t lds, int num_sms, cudaStream_t stream);
+                                 int64_t lds, cudaStream_t stream);
 // The transposed column form (qt, scales_t) and, where q is given, the row form from the same read.
 cudaError_t launch_quantize_cols(int64_t rows, int64_t cols, const void *src, bool bf16, int64_t ld,
                                  const int32_t *gather, int64_t src_rows, int groups, const int32_t *offsets,
@@ -105,9 +105,9 @@ struct RouteArgs {
     bool renorm;
     float scale;
 };
-cudaError_t launch_route(const RouteArgs &r, float *weights, int32_t *indices, int num_sms, cudaStream_t stream);
+cudaError_t launch_route(const RouteArgs &r, float *weights, int32_t *indices, cudaStream_t stream);
 cudaError_t launch_route_backward(const RouteArgs &r, const int32_t *indices, const float *grad_w, void *grad_logits,
-                                  int64_t ld_g, int num_sms, cudaStream_t stream);
+                                  int64_t ld_g, cudaStream_t stream);
 // One-time set-up of the device (shared memory above 48 KB).
 cudaError_t prepare_route();
 // Bytes of scratch launch_dispatch() needs (0: none).
@@ -115,11 +115,10 @@ size_t dispatch_scratch_bytes(int64_t n, int E);
 cudaError_t launch_dispatch(int64_t T, int k, int E, const int32_t *indices, int32_t *offsets, int32_t *row_of,
                             int32_t *token_of, void *scratch, cudaStream_t stream);
 cudaError_t launch_combine(int64_t T, int k, int64_t cols, int64_t rows, const void *Y, bool bf16, int64_t ldy,
-                           const int32_t *row_of, const float *weights, void *out, int64_t ld_out, int num_sms,
-                           cudaStream_t stream);
+                           const int32_t *row_of, const float *weights, void *out, int64_t ld_out, cudaStream_t stream);
 cudaError_t launch_combine_backward(int64_t T, int k, int64_t cols, int64_t rows, const void *grad_out, bool bf16,
                                     int64_t ld_go, const void *Y, int64_t ldy, const int32_t *row_of,
-                                    const float *weights, void *grad_y, int64_t ld_gy, float *grad_w, int num_sms,
+                                    const float *weights, void *grad_y, int64_t ld_gy, float *grad_w,
                                     cudaStream_t stream);
 
 // ------------------------------------------------------------ device helpers

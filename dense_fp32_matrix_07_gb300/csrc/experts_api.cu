@@ -119,7 +119,7 @@ int sgemm_fp8_quantize_rows(int64_t rows, int64_t cols, const void *src, int typ
     DeviceInfo dev;
     if ((rc = device_info(&dev)) != SGEMM_OK) return rc;
     return launched(launch_quantize_rows(rows, cols, src, type == SGEMM_BF16, ld, gather, src_rows, q, ldq, scales, lds,
-                                         dev.num_sms, stream));
+                                         stream));
 }
 
 int sgemm_fp8_quantize_both(int64_t rows, int64_t cols, const void *src, int type, int64_t ld, const int32_t *gather,
@@ -345,7 +345,7 @@ int sgemm_route(int64_t T, int64_t E, const void *logits, int type, int64_t ld, 
     if ((rc = device_info(&dev)) != SGEMM_OK) return rc;
     const RouteArgs r{T, (int)E, logits, type == SGEMM_BF16, ld, bias, score == SGEMM_SCORE_SIGMOID, groups, kept,
                       two == 1, k, renorm == 1, scale};
-    return launched(launch_route(r, weights, indices, dev.num_sms, stream));
+    return launched(launch_route(r, weights, indices, stream));
 }
 
 int sgemm_route_backward(int64_t T, int64_t E, const void *logits, int type, int64_t ld, int score, int k, int renorm,
@@ -366,7 +366,7 @@ int sgemm_route_backward(int64_t T, int64_t E, const void *logits, int type, int
     if ((rc = device_info(&dev)) != SGEMM_OK) return rc;
     const RouteArgs r{T, (int)E, logits, type == SGEMM_BF16, ld, nullptr, score == SGEMM_SCORE_SIGMOID, 1, 1, false, k,
                       renorm == 1, scale};
-    return launched(launch_route_backward(r, indices, grad_w, grad_logits, ld_g, dev.num_sms, stream));
+    return launched(launch_route_backward(r, indices, grad_w, grad_logits, ld_g, stream));
 }
 
 int sgemm_dispatch(int64_t T, int k, int64_t E, const int32_t *indices, int32_t *offsets, int32_t *row_of,
@@ -409,8 +409,7 @@ int sgemm_combine(int64_t T, int k, int64_t cols, int64_t rows, const void *Y, i
     if (rc != SGEMM_OK) return rc;
     DeviceInfo dev;
     if ((rc = device_info(&dev)) != SGEMM_OK) return rc;
-    return launched(launch_combine(T, k, cols, rows, Y, type == SGEMM_BF16, ldy, row_of, weights, out, ld_out, dev.num_sms,
-                                   stream));
+    return launched(launch_combine(T, k, cols, rows, Y, type == SGEMM_BF16, ldy, row_of, weights, out, ld_out, stream));
 }
 
 int sgemm_combine_backward(int64_t T, int k, int64_t cols, int64_t rows, const void *grad_out, int type, int64_t ld_go,
@@ -436,7 +435,7 @@ int sgemm_combine_backward(int64_t T, int k, int64_t cols, int64_t rows, const v
     DeviceInfo dev;
     if ((rc = device_info(&dev)) != SGEMM_OK) return rc;
     return launched(launch_combine_backward(T, k, cols, rows, grad_out, type == SGEMM_BF16, ld_go, Y, ldy, row_of, weights,
-                                            grad_y, ld_gy, grad_w, dev.num_sms, stream));
+                                            grad_y, ld_gy, grad_w, stream));
 }
 
 }  // extern "C"

@@ -47,12 +47,16 @@
 //
 // What bounds it, and what it measured (one GB300):
 //   16384 x 4096 x 4096, blocks form: 219 us, 2.51 PFLOP/s, 1.31 times the
-//   measured bf16 rate. MMAs alone would take 512 cycles a K block (N = 256)
-//   and run beside the reads of tensor memory at full rate; a round through
-//   commit, barrier, read, add and release takes about 1450, of which two
-//   accumulators hide half. 4096 x 4096 x 4096 with scales per row of both
-//   operands: 97 us (two operations per element and a read of the columns'
-//   scales from shared memory).
+//   measured bf16 rate. MMAs alone would take 512 cycles a K block (N = 256);
+//   it takes 830, the rest being the accumulator's round through commit,
+//   barrier, read, add and release, with two accumulators to overlap it.
+//   Counters at 4096^3 (69 us): tensor pipe 52 % active; shared memory gives
+//   384 accesses of 128 bytes a block to the MMAs and 36 to the warps, and its
+//   clients collide in under 1 % of the cycles.
+//   4096 x 4096 x 4096 with scales per row of both operands: 97 us, 1190
+//   cycles a block. There the warps read the columns' scales too: 384 + 620
+//   accesses of shared memory a block are its bound (and an element takes two
+//   operations).
 //   16 x 4096 x 4096: 10.1 us, most of it launch, set-up and the two
 //   barriers of a split tile; 48 experts of 2048 x 2048 on 2 rows each:
 //   38.8 us, 5.2 TB/s of weights.
@@ -118,7 +122,9 @@ struct Fp8Cfg {
     static_assert(OFF_BARS % 8 == 0, "barrier alignment");
 };
 
-// Division by a number the host knows: n / d for n < 2^31.
+// Division by a number the host knows, n / d for n < 2^31, by the multiplier
+// and shift of Granlund and Montgomery ("Division by invariant integers using
+// multiplication", 1994).
 struct FastDiv {
     uint32_t d, mul, shift;   // n / d = (umulhi(n, mul) + n) >> shift, in 33 bits
 };
@@ -492,7 +498,6 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
     auto iempty_bar = [&](uint32_t i) { return bars + 8u * (2 * STAGES + NBUF + 2 * SD + kItems + i); };
     const uint32_t drain_bar = bars + 8u * (2 * STAGES + NBUF + 2 * SD + 2 * kItems);
     const uint32_t tmem_slot = bars + 8u * Cfg::NUM_BARS;
-    auto scale_slot = [&](int s) { return base + Cfg::OFF_SCALES + s * (Cfg::SLOT * 4); };
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = Cfg::CAN_SPLIT ? p.split : 1;
@@ -909,7 +914,8 @@ fp8_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_consta
                 // end inside the 32 at the next group's first, columns that
                 // end inside the 128 bytes (TMA stores whole 16 bytes), and C
                 // that TMA cannot address or that is read, are stored by the
-                // lanes.
+                // lanes. (Read, beta != 0: one element after the other; 16
+                // experts' 2048 x 2048 FP32 gradients 937 us, 115 with beta 0.)
                 const int row0 = w.a_row + 32 * q;
                 const bool whole_rows = p.mode != kFp8GroupRows || row0 + 32 <= w.a_end;
                 // Writes 128 bytes of the warp's columns from h on: 32 floats, or 64 bfloat16.
@@ -1191,8 +1197,14 @@ cudaError_t launch_cfg(const Fp8Args &g, const Fp8Plan &plan, cudaStream_t strea
 //   the SMs (128 x 16384: 22.1 against 26.5; 8000 rows over the experts 75.6
 //   against 97.2), else 64 columns with split tiles (128 x 4096: 14.6 against
 //   17.6).
-//   More: 128 x 256 tiles, unless 128 x 128 ones take fewer waves of CTAs by
-//   more than the quarter that they are slower per value.
+//   More: 128 x 256 or 128 x 128 tiles, by their waves of CTAs, a wave of the
+//   latter counted as 3/4 of one of the former (N = K = 4096: 512 rows, one
+//   wave of either, 23.2 and 17.0; 1024 rows, one and two, 23.2 and 27.3; 1280
+//   rows, two and three, 37.5 and 35.5, where the rule takes the former; 2048
+//   rows, two and four, 39.6 and 45.7).
+// Groups go by their average: how many rows each has only the device knows.
+// 2048 rows over 64 experts are given 32 columns a tile, and where all are in
+// two of them these read their weights 32 times (38.5; as two groups 17.0).
 Fp8Plan plan_fp8(const Fp8Args &g)
 {
     const int64_t nk = ceil_div(g.K, kBlock), sms = g.num_sms;

@@ -457,7 +457,7 @@ cudaError_t launch_tiles(TileArgs &a, int num_sms, cudaStream_t stream)
 
 cudaError_t launch_quantize_rows(int64_t rows, int64_t cols, const void *src, bool bf16, int64_t ld,
                                  const int32_t *gather, int64_t src_rows, uint8_t *q, int64_t ldq, float *scales,
-                                 int64_t lds, int, cudaStream_t stream)
+                                 int64_t lds, cudaStream_t stream)
 {
     const dim3 grid((unsigned)((rows + kRowsPerCta - 1) / kRowsPerCta),
                     (unsigned)((blocks_of(cols) + kBlocksPerCta - 1) / kBlocksPerCta));

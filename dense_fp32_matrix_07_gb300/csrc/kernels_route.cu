@@ -583,13 +583,13 @@ cudaError_t route_of(const RouteArgs &r, float *weights, int32_t *indices, cudaS
 
 }  // namespace
 
-cudaError_t launch_route(const RouteArgs &r, float *weights, int32_t *indices, int, cudaStream_t stream)
+cudaError_t launch_route(const RouteArgs &r, float *weights, int32_t *indices, cudaStream_t stream)
 {
     return r.bf16 ? route_of<__nv_bfloat16>(r, weights, indices, stream) : route_of<float>(r, weights, indices, stream);
 }
 
 cudaError_t launch_route_backward(const RouteArgs &r, const int32_t *indices, const float *grad_w, void *grad_logits,
-                                  int64_t ld_g, int, cudaStream_t stream)
+                                  int64_t ld_g, cudaStream_t stream)
 {
     const unsigned grid = (unsigned)((r.T + kRouteWarps - 1) / kRouteWarps);
     const int64_t per16 = r.bf16 ? 8 : 4;

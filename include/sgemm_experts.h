@@ -116,7 +116,11 @@ int sgemm_fp8_quantize_blocks(int64_t rows, int64_t cols, const void *src, int t
  *   C, c_type, ldc  M x N. beta == 0: C is not read.
  *
  * Products within a block of 128 are summed on the tensor cores, the scaled
- * sums of the blocks in FP32. K == 0 is the empty sum. With x the input
+ * sums of the blocks in FP32. The two scales of a block and its sum are
+ * multiplied in either order: where the product of any two of the three leaves
+ * FP32's range (values near 2^113 and above, or scales whose product is below
+ * 2^-126), the result may be infinite, NaN or short of digits, though the
+ * whole product would not be. K == 0 is the empty sum. With x the input
  * (M x K) and w the weights (N x K) of a layer: its output is A = x (rows), B =
  * w (blocks); the gradient of x is A = the output's gradient (rows), B = w
  * transposed (blocks, transpose = 1); the gradient of w is A = the output's
