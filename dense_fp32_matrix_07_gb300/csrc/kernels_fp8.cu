@@ -46,7 +46,7 @@
 // goes to the teardown, which drains copies and MMAs.
 //
 // What bounds it, and what it measured (one GB300):
-//   16384 x 4096 x 4096, blocks form: 219 us, 2.51 PFLOP/s, 1.31 times the
+//   16384 x 4096 x 4096, blocks form: 217 us, 2.53 PFLOP/s, 1.33 times the
 //   measured bf16 rate. MMAs alone would take 512 cycles a K block (N = 256);
 //   it takes 830, the rest being the accumulator's round through commit,
 //   barrier, read, add and release, with two accumulators to overlap it.

@@ -94,7 +94,7 @@ constexpr int kRouteWarps = 8;
 // instructions (about 450 per warp of 128 experts and 8 rounds), not by the
 // logits' bytes. Fewer lanes with more logits each need fewer instructions a
 // token, but a longer chain of them: 8 lanes of 16 took 12.0 us for 16383
-// tokens and 11.8 us for 8 of them, 32 lanes of 4 take 10.7 us and 6.0 us.
+// tokens and 11.8 us for 8 of them, 32 lanes of 4 take 11.0 us and 5.9 us.
 template <class T, int L, int NPER>
 __global__ void __launch_bounds__(kRouteWarps * 32)
 route_kernel(int64_t tokens, int E, const T *__restrict__ logits, int64_t ld, int vec, const float *__restrict__ bias,
