@@ -41,11 +41,20 @@ EXPORTED_EXPERTS = ("sgemm_fp8_quantize_rows", "sgemm_fp8_quantize_cols", "sgemm
                     "sgemm_fp8_plan", "sgemm_route", "sgemm_route_backward", "sgemm_dispatch", "sgemm_combine",
                     "sgemm_combine_backward", "sgemm_test_fail_next_setups")
 
+# Every function declared in include/sgemm_layers.h.
+EXPORTED_LAYERS = ("sgemm_bf16", "sgemm_bf16_grouped", "sgemm_bf16_grouped_k", "sgemm_bf16_plan",
+                   "sgemm_epilogue_backward", "sgemm_rms_norm", "sgemm_rms_norm_backward")
+
 # Matrix types, scale forms of B, router scores and product modes of sgemm_experts.h.
 SGEMM_F32, SGEMM_BF16 = 0, 1
 SGEMM_SCALE_BLOCKS, SGEMM_SCALE_ROWS = 0, 1
 SGEMM_SCORE_SOFTMAX, SGEMM_SCORE_SIGMOID = 0, 1
 SGEMM_FP8_DENSE, SGEMM_FP8_GROUPED, SGEMM_FP8_GROUPED_K = 0, 1, 2
+
+# Activations, joins and product modes of sgemm_layers.h.
+SGEMM_ACT_NONE, SGEMM_ACT_RELU, SGEMM_ACT_GELU, SGEMM_ACT_GELU_TANH, SGEMM_ACT_SILU = 0, 1, 2, 3, 4
+SGEMM_JOIN_NONE, SGEMM_JOIN_ADD, SGEMM_JOIN_MUL = 0, 1, 2
+SGEMM_BF16_DENSE, SGEMM_BF16_GROUPED, SGEMM_BF16_GROUPED_K = 0, 1, 2
 
 _lock = threading.Lock()
 _lib = None
@@ -137,6 +146,18 @@ def load(rebuild: bool = False):
                 "sgemm_combine_backward": [_i64, i, _i64, _i64, _vp, i, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp,
                                            _vp],
                 "sgemm_test_fail_next_setups": [i],
+                "sgemm_bf16": [i, i, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, i, _vp, _i64, i, _vp, _i64, _vp, i,
+                               _i64, _vp],
+                "sgemm_bf16_grouped": [i, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64, i, _vp,
+                                       _i64, i, _vp, _i64, _vp, i, _i64, _vp],
+                "sgemm_bf16_grouped_k": [_i64, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, i, _vp, i, _i64, _i64, _vp],
+                "sgemm_bf16_plan": [i, _i64, _i64, _i64, _i64, i, _vp, _vp, _vp, _vp, _vp],
+                "sgemm_epilogue_backward": [_i64, _i64, i, _vp, _i64, _vp, _i64, i, i, _vp, _i64, _i64, _vp, _vp, _i64,
+                                            _vp, _i64, _vp, _i64, _vp],
+                "sgemm_rms_norm": [_i64, _i64, i, _vp, _i64, _vp, _i64, _vp, f, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
+                                   _i64, _vp],
+                "sgemm_rms_norm_backward": [_i64, _i64, i, _vp, _i64, _vp, _i64, _vp, f, _vp, _i64, _vp, _i64, _vp,
+                                            _vp],
             }.items():
                 getattr(lib, name).restype = ctypes.c_int
                 getattr(lib, name).argtypes = args
@@ -366,3 +387,59 @@ def sgemm_combine_backward(T, k, cols, rows, grad_out, type, ld_go, Y, ldy, row_
 def sgemm_test_fail_next_setups(n) -> int:
     """Test hook: the next `n` set-ups of the kernels above are treated as failed (host only)."""
     return load().sgemm_test_fail_next_setups(n)
+
+
+# ---------------------------------------------------------------------------
+# include/sgemm_layers.h: 16-bit products with an epilogue, its gradient, the
+# root-mean-square norm. Arguments and status codes as there.
+
+
+def sgemm_bf16(op_a, op_b, M, N, K, A, lda, B, ldb, bias, act, pre, ld_pre, join, D, ldd, C, c_type, ldc,
+               stream=0) -> int:
+    """C = act(op(A) . op(B) + bias), plus or times D, on bfloat16 A and B."""
+    return load().sgemm_bf16(op_a, op_b, M, N, K, A, lda, B, ldb, bias, act, pre, ld_pre, join, D, ldd, C, c_type, ldc,
+                             stream)
+
+
+def sgemm_bf16_grouped(op_b, groups, offsets, rows, N, K, A, lda, B, ldb, stride_b, bias, stride_bias, act, pre, ld_pre,
+                       join, D, ldd, C, c_type, ldc, stream=0) -> int:
+    """sgemm_bf16() of each group of rows of A with its own B and bias: the experts' products."""
+    return load().sgemm_bf16_grouped(op_b, groups, offsets, rows, N, K, A, lda, B, ldb, stride_b, bias, stride_bias,
+                                     act, pre, ld_pre, join, D, ldd, C, c_type, ldc, stream)
+
+
+def sgemm_bf16_grouped_k(groups, offsets, rows, M, N, A, lda, B, ldb, accumulate, C, c_type, ldc, stride_c,
+                         stream=0) -> int:
+    """A_g^T . B_g over each group's rows: the experts' weight gradients."""
+    return load().sgemm_bf16_grouped_k(groups, offsets, rows, M, N, A, lda, B, ldb, accumulate, C, c_type, ldc,
+                                       stride_c, stream)
+
+
+def sgemm_bf16_plan(mode, groups, M, N, K, num_sms):
+    """Host-only: (status, columns, pair, swap, split, grid) of the kernel a 16-bit product takes."""
+    cols, pair, swap, split = (ctypes.c_int(-1) for _ in range(4))
+    grid = ctypes.c_int64(-1)
+    rc = load().sgemm_bf16_plan(mode, groups, M, N, K, num_sms, *(ctypes.addressof(x) for x in
+                                                                  (cols, pair, swap, split, grid)))
+    return rc, cols.value, pair.value, swap.value, split.value, grid.value
+
+
+def sgemm_epilogue_backward(rows, cols, type, grad_out, ld_go, pre, ld_pre, act, join, D, ldd, groups, offsets,
+                            grad_pre, ld_gp, grad_D, ld_gd, grad_bias, stride_gb, stream=0) -> int:
+    """Gradients of a product's epilogue: of its sums, of the factor D, and of the bias per group of rows."""
+    return load().sgemm_epilogue_backward(rows, cols, type, grad_out, ld_go, pre, ld_pre, act, join, D, ldd, groups,
+                                          offsets, grad_pre, ld_gp, grad_D, ld_gd, grad_bias, stride_gb, stream)
+
+
+def sgemm_rms_norm(rows, cols, type, x, ldx, residual, ld_res, weight, eps, sum, ld_sum, y, ldy, q, ldq, scales, lds,
+                   stream=0) -> int:
+    """x + residual, and its rows over their root mean square times weight, in `type` and in 8 bits."""
+    return load().sgemm_rms_norm(rows, cols, type, x, ldx, residual, ld_res, weight, eps, sum, ld_sum, y, ldy, q, ldq,
+                                 scales, lds, stream)
+
+
+def sgemm_rms_norm_backward(rows, cols, type, grad_y, ld_gy, s, ld_s, weight, eps, grad_sum, ld_gsum, grad_s, ld_gs,
+                            grad_weight, stream=0) -> int:
+    """Gradients of sgemm_rms_norm() with respect to the sum and the weight."""
+    return load().sgemm_rms_norm_backward(rows, cols, type, grad_y, ld_gy, s, ld_s, weight, eps, grad_sum, ld_gsum,
+                                          grad_s, ld_gs, grad_weight, stream)

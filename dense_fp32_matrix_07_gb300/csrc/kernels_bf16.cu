@@ -1,0 +1,1143 @@
+// Products of bfloat16 operands on the 5th-generation tensor cores, with an
+// epilogue:
+//
+//   z[m, n] = sum_k op(A)[m, k] op(B)[k, n] + bias[n]     (pre = z on request)
+//   C[m, n] = act(z[m, n])  [+ D[m, n]  or  * D[m, n]]
+//
+// dense, over groups of rows of A with a B (and bias) each, or over each
+// group's rows as K (tcgen05.mma .kind::f16, FP32 sums in tensor memory). The
+// epilogue is FP32, with one rounding as C and pre are stored. The tensor
+// cores cut the sums off after each 16 of K instead of rounding them, which
+// adds up along K (relative errors of 1.7e-6 at K = 2049, 4.4e-6 at 4096); it
+// is far below a bfloat16 C's rounding, but an FP32 C is summed in tensor
+// memory over 512 of K at a time, and these sums in FP32 registers.
+//
+// A tile has 128 (or, by a pair of CTAs, 256) lanes of tensor memory, which
+// hold rows of C, and BN columns, which hold columns of C; with `swap` it is
+// the other way round, so that few rows of A cost few columns and each value
+// of B is read once. Operands come by TMA in slabs of 64 along K with the
+// 128-byte swizzle: one box where K is contiguous, boxes of 64 x 64 where the
+// rows (or columns) of C are; the MMA reads either from its descriptor.
+//
+// Roles of a CTA:
+//   warp 0      TMA producer, full/done barrier per stage;
+//   warp 1      TMEM owner and MMA issuer, two accumulators;
+//   warp 2      finds the CTA's tiles, up to four ahead, for all;
+//   warp 3      over groups' rows as K: zeroes the rows of a group's last slab
+//               that are the next group's (infinities and NaN there must not
+//               meet this group's), as far as an MMA of 16 reads them;
+//   warps 4..   epilogue: warp 4 + i reads lanes 32 (i % 4) .. of columns
+//               (i / 4) * CW .., 32 columns at a time, which turn in shared
+//               memory so that D, pre and C are accessed along rows.
+//
+// Pairs (cta_group::2): each CTA loads its 128 rows of the lanes' operand and
+// half of the columns' operand, and the first CTA's MMA warp issues for both.
+// Few tiles: `split` CTAs of a cluster share a tile's K slabs; each sends its
+// partial sums of column j to the CTA j % split, which adds them in rank order
+// after a cluster barrier: the result does not depend on timing.
+//
+// Every wait is bounded; a role that gives up sets the device error word and
+// goes to the teardown, which drains copies and MMAs.
+#include "common.cuh"
+#include "layers.cuh"
+#include "ptx.cuh"
+#include "tc_roles.cuh"
+
+namespace sgemm_gb300 {
+
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kSlab = 64;        // K values per stage: 128 bytes of a row
+constexpr int kPart = 8;         // slabs that an FP32 C is summed over in tensor memory
+constexpr int kItems = 4;        // tiles found ahead of their sums
+constexpr int kItemBytes = 32;
+constexpr int kStaging = 4096;   // 32 x 32 floats on their way to C
+constexpr int kRaster = 16;      // row tiles walked together, so that a wave of CTAs shares both operands in L2
+
+template <int BN_, bool PAIR_>
+struct Bf16Cfg {
+    static constexpr int BN = BN_;
+    static constexpr bool PAIR = PAIR_;
+    static constexpr int CTAS = PAIR ? 2 : 1;
+    static constexpr int LANES = 128 * CTAS;
+    static constexpr int QR = BN / CTAS;                           // rows of the columns' operand a CTA loads
+    static constexpr int P_TILE = 128 * 128;
+    static constexpr int Q_TILE = (QR < 64 ? 64 : QR) * 128;       // a box of 64 x 64 at least
+    static constexpr int STAGE_BYTES = P_TILE + Q_TILE;
+    static constexpr int STAGES = PAIR ? (BN == 256 ? 5 : 7) : BN == 128 ? 4 : BN == 64 ? 7 : 8;
+    static constexpr int NBUF = 2;
+    static constexpr int TMEM_COLS = NBUF * BN < 32 ? 32 : NBUF * BN;
+    static constexpr int EPI_WARPS = BN >= 128 ? 8 : 4;
+    static constexpr int CW = BN / (EPI_WARPS / 4);                // columns per epilogue warp
+    static constexpr int CHUNK = CW < 32 ? 16 : 32;
+    static constexpr int THREADS = 128 + 32 * EPI_WARPS;
+    // Registers move from the first four warps to the eight of the epilogue:
+    // 168 * 384 at launch, 72 * 128 + 216 * 256 after.
+    static constexpr bool MOVE_REGS = EPI_WARPS == 8;
+    static constexpr bool CAN_SPLIT = !PAIR;
+    // Partial sums of a split tile lie where whole tiles are staged.
+    static constexpr int PARTIAL = CAN_SPLIT ? BN * 128 * 4 : 0;
+    static constexpr int EXTRA = PARTIAL > EPI_WARPS * kStaging ? PARTIAL : EPI_WARPS * kStaging;
+    static constexpr int NUM_BARS = 3 * STAGES + 2 * NBUF + 2 * kItems + 1;
+    static constexpr int OFF_EXTRA = STAGES * STAGE_BYTES;
+    static constexpr int OFF_ITEMS = OFF_EXTRA + EXTRA;
+    static constexpr int OFF_TABLE = OFF_ITEMS + kItems * kItemBytes;
+    static constexpr int OFF_BARS = OFF_TABLE + (kMaxGroups + 2) * 4;
+    static constexpr int SMEM_BYTES = 1024 + OFF_BARS + NUM_BARS * 8 + 16;
+    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
+    static_assert(TMEM_COLS <= 512 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "tensor memory columns");
+    static_assert(OFF_BARS % 8 == 0 && STAGE_BYTES % 1024 == 0, "alignment");
+};
+
+struct Bf16Params {
+    int mode, swap;
+    int M, N, K;                 // GroupK: K = rows of both operands
+    int p_mn, q_mn;              // the operand's rows (not K) are contiguous
+    int groups;
+    const int32_t *offsets;
+    int tm, tn;                  // rows and columns of C per tile
+    int row_tiles, col_tiles;    // (grouped rows: row tiles from the table)
+    FastDiv by_cols, by_group;   // col_tiles; tiles of one group (GroupK)
+    int split;
+    const float *bias;
+    int64_t stride_bias;
+    int act, join;
+    void *pre;
+    int64_t ld_pre;
+    const void *D;
+    int64_t ldd;
+    void *C;
+    int64_t ldc, stride_c;
+    int c_bf16;
+    int vec;                     // C, pre and D in whole 16-byte pieces
+    unsigned int *status;
+};
+
+// The same value in all lanes, known to the compiler as such (what an MMA or a
+// copy takes lies in registers that the warp shares: 75 cycles per MMA to
+// bring it there where the compiler cannot tell).
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(kAll, x, 0); }
+
+// One tile: its group, rows [m, m_end) and first column of C, its range of K.
+struct Item {
+    int group, m, m_end, n, k0, k1, more;
+};
+
+__device__ __forceinline__ void store_item(uint32_t at, const Item &w)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w.group), "r"(w.m), "r"(w.m_end), "r"(w.n)
+                 : "memory");
+    asm volatile("st.shared.v4.u32 [%0+16], {%1,%2,%3,%3};" ::"r"(at), "r"(w.k0), "r"(w.k1), "r"(w.more) : "memory");
+}
+
+__device__ __forceinline__ Item load_item(uint32_t at)
+{
+    Item w;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w.group), "=r"(w.m), "=r"(w.m_end), "=r"(w.n)
+                 : "r"(at)
+                 : "memory");
+    asm volatile("{\n\t.reg .u32 x;\n\tld.shared.v4.u32 {%0,%1,%2,x}, [%3+16];\n\t}"
+                 : "=r"(w.k0), "=r"(w.k1), "=r"(w.more)
+                 : "r"(at)
+                 : "memory");
+    w.group = uniform(w.group), w.m = uniform(w.m), w.m_end = uniform(w.m_end), w.n = uniform(w.n);
+    w.k0 = uniform(w.k0), w.k1 = uniform(w.k1), w.more = uniform(w.more);
+    return w;
+}
+
+__device__ __forceinline__ int slabs(int k0, int k1) { return (int)(((uint32_t)(k1 - k0) + kSlab - 1) / kSlab); }
+
+__device__ __forceinline__ Item find_item(const Bf16Params &p, const int *table, uint32_t t, int rank)
+{
+    Item it;
+    it.group = it.more = 0;
+    int rows = p.row_tiles;
+    if (p.mode == kBf16GroupRows) rows = table[p.groups];
+    if (p.mode == kBf16GroupK) {
+        it.group = (int)div(t, p.by_group);
+        t -= it.group * p.by_group.d;
+    }
+    // Bands of kRaster row tiles, the row tile fastest.
+    const uint32_t band = div(t / kRaster, p.by_cols), first = band * kRaster;
+    const uint32_t r = t - first * p.col_tiles;
+    const uint32_t high = rows - first < (uint32_t)kRaster ? rows - first : kRaster;
+    const uint32_t ct = high == kRaster ? r / kRaster : r / high;
+    const int rt = (int)(first + r - ct * high);
+    it.n = (int)ct * p.tn;
+    it.k0 = 0;
+    it.k1 = p.K;
+    if (p.mode == kBf16GroupRows) {
+        it.group = find_group(table, p.groups, rt);
+        int lo, hi;
+        group_range(p.offsets, it.group, p.M, lo, hi);
+        it.m = lo + (rt - table[it.group]) * p.tm;
+        it.m_end = hi;
+    } else {
+        it.m = rt * p.tm;
+        it.m_end = p.M;
+        if (p.mode == kBf16GroupK) group_range(p.offsets, it.group, p.K, it.k0, it.k1);
+    }
+    if (p.split > 1) {
+        const int n = slabs(0, p.K);
+        const int64_t k1 = (int64_t)((int64_t)n * (rank + 1) / p.split) * kSlab;
+        it.k0 = (int)((int64_t)n * rank / p.split) * kSlab;
+        it.k1 = k1 < p.K ? (int)k1 : p.K;
+    }
+    return it;
+}
+
+// The address of `addr` in the shared memory of the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t map_shared(uint32_t addr, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+// As tma_load_if() and mbar_expect_if(), for a pair: the barrier may be the
+// other CTA's (an address of shared::cluster).
+__device__ __forceinline__ void tma_load_pair_if(uint32_t on, uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t x,
+                                                 int32_t y, int32_t z, uint64_t policy)
+{
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %7, 0;\n\t"
+                 "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+                 ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;\n\t}" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy), "r"(on)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mbar_expect_cluster_if(uint32_t on, uint32_t bar, uint32_t bytes)
+{
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
+                 "@q mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+                 "r"(bytes), "r"(on)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_cluster_if(uint32_t on, uint32_t bar)
+{
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+                 "@q mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar),
+                 "r"(on)
+                 : "memory");
+}
+
+// The commit's arrival at the barrier of both CTAs of the pair.
+__device__ __forceinline__ void mma_commit_pair_if(uint32_t on, uint32_t bar)
+{
+    asm volatile("{\n\t.reg .pred q;\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+                 "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::
+                     "r"(bar),
+                 "r"(on)
+                 : "memory");
+}
+
+// Waits for phase `parity` of the barrier, unless it was `early` seen to be
+// complete; false after about ptx::kWaitLimitNs. The clock is read after 64
+// probes only: reading it costs more than the usual wait.
+__device__ __forceinline__ bool wait_bar(uint32_t early, uint32_t bar, uint32_t parity)
+{
+    if (__builtin_expect(__all_sync(kAll, early) != 0, 1)) return true;
+    bool ok = false;
+    uint64_t t0 = 0;
+    for (uint32_t n = 0; !ok && n < kSpinLimit; ++n) {
+#pragma unroll 1
+        for (int r = 0; !ok && r < 64; ++r) ok = ptx::mbar_try_wait(bar, parity);
+        if (ok) break;
+        const uint64_t t = ptx::global_timer_ns();
+        if (n == 0) t0 = t;
+        else if (t - t0 > ptx::kWaitLimitNs) break;
+    }
+    return __all_sync(kAll, ok) != 0;
+}
+
+// A wait for what may take as long as a tile of nk slabs.
+__device__ __forceinline__ bool wait_tile(uint32_t bar, uint32_t parity, int nk)
+{
+    if (wait_bar(mbar_test(bar, parity), bar, parity)) return true;
+    for (int k = nk >> 16; k > 0; --k)
+        if (wait_bar(0, bar, parity)) return true;
+    return false;
+}
+
+// D (+)= P . Q^T on bfloat16 operands, given the descriptors' lower words (the
+// upper ones are the same for both).
+template <bool PAIR>
+__device__ __forceinline__ void mma_bf16_if(uint32_t on, uint32_t d_tmem, uint32_t p_desc, uint32_t q_desc, uint32_t upper,
+                                            uint32_t idesc, uint32_t accumulate)
+{
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+            "setp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 q, %6, 0;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+            "r"(p_desc), "r"(q_desc), "r"(upper), "r"(idesc), "r"(accumulate), "r"(on)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+            "setp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 q, %6, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+            "r"(p_desc), "r"(q_desc), "r"(upper), "r"(idesc), "r"(accumulate), "r"(on)
+            : "memory");
+}
+
+// Instruction descriptor of .kind::f16: FP32 accumulation (bits 4-5 = 1), both
+// operands bfloat16 (bits 7-9 and 10-12 = 1), K or the rows contiguous (bits
+// 15 and 16), N >> 3 at bits 17-22, M >> 4 at bits 24-28.
+__device__ __forceinline__ uint32_t idesc_bf16(int m, int n, int p_mn, int q_mn)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)p_mn << 15) | ((uint32_t)q_mn << 16) |
+           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// Shared-memory descriptor of an operand in boxes of 64 (contiguous rows) by
+// 64 (along K), 128-byte swizzle: 8192 bytes from one 64 rows to the next
+// (leading offset), 1024 from 8 values of K to the next (stride).
+__device__ __forceinline__ uint64_t sdesc_rows(uint32_t smem_addr)
+{
+    return (uint64_t)((smem_addr & 0x3FFFFu) >> 4) | ((uint64_t)(8192 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols)
+{
+    if constexpr (PAIR) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        ptx::tmem_alloc(slot, cols);
+    }
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t cols)
+{
+    if constexpr (PAIR)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
+    else
+        ptx::tmem_dealloc(taddr, cols);
+}
+
+// ------------------------------------------------------------------- epilogue
+
+// Where the rows of a tile lie in C, pre and D, and its group's bias.
+template <class T>
+struct Place {
+    T *C, *pre;
+    const T *D;
+    const float *bias;
+};
+
+template <class T>
+__device__ __forceinline__ Place<T> place_of(const Bf16Params &p, int group)
+{
+    const int64_t base = p.mode == kBf16GroupK ? group * p.stride_c : 0;
+    Place<T> q;
+    q.C = static_cast<T *>(p.C) + base;
+    q.pre = p.pre ? static_cast<T *>(p.pre) : nullptr;
+    q.D = p.join != kJoinNone ? static_cast<const T *>(p.D) + base : nullptr;
+    q.bias = p.bias ? p.bias + (p.mode == kBf16GroupRows ? group * p.stride_bias : 0) : nullptr;
+    return q;
+}
+
+__device__ __forceinline__ float joined(float y, float d, int join)
+{
+    return join == kJoinAdd ? y + d : join == kJoinMul ? y * d : y;
+}
+
+// One element (m, n) of C from its sum.
+template <class T>
+__device__ __forceinline__ void store_one(const Bf16Params &p, const Place<T> &q, int64_t m, int n, float z)
+{
+    if (q.bias) z += __ldg(q.bias + n);
+    if (q.pre) store_from_float(q.pre + m * p.ld_pre + n, z);
+    float y = activate(z, p.act);
+    if (q.D) y = joined(y, load_as_float(q.D + m * p.ldd + n), p.join);
+    store_from_float(q.C + m * p.ldc + n, y);
+}
+
+// Staging of R x COLS sums of C, rows of 128 bytes, their 16-byte pieces
+// exchanged by row: element (r, c).
+__device__ __forceinline__ uint32_t staged(uint32_t st, int r, int c)
+{
+    return st + 128 * r + 16 * ((c >> 2) ^ (r & 7)) + 4 * (c & 3);
+}
+
+// Staged values z to act(z), 4 at a time.
+template <int R, int COLS>
+__device__ __forceinline__ void activate_staged(uint32_t st, int lane, int act)
+{
+    constexpr int PER_ROW = COLS / 4, PER_PASS = 32 / PER_ROW;
+#pragma unroll 2
+    for (int r = lane / PER_ROW; r < R; r += PER_PASS) {
+        const uint32_t at = staged(st, r, 4 * (lane % PER_ROW));
+        uint4 u = ld_shared_u32x4(at);
+        float z[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[e] = activate(z[e], act);
+        st_shared_u32x4(at, make_uint4(__float_as_uint(z[0]), __float_as_uint(z[1]), __float_as_uint(z[2]),
+                                       __float_as_uint(z[3])));
+    }
+}
+
+// A chunk of the warp's sums, which get() gives (column j of this lane in
+// v[j]): through staging to rows m .. of C, columns n .. (`rows` and `cols` of
+// them exist), V values of a row per access. D is requested before the sums.
+template <class T, int CHUNK, bool SWAP, int V, class Get>
+__device__ __forceinline__ void store_chunk(const Bf16Params &p, const Place<T> &q, uint32_t st, int lane, Get get, int64_t m,
+                                            int rows, int n, int cols)
+{
+    constexpr int R = SWAP ? CHUNK : 32, COLS = SWAP ? 32 : CHUNK;
+    constexpr int PER_ROW = COLS / V, PER_PASS = 32 / PER_ROW, PASSES = R / PER_PASS;
+    constexpr int MOST = sizeof(T) == 4 && V > 1 ? 4 : 8;
+    constexpr int AHEAD = PASSES < MOST ? PASSES : MOST;      // accesses of D under way
+    const int r0 = lane / PER_ROW, c0 = (lane % PER_ROW) * V;
+    const bool whole = V == 1 ? c0 < cols : c0 + V <= cols;
+    Values<T, V> d[AHEAD];
+    auto fetch = [&](int i0) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int r = r0 + (i0 + i) * PER_PASS;
+            if (whole && r < rows) d[i] = *reinterpret_cast<const Values<T, V> *>(q.D + (m + r) * p.ldd + n + c0);
+        }
+    };
+    auto read = [&](int r, float (&z)[V]) {
+        if constexpr (V == 1) {
+            z[0] = ld_shared_f32(staged(st, r, c0));
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; e += 4) {
+                const uint4 u = ld_shared_u32x4(staged(st, r, c0 + e));
+                z[e] = __uint_as_float(u.x), z[e + 1] = __uint_as_float(u.y);
+                z[e + 2] = __uint_as_float(u.z), z[e + 3] = __uint_as_float(u.w);
+            }
+        }
+    };
+    if (q.D) fetch(0);
+    // The bias of column n + lane.
+    float b = 0.0f;
+    if (q.bias && lane < (COLS < cols ? COLS : cols)) b = __ldg(q.bias + n + lane);
+    {
+        uint32_t v[CHUNK];
+        get(v);
+        if constexpr (SWAP) {
+#pragma unroll
+            for (int j = 0; j < CHUNK; ++j)
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(staged(st, j, lane)), "f"(__uint_as_float(v[j]) + b) : "memory");
+        } else {
+            if (q.bias) {
+#pragma unroll
+                for (int j = 0; j < CHUNK; ++j)
+                    v[j] = __float_as_uint(__uint_as_float(v[j]) + __shfl_sync(kAll, b, j));
+            }
+#pragma unroll
+            for (int j = 0; j < CHUNK; j += 4)
+                st_shared_u32x4(staged(st, lane, j), make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]));
+        }
+    }
+    __syncwarp();
+    if (q.pre) {
+#pragma unroll 4
+        for (int r = r0; r < R; r += PER_PASS) {
+            if (r >= rows) break;
+            T *to = q.pre + (m + r) * p.ld_pre + n + c0;
+            if (whole) {
+                float z[V];
+                read(r, z);
+                Values<T, V> o;
+#pragma unroll
+                for (int e = 0; e < V; ++e) store_from_float(&o.v[e], z[e]);
+                *reinterpret_cast<Values<T, V> *>(to) = o;
+            } else {
+#pragma unroll 1
+                for (int e = 0; e < cols - c0; ++e) store_from_float(to + e, ld_shared_f32(staged(st, r, c0 + e)));
+            }
+        }
+    }
+    if (p.act != kActNone) {
+        __syncwarp();
+        activate_staged<R, COLS>(st, lane, p.act);
+        __syncwarp();
+    }
+#pragma unroll 1
+    for (int i0 = 0; i0 < PASSES; i0 += AHEAD) {
+        if (i0 > 0 && q.D) fetch(i0);
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int r = r0 + (i0 + i) * PER_PASS;
+            if (r >= rows) continue;
+            T *to = q.C + (m + r) * p.ldc + n + c0;
+            if (whole) {
+                float z[V];
+                read(r, z);
+                if (q.D) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) z[e] = joined(z[e], load_as_float(&d[i].v[e]), p.join);
+                }
+                Values<T, V> o;
+#pragma unroll
+                for (int e = 0; e < V; ++e) store_from_float(&o.v[e], z[e]);
+                *reinterpret_cast<Values<T, V> *>(to) = o;
+            } else {
+                const T *from = q.D ? q.D + (m + r) * p.ldd + n + c0 : nullptr;
+#pragma unroll 1
+                for (int e = 0; e < cols - c0; ++e) {
+                    const float y = ld_shared_f32(staged(st, r, c0 + e));
+                    store_from_float(to + e, from ? joined(y, load_as_float(from + e), p.join) : y);
+                }
+            }
+        }
+    }
+    __syncwarp();
+}
+
+// A warp's part of a tile: CW columns from the tile's column col0 on. get(c, v)
+// gives the chunk from its column c on.
+template <class T, class Cfg, bool SWAP, class Get>
+__device__ __forceinline__ void store_part(const Bf16Params &p, const Item &w, uint32_t st, int lane, int lane0, int col0,
+                                           Get get)
+{
+    constexpr int CHUNK = Cfg::CHUNK, V = 16 / (int)sizeof(T);
+    const Place<T> q = place_of<T>(p, w.group);
+#pragma unroll 1
+    for (int c = 0; c < Cfg::CW; c += CHUNK) {
+        const int m = w.m + (SWAP ? col0 + c : lane0), n = w.n + (SWAP ? lane0 : col0 + c);
+        const int rows = w.m_end - m, cols = p.N - n;
+        if (rows <= 0 || cols <= 0) continue;
+        auto chunk = [&](uint32_t (&v)[CHUNK]) { get(c, v); };
+        if (p.vec)
+            store_chunk<T, CHUNK, SWAP, V>(p, q, st, lane, chunk, m, rows, n, cols);
+        else
+            store_chunk<T, CHUNK, SWAP, 1>(p, q, st, lane, chunk, m, rows, n, cols);
+    }
+}
+
+template <class Cfg>
+__global__ void __launch_bounds__(Cfg::THREADS, 1)
+bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_constant__ CUtensorMap mapQ,
+                    const __grid_constant__ Bf16Params p)
+{
+    constexpr int BN = Cfg::BN, STAGES = Cfg::STAGES, NBUF = Cfg::NBUF, CW = Cfg::CW, QR = Cfg::QR;
+    constexpr bool PAIR = Cfg::PAIR;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    int *const table = reinterpret_cast<int *>(smem_raw + (base - raw) + Cfg::OFF_TABLE);
+    const uint32_t bars = base + Cfg::OFF_BARS;
+    auto stage_p = [&](int s) { return base + s * Cfg::STAGE_BYTES; };
+    auto stage_q = [&](int s) { return base + s * Cfg::STAGE_BYTES + Cfg::P_TILE; };
+    auto full_bar = [&](int s) { return bars + 8u * s; };
+    auto done_bar = [&](int s) { return bars + 8u * (STAGES + s); };
+    auto accf_bar = [&](int b) { return bars + 8u * (2 * STAGES + b); };
+    auto acce_bar = [&](int b) { return bars + 8u * (2 * STAGES + NBUF + b); };
+    auto ifull_bar = [&](uint32_t i) { return bars + 8u * (2 * STAGES + 2 * NBUF + i); };
+    auto iempty_bar = [&](uint32_t i) { return bars + 8u * (2 * STAGES + 2 * NBUF + kItems + i); };
+    auto tail_bar = [&](int s) { return bars + 8u * (2 * STAGES + 2 * NBUF + 2 * kItems + s); };
+    const uint32_t drain_bar = bars + 8u * (3 * STAGES + 2 * NBUF + 2 * kItems);
+    const uint32_t tmem_slot = bars + 8u * Cfg::NUM_BARS;
+
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int split = Cfg::CAN_SPLIT ? p.split : 1;
+    const int cluster = PAIR ? 2 : split;
+    const int rank = cluster > 1 ? (int)ptx::cluster_ctarank() : 0;
+    if (cluster > 1 && ptx::cluster_nctarank() != (uint32_t)cluster) {
+        // Launched without its cluster, it would reach for peers that do not exist.
+        if (threadIdx.x == 0) atomicOr(p.status, kStatusLaunchConfig);
+        return;
+    }
+    const bool group_k = p.mode == kBf16GroupK;
+
+    if (warp == 2 && lane == 0) {
+        ptx::prefetch_tensormap(&mapP);
+        ptx::prefetch_tensormap(&mapQ);
+    }
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            ptx::mbar_init(full_bar(s), Cfg::CTAS);   // the producer (or the last slab's warp 3) of each CTA
+            ptx::mbar_init(done_bar(s), 1);
+            ptx::mbar_init(tail_bar(s), 1);
+        }
+        for (int b = 0; b < NBUF; ++b) {
+            ptx::mbar_init(accf_bar(b), 1);
+            ptx::mbar_init(acce_bar(b), Cfg::CTAS * Cfg::EPI_WARPS);
+        }
+        for (int i = 0; i < kItems; ++i) {
+            // Read by the producer, the MMA issuer, the epilogue and, over groups' K, warp 3.
+            ptx::mbar_init(ifull_bar(i), 1);
+            ptx::mbar_init(iempty_bar(i), Cfg::EPI_WARPS + (group_k ? 3 : 2));
+        }
+        ptx::mbar_init(drain_bar, 1);
+        ptx::mbar_init_fence();
+    }
+    if (warp == 1) tmem_alloc<PAIR>(tmem_slot, Cfg::TMEM_COLS);
+    if (p.mode == kBf16GroupRows) {
+        // table[g] = row tiles of the groups before g.
+        for (int g = threadIdx.x; g < p.groups; g += Cfg::THREADS) {
+            int lo, hi;
+            group_range(p.offsets, g, p.M, lo, hi);
+            table[g] = (int)(((uint32_t)(hi - lo) + (uint32_t)p.tm - 1) / (uint32_t)p.tm);
+        }
+        __syncthreads();
+        if (warp == 0) {
+            // Offsets that are not a partition may sum to anything: no entry
+            // passes what the kernel can walk.
+            const uint32_t most = (uint32_t)(INT32_MAX / p.col_tiles - 2 * kRaster);
+            const uint32_t held = most < (1u << 26) ? most : 1u << 26;
+            uint32_t carry = 0;
+            for (int g0 = 0; g0 < p.groups; g0 += 32) {
+                const int g = g0 + lane;
+                const uint32_t mine = g < p.groups ? table[g] : 0;
+                uint32_t sum = mine < held ? mine : held;
+#pragma unroll
+                for (int d = 1; d < 32; d *= 2) {
+                    const uint32_t up = __shfl_up_sync(kAll, sum, d);
+                    if (lane >= d) sum = sum + up < held ? sum + up : held;
+                }
+                const uint32_t end = carry + sum < held ? carry + sum : held;
+                const uint32_t before = __shfl_up_sync(kAll, end, 1);
+                if (g < p.groups) table[g] = (int)(lane == 0 ? carry : before);
+                carry = __shfl_sync(kAll, end, 31);
+                if (g0 + 32 >= p.groups && lane == 0) table[p.groups] = (int)carry;
+            }
+        }
+    }
+    ptx::tc_fence_before();
+    // A pair's barriers and tensor memory are there in both CTAs before either goes on.
+    if constexpr (PAIR) ptx::cluster_sync_all();
+    else __syncthreads();
+    ptx::tc_fence_after();
+    // The CTAs of a split tile write into each other's shared memory in the
+    // end: each says that it has begun, and waits for the others before that.
+    if (Cfg::CAN_SPLIT && split > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    const uint32_t taddr = *reinterpret_cast<uint32_t *>(smem_raw + (tmem_slot - raw));
+
+    const uint32_t t_first = blockIdx.x / cluster, t_step = gridDim.x / cluster;
+    uint32_t tiles = (uint32_t)p.col_tiles * (uint32_t)(p.mode == kBf16Dense       ? p.row_tiles
+                                                        : p.mode == kBf16GroupRows ? table[p.groups]
+                                                                                   : p.row_tiles * p.groups);
+    if (split > 1 && tiles > t_step) tiles = t_step;   // a split grid has one tile per cluster
+
+    // The CTA's nth tile, once warp 2 has found it; not to be read after done_with().
+    const int longest = slabs(0, p.K);
+    auto item_at = [&](uint32_t n) { return base + Cfg::OFF_ITEMS + (n % kItems) * kItemBytes; };
+    auto item_there = [&](uint32_t n) {
+        const uint32_t bar = ifull_bar(n % kItems), phase = (n / kItems) & 1;
+        return wait_tile(bar, phase, longest);
+    };
+    auto done_with = [&](uint32_t n) {
+        __syncwarp();
+        mbar_arrive_if(lane == 0, iempty_bar(n % kItems));
+    };
+    auto gave_up = [&]() {
+        if (lane == 0) atomicOr(p.status, kStatusTimeout);
+    };
+    // K that an accumulator takes before it is handed on.
+    const int part = p.c_bf16 && split == 1 ? INT32_MAX : kPart * kSlab;
+    // Where this CTA's lanes and its rows of the columns' operand begin.
+    const int pair_rank = PAIR ? rank : 0;
+
+    if constexpr (Cfg::MOVE_REGS) {
+        if (warp < 4) ptx::setmaxnreg_dec<72>();
+    }
+    if (warp == 0) {
+        // ------------------------------ TMA producer ------------------------------
+        const uint32_t on = elect_one();
+        const uint64_t policy = ptx::policy_evict_last();
+        // Boxes of 64 rows (or columns of C) by 64 along K, or fewer rows for
+        // a narrow operand whose K is contiguous: the same number of copies
+        // whichever is, so that the loop has no branches but its own.
+        constexpr int Q_BOXES = QR > 64 ? QR / 64 : 1;
+        const uint32_t bytes = Cfg::P_TILE + (p.q_mn || QR >= 64 ? Q_BOXES * 8192 : QR * 128);
+        const bool p_mn = p.p_mn, q_mn = p.q_mn;
+        auto load = [&](uint32_t dst, const CUtensorMap *map, uint32_t bar, bool mn, int row, int k, int z) {
+            const int x = mn ? row : k, y = mn ? k : row;
+            if constexpr (PAIR) tma_load_pair_if(on, dst, map, bar, x, y, z, policy);
+            else tma_load_if(on, dst, map, bar, x, y, z, policy);
+        };
+        uint32_t it = 0, n = 0, early = 1;
+        bool ok = true;
+        for (uint32_t t = t_first; ok && t < tiles; t += t_step, ++n) {
+            if (!item_there(n)) {
+                gave_up();
+                break;
+            }
+            const Item w = load_item(item_at(n));
+            done_with(n);
+            const int z = p.mode == kBf16GroupRows ? w.group : 0;
+            const int pz = p.swap ? z : 0, qz = p.swap ? 0 : z;
+            const int p_row = (p.swap ? w.n : w.m) + 128 * pair_rank, q_row = (p.swap ? w.m : w.n) + QR * pair_rank;
+            for (int k = w.k0; k < w.k1; k += kSlab, ++it) {
+                const int s = (int)(it % STAGES);
+                if (!wait_bar(early, done_bar(s), ((it / STAGES) & 1) ^ 1)) {
+                    gave_up();
+                    ok = false;
+                    break;
+                }
+                // A group's last rows go to warp 3 first.
+                const bool tail = group_k && w.k1 - k < kSlab;
+                uint32_t bar = tail ? tail_bar(s) : full_bar(s);
+                if constexpr (PAIR) {
+                    bar = map_shared(bar, tail ? rank : 0);
+                    mbar_expect_cluster_if(on, bar, bytes);
+                } else {
+                    mbar_expect_if(on, bar, bytes);
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) load(stage_p(s) + 8192 * c, &mapP, bar, p_mn, p_row + 64 * c, k, pz);
+#pragma unroll
+                for (int c = 0; c < Q_BOXES; ++c) load(stage_q(s) + 8192 * c, &mapQ, bar, q_mn, q_row + 64 * c, k, qz);
+                const uint32_t next = it + 1;
+                early = mbar_test(done_bar((int)(next % STAGES)), ((next / STAGES) & 1) ^ 1);
+            }
+        }
+        // Every byte bound for this CTA lands before it leaves: its MMAs wait
+        // for all of them, and the last of each stage are done with.
+        for (uint32_t back = 0; back < STAGES && back < it; ++back) {
+            const uint32_t i = it - 1 - back;
+            if (!wait_bar(0, done_bar((int)(i % STAGES)), (i / STAGES) & 1)) gave_up();
+        }
+    } else if (warp == 1) {
+        // ------------------------------ MMA issuer ------------------------------
+        const uint32_t idesc = idesc_bf16(Cfg::LANES, BN, p.p_mn, p.q_mn);
+        const uint64_t desc_p = p.p_mn ? sdesc_rows(stage_p(0)) : ptx::sdesc_kmajor(stage_p(0), 128);
+        const uint64_t desc_q = p.q_mn ? sdesc_rows(stage_q(0)) : ptx::sdesc_kmajor(stage_q(0), 128);
+        const uint32_t upper = (uint32_t)(desc_p >> 32);   // stride, version, swizzle: 1024 bytes either way
+        const uint32_t first_p = (uint32_t)desc_p, first_q = (uint32_t)desc_q;
+        // 16 values of K further, in 16 bytes: along a row, or 16 rows down.
+        const uint32_t step_p = p.p_mn ? 128 : 2, step_q = p.q_mn ? 128 : 2;
+        const bool leader = rank == 0 || !PAIR;
+        const uint32_t on = elect_one();
+        uint32_t it = 0, n = 0, acc = 0, early = 0;
+        bool ok = true;
+        for (uint32_t t = t_first; ok && t < tiles; t += t_step, ++n) {
+            if (!item_there(n)) {
+                gave_up();
+                break;
+            }
+            const Item w = load_item(item_at(n));
+            done_with(n);
+            if (!leader) continue;
+            int k = w.k0;
+            do {
+                const int b = (int)(acc % NBUF), first = k, end = w.k1 - k > part ? k + part : w.k1;
+                if (!wait_tile(acce_bar(b), ((acc / NBUF) & 1) ^ 1, longest)) {
+                    gave_up();
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t d = taddr + (uint32_t)(b * BN);
+                for (; k < end; k += kSlab, ++it) {
+                    const int s = (int)(it % STAGES);
+                    if (!wait_bar(early, full_bar(s), (it / STAGES) & 1)) {
+                        gave_up();
+                        ok = false;
+                        break;
+                    }
+                    // What warp 3 of the other CTA zeroed there is seen here too.
+                    if (PAIR && group_k && w.k1 - k < kSlab) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                    ptx::tc_fence_after();
+                    const uint32_t off = (uint32_t)(s * (Cfg::STAGE_BYTES / 16));
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_bf16_if<PAIR>(on & (uint32_t)(16 * ks < w.k1 - k), d, first_p + off + ks * step_p,
+                                          first_q + off + ks * step_q, upper, idesc, ks != 0 || k != first ? 1u : 0u);
+                    if constexpr (PAIR) mma_commit_pair_if(on, done_bar(s));
+                    else mma_commit_if(on, done_bar(s));
+                    const uint32_t next = it + 1;
+                    early = mbar_test(full_bar((int)(next % STAGES)), (next / STAGES) & 1);
+                }
+                if constexpr (PAIR) mma_commit_pair_if(on & (uint32_t)ok, accf_bar(b));
+                else mma_commit_if(on & (uint32_t)ok, accf_bar(b));
+                ++acc;
+            } while (ok && k < w.k1);
+        }
+        // Everything issued finishes before TMEM is released.
+        if (leader) {
+            if constexpr (PAIR)
+                asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+                             "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+                                 drain_bar),
+                             "r"(on)
+                             : "memory");
+            else mma_commit_if(on, drain_bar);
+            if (!wait_bar(0, drain_bar, 0)) gave_up();
+        }
+    } else if (warp == 2) {
+        // ------------------------------ tiles ------------------------------
+        uint32_t n = 0;
+        for (uint32_t t = t_first; t < tiles; t += t_step, ++n) {
+            Item w = find_item(p, table, t, split > 1 ? rank : 0);
+            w.more = t + t_step < tiles;
+            // The place is free when the tile kItems before is stored.
+            if (!wait_tile(iempty_bar(n % kItems), ((n / kItems) & 1) ^ 1, longest)) {
+                gave_up();
+                break;
+            }
+            if (lane == 0) store_item(item_at(n), w);
+            __syncwarp();
+            mbar_arrive_if(lane == 0, ifull_bar(n % kItems));
+        }
+    } else if (warp == 3) {
+        // --------------------- the ends of groups along K ---------------------
+        // Both operands have K along the rows of their boxes here.
+        // A stage's next such slab comes after this one's MMAs: one phase each.
+        uint32_t it = 0, n = 0, phases = 0;
+        for (uint32_t t = t_first; group_k && t < tiles; t += t_step, ++n) {
+            if (!item_there(n)) {
+                gave_up();
+                break;
+            }
+            const Item w = load_item(item_at(n));
+            done_with(n);
+            const int nk = slabs(w.k0, w.k1), valid = (w.k1 - w.k0) % kSlab;
+            it += nk;
+            if (valid == 0) continue;
+            const int s = (int)((it - 1) % STAGES);
+            if (!wait_tile(tail_bar(s), (phases >> s) & 1, longest)) {
+                gave_up();
+                break;
+            }
+            phases ^= 1u << s;
+            const int end = (valid + 15) / 16 * 16;
+            constexpr int boxes = 2 + (QR + 63) / 64;
+            const int pieces = (end - valid) * 8;   // 16 bytes each, per box
+            for (int i = lane; i < boxes * pieces; i += 32) {
+                const int box = i / pieces, at = i - box * pieces;
+                st_shared_u32x4(stage_p(s) + 8192 * box + 128 * valid + 16 * at, make_uint4(0, 0, 0, 0));
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if constexpr (PAIR) mbar_arrive_cluster_if(lane == 0, map_shared(full_bar(s), 0));
+            else mbar_arrive_if(lane == 0, full_bar(s));
+        }
+    } else {
+        // ------------------------------ epilogue ------------------------------
+        const int ew = warp - 4, quarter = ew & 3, col0 = (ew >> 2) * CW;
+        const int lane0 = 32 * quarter + 128 * pair_rank;
+        const uint32_t lanes = taddr + ((uint32_t)(32 * quarter) << 16) + (uint32_t)col0;
+        const uint32_t st = base + Cfg::OFF_EXTRA + ew * kStaging;
+        if (Cfg::CAN_SPLIT && split > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        if constexpr (Cfg::MOVE_REGS) ptx::setmaxnreg_inc<216>();
+        constexpr int CHUNK = Cfg::CHUNK;
+        uint32_t n = 0, acc = 0;
+        // The next accumulator, once complete, and its way back to the MMA warp.
+        auto take = [&](uint32_t &from) {
+            const int b = (int)(acc % NBUF);
+            from = lanes + (uint32_t)(b * BN);
+            const bool there = wait_tile(accf_bar(b), (acc / NBUF) & 1, longest);
+            ptx::tc_fence_after();
+            if (!there) gave_up();
+            return there;
+        };
+        auto give_back = [&]() {
+            const int b = (int)(acc % NBUF);
+            ptx::tc_fence_before();
+            __syncwarp();
+            if constexpr (PAIR) mbar_arrive_cluster_if(lane == 0, map_shared(acce_bar(b), 0));
+            else mbar_arrive_if(lane == 0, acce_bar(b));
+            ++acc;
+        };
+        for (uint32_t t = t_first; t < tiles; t += t_step, ++n) {
+            if (!item_there(n)) {
+                gave_up();
+                break;
+            }
+            const Item w = load_item(item_at(n));
+            uint32_t from;
+            if (part == INT32_MAX) {
+                // bfloat16 C: from tensor memory.
+                if (!take(from)) break;
+                auto get = [&](int c, uint32_t (&v)[CHUNK]) {
+                    tmem_ld_chunk<CHUNK>(from + c, v);
+                    tmem_ld_wait_for<CHUNK>(v);
+                    if (w.k0 >= w.k1) {
+#pragma unroll
+                        for (int j = 0; j < CHUNK; ++j) v[j] = 0;
+                    }
+                };
+                if (p.swap) store_part<__nv_bfloat16, Cfg, true>(p, w, st, lane, lane0, col0, get);
+                else store_part<__nv_bfloat16, Cfg, false>(p, w, st, lane, lane0, col0, get);
+                give_back();
+                done_with(n);
+                continue;
+            }
+            float sum[CW];
+#pragma unroll
+            for (int j = 0; j < CW; ++j) sum[j] = 0.0f;
+            bool ok = true;
+            int k = w.k0;
+            do {
+                if (!(ok = take(from))) break;
+                if (k < w.k1) {
+#pragma unroll
+                    for (int c = 0; c < CW; c += CHUNK) {
+                        uint32_t v[CHUNK];
+                        tmem_ld_chunk<CHUNK>(from + c, v);
+                        tmem_ld_wait_for<CHUNK>(v);
+#pragma unroll
+                        for (int j = 0; j < CHUNK; ++j) sum[c + j] += __uint_as_float(v[j]);
+                    }
+                }
+                give_back();
+                k = w.k1 - k > part ? k + part : w.k1;
+            } while (k < w.k1);
+            if (!ok) break;
+            if (split == 1) {
+                auto get = [&](int c, uint32_t (&v)[CHUNK]) {
+#pragma unroll
+                    for (int i = 0; i < CW; i += CHUNK)
+                        if (c == i) {
+#pragma unroll
+                            for (int j = 0; j < CHUNK; ++j) v[j] = __float_as_uint(sum[i + j]);
+                        }
+                };
+                if (p.swap) store_part<float, Cfg, true>(p, w, st, lane, lane0, col0, get);
+                else store_part<float, Cfg, false>(p, w, st, lane, lane0, col0, get);
+            } else if constexpr (Cfg::CAN_SPLIT) {
+                // To the CTA that adds column j over the cluster: j % split.
+                const int per = BN / split, shift = __ffs(split) - 1;
+                const uint32_t mine = base + Cfg::OFF_EXTRA + 4 * (rank * per * 128 + 32 * quarter + lane);
+#pragma unroll
+                for (int j = 0; j < CW; ++j) {
+                    const int col = col0 + j;
+                    st_cluster_f32(mine + 4 * 128 * (col >> shift), (uint32_t)(col & (split - 1)), sum[j]);
+                }
+            }
+            done_with(n);
+        }
+        __syncwarp();
+        ptx::tc_fence_before();
+    }
+
+    // ------------------------------ teardown ------------------------------
+    if constexpr (Cfg::CAN_SPLIT) {
+        if (split > 1) {
+            __syncwarp();
+            if (warp < 4) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+            // One tile per cluster. Its columns' parts are here, one set per
+            // CTA of the cluster; this CTA adds columns rank, rank + split, ..
+            // in rank order (of lanes that hold columns of C: a split tile is
+            // swapped). Nothing reaches into another CTA after this barrier.
+            ptx::cluster_sync_all();
+            if (t_first < tiles) {
+                const Item w = find_item(p, table, t_first, rank);
+                const uint32_t part = base + Cfg::OFF_EXTRA;
+                const int per = BN / split;
+                auto add = [&](auto q) {
+                    for (int i = threadIdx.x; i < per * 128; i += Cfg::THREADS) {
+                        const int m = w.m + (i >> 7) * split + rank, n = w.n + (i & 127);
+                        if (m < w.m_end && n < p.N) {
+                            float v = 0.0f;
+#pragma unroll
+                            for (int r = 0; r < 8; ++r)
+                                if (r < split) v += ld_shared_f32(part + 4 * (r * per * 128 + i));
+                            store_one(p, q, m, n, v);
+                        }
+                    }
+                };
+                if (p.c_bf16) add(place_of<__nv_bfloat16>(p, w.group));
+                else add(place_of<float>(p, w.group));
+            }
+        }
+    }
+    // Neither CTA of a pair leaves while the other's MMAs or arrivals reach it.
+    if constexpr (PAIR) {
+        __syncwarp();
+        ptx::cluster_sync_all();
+    } else {
+        __syncthreads();
+    }
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        tmem_dealloc<PAIR>(taddr, Cfg::TMEM_COLS);
+    }
+}
+
+// Tensor map of an operand: `outer` rows of `inner` values, `groups` of them
+// `stride` values apart, in boxes of 64 values by box_rows rows.
+cudaError_t encode_bf16(CUtensorMap *map, const void *ptr, int64_t inner, int64_t outer, int64_t ld, int64_t groups,
+                        int64_t stride, int box_rows)
+{
+    const auto encode = tensor_map_encoder();
+    if (!encode) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)outer, (cuuint64_t)groups};
+    const cuuint64_t strides[2] = {(cuuint64_t)(2 * ld), (cuuint64_t)(2 * stride)};
+    const cuuint32_t box[3] = {(cuuint32_t)kSlab, (cuuint32_t)box_rows, 1};
+    const cuuint32_t elem[3] = {1, 1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, elem,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <class Cfg>
+cudaError_t prepare_cfg()
+{
+    return cudaFuncSetAttribute(bf16_product_kernel<Cfg>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
+}
+
+bool pieces16(const void *p, int64_t ld, int64_t per16)
+{
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % per16 == 0;
+}
+
+template <class Cfg>
+cudaError_t launch_cfg(const Bf16Args &g, const Bf16Plan &plan, cudaStream_t stream)
+{
+    Bf16Params p{};
+    p.mode = g.mode;
+    p.swap = plan.swap;
+    p.M = (int)g.M, p.N = (int)g.N, p.K = (int)g.K;
+    p.tm = plan.swap ? Cfg::BN : Cfg::LANES;
+    p.tn = plan.swap ? Cfg::LANES : Cfg::BN;
+    // A stored K x M and B stored K x N have their rows (M, N) contiguous.
+    const bool a_mn = g.op_a == 1, b_mn = g.op_b == 0;
+    p.p_mn = plan.swap ? b_mn : a_mn;
+    p.q_mn = plan.swap ? a_mn : b_mn;
+    CUtensorMap map_a, map_b;
+    const int64_t bg = g.mode == kBf16GroupRows ? g.groups : 1;
+    const int q_rows = Cfg::QR < 64 ? Cfg::QR : 64, a_rows = plan.swap ? q_rows : 64, b_rows = plan.swap ? 64 : q_rows;
+    cudaError_t e;
+    if (g.K > 0) {
+        const int64_t a_outer = a_mn ? g.K : g.M, b_outer = b_mn ? g.K : g.N;
+        e = encode_bf16(&map_a, g.A, a_mn ? g.M : g.K, a_outer, g.lda, 1, a_outer * g.lda, a_mn ? kSlab : a_rows);
+        if (e == cudaSuccess)
+            e = encode_bf16(&map_b, g.B, b_mn ? g.N : g.K, b_outer, g.ldb, bg, bg > 1 ? g.stride_b : b_outer * g.ldb,
+                            b_mn ? kSlab : b_rows);
+    } else {
+        // The empty sum: no copy is ever issued, the maps only have to be valid.
+        const void *any = reinterpret_cast<const void *>(reinterpret_cast<uintptr_t>(g.C) & ~uintptr_t(15));
+        e = encode_bf16(&map_a, any, 8, 1, 8, 1, 8, 8);
+        map_b = map_a;
+    }
+    if (e != cudaSuccess) return e;
+    p.groups = g.groups;
+    p.offsets = g.offsets;
+    p.row_tiles = (int)ceil_div(g.M, p.tm);
+    p.col_tiles = (int)ceil_div(g.N, p.tn);
+    // Tiles are counted in 32 bits.
+    const int64_t hit = g.groups < g.M ? g.groups : g.M;
+    const int64_t rows = g.mode == kBf16Dense       ? p.row_tiles
+                         : g.mode == kBf16GroupRows ? g.M / p.tm + hit
+                                                    : (int64_t)p.row_tiles * g.groups;
+    if (rows + 2 * kRaster > INT32_MAX / p.col_tiles - 2 * kRaster) return cudaErrorInvalidValue;
+    p.by_cols = fast_div((uint32_t)p.col_tiles);
+    p.by_group = fast_div((uint32_t)((int64_t)p.row_tiles * p.col_tiles));
+    p.split = plan.split;
+    p.bias = g.bias;
+    p.stride_bias = g.stride_bias;
+    p.act = g.act;
+    p.join = g.join;
+    p.pre = g.pre;
+    p.ld_pre = g.ld_pre;
+    p.D = g.D;
+    p.ldd = g.ldd;
+    p.C = g.C;
+    p.ldc = g.ldc;
+    p.stride_c = g.stride_c;
+    p.c_bf16 = g.c_bf16;
+    const int64_t per16 = g.c_bf16 ? 8 : 4;
+    p.vec = pieces16(g.C, g.ldc, per16) && (!g.pre || pieces16(g.pre, g.ld_pre, per16)) &&
+            (g.join == kJoinNone || pieces16(g.D, g.ldd, per16)) && (g.mode != kBf16GroupK || g.stride_c % per16 == 0);
+    p.status = g.status;
+    CUtensorMap &mp = plan.swap ? map_b : map_a, &mq = plan.swap ? map_a : map_b;
+    void *args[] = {&mp, &mq, &p};
+    cudaLaunchConfig_t lc = {};
+    cudaLaunchAttribute attrs[1];
+    const unsigned cluster = Cfg::PAIR ? 2u : (unsigned)plan.split;
+    if (cluster > 1) {
+        attrs[0].id = cudaLaunchAttributeClusterDimension;
+        attrs[0].val.clusterDim.x = cluster;
+        attrs[0].val.clusterDim.y = 1;
+        attrs[0].val.clusterDim.z = 1;
+        lc.attrs = attrs;
+        lc.numAttrs = 1;
+    }
+    lc.gridDim = dim3((unsigned)plan.grid);
+    lc.blockDim = dim3(Cfg::THREADS);
+    lc.dynamicSmemBytes = Cfg::SMEM_BYTES;
+    lc.stream = stream;
+    e = cudaLaunchKernelExC(&lc, reinterpret_cast<const void *>(bf16_product_kernel<Cfg>), args);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+using Pair256 = Bf16Cfg<256, true>;
+using Pair128 = Bf16Cfg<128, true>;
+using One128 = Bf16Cfg<128, false>;
+using One64 = Bf16Cfg<64, false>;
+using One32 = Bf16Cfg<32, false>;
+using One16 = Bf16Cfg<16, false>;
+
+}  // namespace
+
+Bf16Plan plan_bf16(const Bf16Args &g)
+{
+    const int64_t sms = g.num_sms;
+    const int64_t hit = g.groups < g.M ? g.groups : g.M;
+    auto tiles_of = [&](int64_t tm, int64_t tn) {
+        const int64_t rows = g.mode == kBf16GroupRows ? g.M / tm + hit : ceil_div(g.M, tm);
+        return rows * ceil_div(g.N, tn) * (g.mode == kBf16GroupK ? g.groups : 1);
+    };
+    const int64_t nk = ceil_div(g.mode == kBf16GroupK ? ceil_div(g.K, g.groups) : g.K, kSlab);
+    const int64_t per = g.mode == kBf16GroupRows ? ceil_div(g.M, g.groups) : g.M;
+    Bf16Plan best{256, true, false, 1, 0};
+    double least = 0.0;
+    auto consider = [&](int cols, bool pair, bool swap, int split) {
+        const int lanes = pair ? 256 : 128;
+        const int64_t tm = swap ? cols : lanes, tn = swap ? lanes : cols;
+        // Row tiles of groups by their average, as the device finds them.
+        const int64_t rows = g.mode == kBf16GroupRows ? hit * ceil_div(per, tm) : ceil_div(g.M, tm);
+        const int64_t tiles = rows * ceil_div(g.N, tn) * (g.mode == kBf16GroupK ? g.groups : 1);
+        const int64_t at_once = sms / ((pair ? 2 : 1) * split);
+        const int64_t waves = ceil_div(tiles, at_once > 0 ? at_once : 1);
+        const double slab = pair ? 80.0 + 1.75 * cols : 220.0 + 1.4 * cols;
+        const double time = (double)waves * ((double)ceil_div(nk, split) * slab + 600.0 + 8.0 * cols) + (split > 1 ? 1500.0 : 0.0);
+        if (least == 0.0 || time < least) {
+            least = time;
+            best = Bf16Plan{cols, pair, swap, split, 0};
+        }
+    };
+    for (int cols = 16; cols <= 128; cols *= 2) {
+        consider(cols, false, true, 1);
+        if (g.mode == kBf16Dense) consider(cols, false, false, 1);
+        if (g.mode != kBf16GroupK)
+            for (int split = 2; split <= 8; split *= 2)
+                if (nk >= 4 * split && tiles_of(cols, 128) * split <= sms) consider(cols, false, true, split);
+    }
+    for (int cols = 128; sms >= 2 && cols <= 256; cols *= 2) consider(cols, true, g.mode == kBf16GroupRows, 1);
+    const int64_t lanes = best.pair ? 256 : 128;
+    const int64_t tiles = best.swap ? tiles_of(best.cols, lanes) : tiles_of(lanes, best.cols);
+    const int64_t cluster = best.pair ? 2 : best.split;
+    const int64_t most = sms / cluster * cluster;
+    best.grid = tiles * cluster < most ? tiles * cluster : most;
+    return best;
+}
+
+cudaError_t prepare_bf16()
+{
+    cudaError_t e = prepare_cfg<Pair256>();
+    if (e == cudaSuccess) e = prepare_cfg<Pair128>();
+    if (e == cudaSuccess) e = prepare_cfg<One128>();
+    if (e == cudaSuccess) e = prepare_cfg<One64>();
+    if (e == cudaSuccess) e = prepare_cfg<One32>();
+    if (e == cudaSuccess) e = prepare_cfg<One16>();
+    return e;
+}
+
+cudaError_t launch_bf16(const Bf16Args &g, cudaStream_t stream)
+{
+    const Bf16Plan p = plan_bf16(g);
+    if (p.grid == 0) return cudaSuccess;
+    if (p.pair) return p.cols == 256 ? launch_cfg<Pair256>(g, p, stream) : launch_cfg<Pair128>(g, p, stream);
+    return p.cols == 128  ? launch_cfg<One128>(g, p, stream)
+           : p.cols == 64 ? launch_cfg<One64>(g, p, stream)
+           : p.cols == 32 ? launch_cfg<One32>(g, p, stream)
+                          : launch_cfg<One16>(g, p, stream);
+}
+
+}  // namespace sgemm_gb300

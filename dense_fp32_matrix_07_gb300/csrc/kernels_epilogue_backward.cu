@@ -1,0 +1,302 @@
+// Gradient of the 16-bit products' epilogue, C = act(z) [* D], z = A.B + bias:
+//
+//   dz = g act'(z) [* D],   dD = g act(z),   db[n] = sum over a group's rows of dz[., n]
+//
+// Bound by memory: g, z and D are read once, dz and dD written once. A block
+// takes 64 rows of one group by 256 columns at a time, a warp every eighth of
+// the rows, a lane eight columns, whose sums it keeps; the block's sums go to
+// scratch, and a second launch adds each group's in order (no atomics: the
+// result does not depend on timing). db sums the unrounded dz, in FP32.
+#include "layers.cuh"
+
+namespace sgemm_gb300 {
+
+namespace {
+
+constexpr int kRows = 64;     // rows of a block's unit
+constexpr int kCols = 256;    // columns of a block's unit: 32 lanes, 8 each
+
+template <class T>
+struct Params {
+    int64_t rows, cols;
+    const T *g, *z, *D;
+    int64_t ld_g, ld_z, ldd;
+    int act, join;
+    int groups;
+    const int32_t *offsets;
+    T *dz, *dD;
+    int64_t ld_dz, ld_dD;
+    float *parts;             // sums of each unit of rows, or null
+    int units;                // units of rows, at most
+    int strips;               // of kCols columns
+};
+
+__device__ __forceinline__ void group_rows(const int32_t *offsets, int groups, int64_t rows, int g, int64_t &lo, int64_t &hi)
+{
+    if (!offsets) {
+        lo = 0, hi = rows;
+        return;
+    }
+    lo = offsets[g], hi = offsets[g + 1];
+    lo = lo < 0 ? 0 : lo > rows ? rows : lo;
+    hi = hi < lo ? lo : hi > rows ? rows : hi;
+}
+
+// table[g] = units of the groups before g, held to `units` (offsets that are
+// not a partition may sum to anything). By one block of 256 threads.
+__device__ void fill_table(int *table, const int32_t *offsets, int groups, int64_t rows, int units)
+{
+    __shared__ int sums[256];
+    const int per = (groups + 255) / 256, first = threadIdx.x * per;
+    int64_t mine = 0;
+    for (int g = first; g < first + per && g < groups; ++g) {
+        int64_t lo, hi;
+        group_rows(offsets, groups, rows, g, lo, hi);
+        mine += (hi - lo + kRows - 1) / kRows;
+    }
+    sums[threadIdx.x] = (int)(mine < units ? mine : units);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        int64_t at = 0;
+        for (int i = 0; i < 256; ++i) {
+            const int n = sums[i];
+            sums[i] = (int)at;
+            at = at + n < units ? at + n : units;
+        }
+        table[groups] = (int)at;
+    }
+    __syncthreads();
+    int64_t at = sums[threadIdx.x];
+    for (int g = first; g < first + per && g < groups; ++g) {
+        int64_t lo, hi;
+        group_rows(offsets, groups, rows, g, lo, hi);
+        table[g] = (int)at;
+        at += (hi - lo + kRows - 1) / kRows;
+        at = at < units ? at : units;
+    }
+    __syncthreads();
+}
+
+// act(z) and its slope.
+__device__ __forceinline__ float2 act_and_slope(float z, int act)
+{
+    switch (act) {
+    case kActRelu: return make_float2(z < 0.0f ? 0.0f : z, z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z);
+    case kActGelu: {
+        const float phi = 0.5f * (1.0f + erff(z * 0.70710678118654752f));
+        return make_float2(z * phi, phi + z * (0.39894228040143268f * expf(-0.5f * z * z)));
+    }
+    case kActGeluTanh: {
+        constexpr float c = 0.79788456080286536f;
+        const float z2 = z * z, t = tanhf(c * (z + 0.044715f * z2 * z));
+        const float half = 0.5f * (1.0f + t);
+        // Where 1 - t^2 is 0 the polynomial beside it may be infinite.
+        const float edge = 1.0f - t * t;
+        return make_float2(z * half, half + (edge > 0.0f ? 0.5f * z * edge * (c * (1.0f + 0.134145f * z2)) : edge));
+    }
+    case kActSilu: {
+        const float s = __fdividef(1.0f, 1.0f + expf(-z));
+        return make_float2(z * s, s * (1.0f + z * (1.0f - s)));
+    }
+    default: return make_float2(z, 1.0f);
+    }
+}
+
+// VEC: a lane's eight columns are neighbours, by 16-byte accesses; else they
+// are 32 apart, one at a time.
+template <class T, bool VEC>
+__device__ __forceinline__ int column(int lane, int e) { return VEC ? 8 * lane + e : lane + 32 * e; }
+
+template <class T, bool VEC>
+__device__ __forceinline__ void load8(const T *row, int lane, int cols, float (&v)[8])
+{
+    if (VEC && 8 * lane + 8 <= cols) {
+        constexpr int N = 16 / (int)sizeof(T);
+#pragma unroll
+        for (int i = 0; i < 8; i += N) {
+            const Values<T, N> x = *reinterpret_cast<const Values<T, N> *>(row + 8 * lane + i);
+#pragma unroll
+            for (int e = 0; e < N; ++e) v[i + e] = load_as_float(&x.v[e]);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int c = column<T, VEC>(lane, e);
+            v[e] = c < cols ? load_as_float(row + c) : 0.0f;
+        }
+    }
+}
+
+template <class T, bool VEC>
+__device__ __forceinline__ void store8(T *row, int lane, int cols, const float (&v)[8])
+{
+    if (VEC && 8 * lane + 8 <= cols) {
+        constexpr int N = 16 / (int)sizeof(T);
+#pragma unroll
+        for (int i = 0; i < 8; i += N) {
+            Values<T, N> x;
+#pragma unroll
+            for (int e = 0; e < N; ++e) store_from_float(&x.v[e], v[i + e]);
+            *reinterpret_cast<Values<T, N> *>(row + 8 * lane + i) = x;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int c = column<T, VEC>(lane, e);
+            if (c < cols) store_from_float(row + c, v[e]);
+        }
+    }
+}
+
+template <class T, bool VEC>
+__global__ void __launch_bounds__(256)
+epilogue_backward_kernel(const __grid_constant__ Params<T> p)
+{
+    __shared__ int table[kMaxGroups + 1];
+    __shared__ float sums[8][kCols];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    if (p.offsets) fill_table(table, p.offsets, p.groups, p.rows, p.units);
+    const int units = p.offsets ? table[p.groups] : p.units;
+    const int64_t all = (int64_t)units * p.strips;
+    for (int64_t t = blockIdx.x; t < all; t += gridDim.x) {
+        const int unit = (int)(t / p.strips), strip = (int)(t % p.strips);
+        int64_t lo, hi;
+        int first = unit;
+        if (p.offsets) {
+            int a = 0, b = p.groups - 1;
+            while (a < b) {
+                const int mid = (a + b + 1) / 2;
+                if (table[mid] <= unit) a = mid;
+                else b = mid - 1;
+            }
+            first = unit - table[a];
+            group_rows(p.offsets, p.groups, p.rows, a, lo, hi);
+        } else {
+            lo = 0, hi = p.rows;
+        }
+        lo += (int64_t)first * kRows;
+        hi = lo + kRows < hi ? lo + kRows : hi;
+        const int64_t c0 = (int64_t)strip * kCols;
+        const int cols = (int)(p.cols - c0 < kCols ? p.cols - c0 : kCols);
+        float sum[8] = {};
+#pragma unroll 2
+        for (int64_t r = lo + warp; r < hi; r += 8) {
+            float g[8], z[8] = {}, d[8], o[8];
+            load8<T, VEC>(p.g + r * p.ld_g + c0, lane, cols, g);
+            if (p.z) load8<T, VEC>(p.z + r * p.ld_z + c0, lane, cols, z);
+            if (p.join == kJoinMul) load8<T, VEC>(p.D + r * p.ldd + c0, lane, cols, d);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float2 a = act_and_slope(z[e], p.act);
+                o[e] = g[e] * a.x;
+                if (p.act != kActNone) g[e] *= a.y;
+                if (p.join == kJoinMul) g[e] *= d[e];
+                sum[e] += g[e];
+            }
+            if (p.dz) store8<T, VEC>(p.dz + r * p.ld_dz + c0, lane, cols, g);
+            if (p.dD) store8<T, VEC>(p.dD + r * p.ld_dD + c0, lane, cols, o);
+        }
+        if (p.parts) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sums[warp][column<T, VEC>(lane, e)] = sum[e];
+            __syncthreads();
+            if ((int)threadIdx.x < cols) {
+                float s = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s += sums[i][threadIdx.x];
+                p.parts[(int64_t)unit * p.cols + c0 + threadIdx.x] = s;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// db[g][c] = sum of the parts of group g's units, in order within 8 runs.
+__global__ void __launch_bounds__(256)
+add_units_kernel(const float *parts, int64_t rows, int64_t cols, int groups, const int32_t *offsets, int units,
+                 float *grad_bias, int64_t stride)
+{
+    __shared__ int table[kMaxGroups + 1];
+    __shared__ float sums[8][33];
+    const int lane = threadIdx.x % 32, run = threadIdx.x / 32, g = blockIdx.y;
+    int u0 = 0, u1 = units;
+    if (offsets) {
+        fill_table(table, offsets, groups, rows, units);
+        u0 = table[g], u1 = table[g + 1];
+    }
+    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+    float s = 0.0f;
+    if (c < cols) {
+#pragma unroll 4
+        for (int u = u0 + run; u < u1; u += 8) s += parts[(int64_t)u * cols + c];
+    }
+    sums[run][lane] = s;
+    __syncthreads();
+    if (run == 0 && c < cols) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) s += sums[i][lane];
+        grad_bias[g * stride + c] = s;
+    }
+}
+
+// Units of rows at most: each group's last may be short.
+int64_t most_units(const EpilogueBackwardArgs &g)
+{
+    if (!g.offsets) return (g.rows + kRows - 1) / kRows;
+    return g.rows / kRows + (g.groups < g.rows ? g.groups : g.rows);
+}
+
+bool pieces16(const void *p, int64_t ld, int64_t per16)
+{
+    return !p || ((reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % per16 == 0);
+}
+
+template <class T>
+cudaError_t backward_of(const EpilogueBackwardArgs &g, void *scratch, cudaStream_t stream)
+{
+    constexpr int64_t per16 = 16 / (int64_t)sizeof(T);
+    Params<T> p{};
+    p.rows = g.rows, p.cols = g.cols;
+    p.g = static_cast<const T *>(g.grad_out), p.ld_g = g.ld_go;
+    const bool uses_z = g.act != kActNone || g.grad_D;
+    p.z = uses_z ? static_cast<const T *>(g.pre) : nullptr, p.ld_z = g.ld_pre;
+    p.D = static_cast<const T *>(g.D), p.ldd = g.ldd;
+    p.act = g.act, p.join = g.join;
+    p.groups = g.groups, p.offsets = g.offsets;
+    p.dz = static_cast<T *>(g.grad_pre), p.ld_dz = g.ld_gp;
+    p.dD = static_cast<T *>(g.grad_D), p.ld_dD = g.ld_gd;
+    p.parts = g.grad_bias ? static_cast<float *>(scratch) : nullptr;
+    p.units = (int)most_units(g);
+    p.strips = (int)((g.cols + kCols - 1) / kCols);
+    const bool vec = pieces16(p.g, p.ld_g, per16) && pieces16(p.z, p.ld_z, per16) && pieces16(p.dz, p.ld_dz, per16) &&
+                     pieces16(p.dD, p.ld_dD, per16) && (g.join != kJoinMul || pieces16(p.D, p.ldd, per16));
+    if (p.units > 0) {
+        const int64_t all = (int64_t)p.units * p.strips, most = (int64_t)g.num_sms * 8;
+        const unsigned grid = (unsigned)(all < most ? all : most);
+        if (vec) epilogue_backward_kernel<T, true><<<grid, 256, 0, stream>>>(p);
+        else epilogue_backward_kernel<T, false><<<grid, 256, 0, stream>>>(p);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    if (g.grad_bias) {
+        const dim3 grid((unsigned)((g.cols + 31) / 32), (unsigned)g.groups);
+        add_units_kernel<<<grid, 256, 0, stream>>>(p.parts, g.rows, g.cols, g.groups, g.offsets, p.units, g.grad_bias,
+                                                   g.stride_gb);
+        return cudaGetLastError();
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+
+size_t epilogue_backward_scratch_bytes(const EpilogueBackwardArgs &g)
+{
+    return g.grad_bias ? (size_t)most_units(g) * (size_t)g.cols * 4 : 0;
+}
+
+cudaError_t launch_epilogue_backward(const EpilogueBackwardArgs &g, void *scratch, cudaStream_t stream)
+{
+    return g.bf16 ? backward_of<__nv_bfloat16>(g, scratch, stream) : backward_of<float>(g, scratch, stream);
+}
+
+}  // namespace sgemm_gb300

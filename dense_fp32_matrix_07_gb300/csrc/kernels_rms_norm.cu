@@ -1,0 +1,506 @@
+// Root-mean-square norm of rows, with the residual's addition before it and
+// 8-bit values after it, and its gradient:
+//
+//   s = x + residual,  i = 1 / sqrt(mean(s^2) + eps),  y = s i w
+//   q, scales: y in the rows form (a scale per row and 128 columns)
+//
+//   h = s i,  ds = i (g w - h mean(g w h)) + gs,  dw = sum over rows of g h
+//
+// A row is held in registers by one warp (short rows) or one block, eight
+// neighbouring columns to a thread, so that everything is read once and
+// written once. Sums are in FP32; y and q come from the unrounded s, and each
+// stored value is rounded once. The gradient takes s as it was stored and
+// finds i again from it.
+//
+// Rows that are not in whole 16-byte pieces pass through shared memory, which
+// turns accesses of single neighbouring values into the threads' eights.
+#include "fp8_values.cuh"
+#include "layers.cuh"
+
+#include <type_traits>
+
+namespace sgemm_gb300 {
+
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+
+// Eight neighbouring values of a row as they are stored, by 16-byte accesses.
+template <class T>
+struct Raw8 {
+    uint4 u[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T *p)
+    {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = reinterpret_cast<const uint4 *>(p)[i];
+    }
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = make_uint4(0, 0, 0, 0);
+    }
+    // The first n of them.
+    __device__ __forceinline__ void load_some(const T *p, int n)
+    {
+        uint32_t w[2 * sizeof(T)] = {};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (e >= n) continue;
+            if constexpr (sizeof(T) == 4) w[e] = __float_as_uint(p[e]);
+            else w[e / 2] |= (uint32_t) * reinterpret_cast<const uint16_t *>(p + e) << (16 * (e & 1));
+        }
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+    __device__ __forceinline__ float get(int e) const
+    {
+        const uint4 &q = u[sizeof(T) == 4 ? e / 4 : 0];
+        const int i = sizeof(T) == 4 ? e % 4 : e / 2;
+        const uint32_t x = i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w;
+        if constexpr (sizeof(T) == 4) return __uint_as_float(x);
+        else return __uint_as_float((e & 1) ? x & 0xffff0000u : x << 16);
+    }
+};
+
+__device__ __forceinline__ void store8(float *p, const float (&v)[8])
+{
+    reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8])
+{
+    uint32_t u[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+        u[j] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// The threads that share a row: a warp each (WARPS = 1, eight rows a block) or
+// the whole block.
+template <int WARPS>
+struct Team {
+    static constexpr int SIZE = 32 * WARPS;
+    static constexpr int ROWS = WARPS == 1 ? 8 : 1;
+    static constexpr int THREADS = SIZE * ROWS;
+    static __device__ __forceinline__ int rank() { return (int)threadIdx.x % SIZE; }
+    static __device__ __forceinline__ int row() { return (int)threadIdx.x / SIZE; }
+    static __device__ __forceinline__ void sync()
+    {
+        if constexpr (WARPS == 1) __syncwarp();
+        else __syncthreads();
+    }
+    // The sums of a and of b over the team, in a fixed order; `turn` alternates
+    // between calls, so that one barrier is enough.
+    static __device__ __forceinline__ float2 sum(float2 v, int turn)
+    {
+#pragma unroll
+        for (int d = 16; d; d /= 2) {
+            v.x += __shfl_xor_sync(kAll, v.x, d);
+            v.y += __shfl_xor_sync(kAll, v.y, d);
+        }
+        if constexpr (WARPS > 1) {
+            __shared__ float2 part[2][WARPS];
+            if (threadIdx.x % 32 == 0) part[turn][threadIdx.x / 32] = v;
+            __syncthreads();
+            v = part[turn][threadIdx.x % WARPS];
+#pragma unroll
+            for (int d = WARPS / 2; d; d /= 2) {
+                v.x += __shfl_xor_sync(kAll, v.x, d);
+                v.y += __shfl_xor_sync(kAll, v.y, d);
+            }
+        }
+        return v;
+    }
+};
+
+// Columns of a thread's pack k: 8 from here on.
+template <int WARPS>
+__device__ __forceinline__ int column(int k)
+{
+    return 8 * (Team<WARPS>::rank() + k * Team<WARPS>::SIZE);
+}
+
+template <class T>
+struct NormParams {
+    int64_t rows;
+    int cols;
+    const T *x, *residual;
+    const float *weight;
+    float eps;
+    T *sum, *y;
+    uint8_t *q;
+    float *scales;
+    int64_t ldx, ld_res, ld_sum, ldy, ldq, lds;
+    int weight16;      // the weights lie on 16 bytes
+};
+
+__device__ __forceinline__ void load_weight(const float *w, int c, int cols, bool whole16, float (&v)[8])
+{
+    if (whole16 && c + 8 <= cols) {
+        const float4 a = __ldg(reinterpret_cast<const float4 *>(w + c)), b = __ldg(reinterpret_cast<const float4 *>(w + c) + 1);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? __ldg(w + c + e) : 0.0f;
+}
+
+// A thread's eights of a row, zeros past the end; !VEC: through `line`.
+template <class T, int WARPS, int PACKS, bool VEC>
+__device__ __forceinline__ void load_row(const T *row, int cols, T *line, Raw8<T> (&v)[PACKS])
+{
+    using Tm = Team<WARPS>;
+    if constexpr (!VEC) {
+        Tm::sync();
+#pragma unroll 4
+        for (int c = Tm::rank(); c < (cols + 7) / 8 * 8; c += Tm::SIZE) store_from_float(line + c, c < cols ? load_as_float(row + c) : 0.0f);
+        Tm::sync();
+    }
+#pragma unroll
+    for (int k = 0; k < PACKS; ++k) {
+        const int c = column<WARPS>(k);
+        if constexpr (VEC) {
+            if (c + 8 <= cols) v[k].load(row + c);
+            else v[k].load_some(row + c, cols - c);
+        } else {
+            if (c < cols) v[k].load(line + c);
+            else v[k].zero();
+        }
+    }
+}
+
+// A thread's eight from column c on to a row (!VEC: to `line`).
+template <class T, bool VEC>
+__device__ __forceinline__ void store_pack(T *row, T *line, int c, int cols, const float (&v)[8])
+{
+    if constexpr (!VEC) {
+        if (c < cols) store8(line + c, v);
+    } else if (c + 8 <= cols) {
+        store8(row + c, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (c + e < cols) store_from_float(row + c + e, v[e]);
+    }
+}
+
+// !VEC: `line`, as the team has stored it, to a row.
+template <class T, int WARPS>
+__device__ __forceinline__ void store_line(T *row, const T *line, int cols)
+{
+    using Tm = Team<WARPS>;
+    Tm::sync();
+#pragma unroll 4
+    for (int c = Tm::rank(); c < cols; c += Tm::SIZE) row[c] = line[c];
+}
+
+template <class T, int WARPS, int PACKS, bool VEC>
+__global__ void __launch_bounds__(Team<WARPS>::THREADS)
+rms_norm_kernel(const __grid_constant__ NormParams<T> p)
+{
+    using Tm = Team<WARPS>;
+    extern __shared__ uint4 staging[];
+    const int64_t r = (int64_t)blockIdx.x * Tm::ROWS + Tm::row();
+    if (r >= p.rows) return;          // whole teams
+    const int cols = p.cols;
+    T *const line = reinterpret_cast<T *>(staging) + Tm::row() * ((cols + 7) / 8 * 8);
+    float v[PACKS][8];
+    {
+        Raw8<T> x[PACKS], a[PACKS];
+        load_row<T, WARPS, PACKS, VEC>(p.x + r * p.ldx, cols, line, x);
+        if (p.residual) load_row<T, WARPS, PACKS, VEC>(p.residual + r * p.ld_res, cols, line, a);
+#pragma unroll
+        for (int k = 0; k < PACKS; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[k][e] = p.residual ? x[k].get(e) + a[k].get(e) : x[k].get(e);
+    }
+    float2 ss = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < PACKS; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss.x = fmaf(v[k][e], v[k][e], ss.x);
+    // Every value of the row has been read: the sum may go where x or the residual was.
+    const float inv = rsqrtf(Tm::sum(ss, 0).x / (float)cols + p.eps);
+
+    if (p.sum) {
+        T *const to = p.sum + r * p.ld_sum;
+        if constexpr (!VEC) Tm::sync();
+#pragma unroll
+        for (int k = 0; k < PACKS; ++k) store_pack<T, VEC>(to, line, column<WARPS>(k), cols, v[k]);
+        if constexpr (!VEC) {
+            store_line<T, WARPS>(to, line, cols);
+            Tm::sync();
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < PACKS; ++k) {
+        const int c = column<WARPS>(k);
+        if (p.weight) {
+            float w[8];
+            load_weight(p.weight, c, cols, p.weight16, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[k][e] = v[k][e] * inv * w[e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[k][e] *= inv;
+        }
+        if (p.y) store_pack<T, VEC>(p.y + r * p.ldy, line, c, cols, v[k]);
+        if (p.q) {
+            // A block of 128 columns lies in 16 neighbouring lanes.
+            uint32_t most = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) most = umax(most, c + e < cols ? magnitude(v[k][e]) : 0u);
+#pragma unroll
+            for (int d = 8; d; d /= 2) most = umax(most, __shfl_xor_sync(kAll, most, d));
+            if (c < cols) {
+                const Scale s = scale_of(most);
+                const uint2 b = make_uint2(
+                    to_e4m3x4(v[k][0] * s.inv, v[k][1] * s.inv, v[k][2] * s.inv, v[k][3] * s.inv),
+                    to_e4m3x4(v[k][4] * s.inv, v[k][5] * s.inv, v[k][6] * s.inv, v[k][7] * s.inv));
+                *reinterpret_cast<uint2 *>(p.q + r * p.ldq + c) = b;
+                if (c % kBlock == 0) p.scales[(int64_t)(c / kBlock) * p.lds + r] = s.scale;
+            }
+        }
+    }
+    if constexpr (!VEC) {
+        if (p.y) store_line<T, WARPS>(p.y + r * p.ldy, line, cols);
+    }
+}
+
+template <class T>
+struct NormBackwardParams {
+    int64_t rows;
+    int cols;
+    const T *g, *x, *gs;
+    const float *weight;
+    float eps;
+    T *dx;
+    float *parts;      // one row of partial weight gradients per block, or null
+    int64_t ld_g, ldx, ld_gs, ld_dx;
+    int weight16;
+};
+
+template <class T, int WARPS, int PACKS, bool VEC>
+__global__ void __launch_bounds__(Team<WARPS>::THREADS)
+rms_norm_backward_kernel(const __grid_constant__ NormBackwardParams<T> p)
+{
+    using Tm = Team<WARPS>;
+    extern __shared__ uint4 staging[];
+    const int cols = p.cols, padded = (cols + 7) / 8 * 8;
+    T *const line = reinterpret_cast<T *>(staging) + Tm::row() * padded;
+    float dw[PACKS][8];
+#pragma unroll
+    for (int k = 0; k < PACKS; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[k][e] = 0.0f;
+    int turn = 0;
+    for (int64_t r = (int64_t)blockIdx.x * Tm::ROWS + Tm::row(); r < p.rows; r += (int64_t)gridDim.x * Tm::ROWS, turn ^= 1) {
+        Raw8<T> x[PACKS], g[PACKS], gs[PACKS];
+        load_row<T, WARPS, PACKS, VEC>(p.x + r * p.ldx, cols, line, x);
+        load_row<T, WARPS, PACKS, VEC>(p.g + r * p.ld_g, cols, line, g);
+        if (p.gs) load_row<T, WARPS, PACKS, VEC>(p.gs + r * p.ld_gs, cols, line, gs);
+        float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < PACKS; ++k) {
+            float w[8];
+            if (p.weight) load_weight(p.weight, column<WARPS>(k), cols, p.weight16, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                s.x = fmaf(x[k].get(e), x[k].get(e), s.x);
+                s.y = fmaf(p.weight ? g[k].get(e) * w[e] : g[k].get(e), x[k].get(e), s.y);
+            }
+        }
+        s = Tm::sum(s, turn);
+        const float inv = rsqrtf(s.x / (float)cols + p.eps);
+        const float mean = s.y * inv / (float)cols;     // of g w h
+        T *const to = p.dx + r * p.ld_dx;
+        if constexpr (!VEC) Tm::sync();
+#pragma unroll
+        for (int k = 0; k < PACKS; ++k) {
+            const int c = column<WARPS>(k);
+            float w[8], d[8];
+            if (p.weight) load_weight(p.weight, c, cols, p.weight16, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float h = x[k].get(e) * inv, gw = p.weight ? g[k].get(e) * w[e] : g[k].get(e);
+                dw[k][e] = fmaf(g[k].get(e), h, dw[k][e]);
+                d[e] = inv * (gw - h * mean);
+                if (p.gs) d[e] += gs[k].get(e);
+            }
+            store_pack<T, VEC>(to, line, c, cols, d);
+        }
+        if constexpr (!VEC) store_line<T, WARPS>(to, line, cols);
+    }
+    if (!p.parts) return;
+    float *const to = p.parts + (int64_t)blockIdx.x * cols;
+    if constexpr (WARPS == 1) {
+        // The eight rows' warps, in order.
+        float *const all = reinterpret_cast<float *>(staging);
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < PACKS; ++k) {
+            const int c = column<WARPS>(k);
+            if (c < cols) store8(all + Tm::row() * padded + c, dw[k]);
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < cols; c += Tm::THREADS) {
+            float s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < Tm::ROWS; ++i) s += all[i * padded + c];
+            to[c] = s;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < PACKS; ++k) {
+            const int c = column<WARPS>(k);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c + e < cols) to[c + e] = dw[k][e];
+        }
+    }
+}
+
+// out[c] = sum of parts[.][c], in order within 8 interleaved runs.
+__global__ void __launch_bounds__(256) add_parts_kernel(const float *parts, int count, int cols, float *out)
+{
+    __shared__ float sums[8][33];
+    const int lane = threadIdx.x % 32, run = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
+    float s = 0.0f;
+    if (c < cols) {
+#pragma unroll 8
+        for (int i = run; i < count; i += 8) s += parts[(int64_t)i * cols + c];
+    }
+    sums[run][lane] = s;
+    __syncthreads();
+    if (run == 0 && c < cols) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) s += sums[i][lane];
+        out[c] = s;
+    }
+}
+
+bool pieces16(const void *p, int64_t ld, int64_t per16)
+{
+    return !p || ((reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % per16 == 0);
+}
+
+// Calls f(Warps, Packs) with the shape of `cols` columns.
+template <class F>
+cudaError_t with_shape(int64_t cols, F f)
+{
+    using std::integral_constant;
+    auto call = [&](auto w, auto k) { return f(w, k); };
+    if (cols <= 256) return call(integral_constant<int, 1>{}, integral_constant<int, 1>{});
+    if (cols <= 1024) return call(integral_constant<int, 1>{}, integral_constant<int, 4>{});
+    if (cols <= 2048) return call(integral_constant<int, 4>{}, integral_constant<int, 2>{});
+    if (cols <= 4096) return call(integral_constant<int, 8>{}, integral_constant<int, 2>{});
+    if (cols <= 8192) return call(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+    return call(integral_constant<int, 32>{}, integral_constant<int, 2>{});
+}
+
+// Shared memory of a block whose rows pass through it.
+int staging_bytes(int64_t cols, int rows) { return (int)((cols + 7) / 8 * 32 * rows); }
+
+template <class K>
+cudaError_t launch(K kernel, unsigned grid, int threads, int bytes, const void *params, cudaStream_t stream)
+{
+    if (bytes > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+    }
+    void *args[] = {const_cast<void *>(params)};
+    const cudaError_t e = cudaLaunchKernel(reinterpret_cast<const void *>(kernel), dim3(grid), dim3(threads), args,
+                                           (size_t)bytes, stream);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <class T>
+cudaError_t norm_of(const RmsNormArgs &g, cudaStream_t stream)
+{
+    constexpr int64_t per16 = 16 / (int64_t)sizeof(T);
+    NormParams<T> p{};
+    p.rows = g.rows, p.cols = (int)g.cols;
+    p.x = static_cast<const T *>(g.x), p.ldx = g.ldx;
+    p.residual = static_cast<const T *>(g.residual), p.ld_res = g.ld_res;
+    p.weight = g.weight, p.eps = g.eps;
+    p.weight16 = (reinterpret_cast<uintptr_t>(g.weight) & 15u) == 0;
+    p.sum = static_cast<T *>(g.sum), p.ld_sum = g.ld_sum;
+    p.y = static_cast<T *>(g.y), p.ldy = g.ldy;
+    p.q = g.q, p.ldq = g.ldq, p.scales = g.scales, p.lds = g.lds;
+    const bool vec = pieces16(g.x, g.ldx, per16) && pieces16(g.residual, g.ld_res, per16) &&
+                     pieces16(g.sum, g.ld_sum, per16) && pieces16(g.y, g.ldy, per16);
+    return with_shape(g.cols, [&](auto w, auto k) {
+        constexpr int W = decltype(w)::value, P = decltype(k)::value;
+        const unsigned grid = (unsigned)((g.rows + Team<W>::ROWS - 1) / Team<W>::ROWS);
+        if (vec) return launch(rms_norm_kernel<T, W, P, true>, grid, Team<W>::THREADS, 0, &p, stream);
+        return launch(rms_norm_kernel<T, W, P, false>, grid, Team<W>::THREADS, staging_bytes(g.cols, Team<W>::ROWS), &p,
+                      stream);
+    });
+}
+
+// Blocks of the gradient's kernel: each holds a row of weight gradients.
+template <int W>
+unsigned backward_blocks(const RmsNormBackwardArgs &g)
+{
+    const int64_t all = (g.rows + Team<W>::ROWS - 1) / Team<W>::ROWS;
+    const int64_t most = (int64_t)g.num_sms * (Team<W>::THREADS >= 1024 ? 1 : Team<W>::THREADS >= 512 ? 2 : 4);
+    return (unsigned)(all < most ? all : most);
+}
+
+template <class T>
+cudaError_t norm_backward_of(const RmsNormBackwardArgs &g, void *scratch, cudaStream_t stream)
+{
+    constexpr int64_t per16 = 16 / (int64_t)sizeof(T);
+    NormBackwardParams<T> p{};
+    p.rows = g.rows, p.cols = (int)g.cols;
+    p.g = static_cast<const T *>(g.grad_y), p.ld_g = g.ld_gy;
+    p.x = static_cast<const T *>(g.x), p.ldx = g.ldx;
+    p.gs = static_cast<const T *>(g.grad_sum), p.ld_gs = g.ld_gs;
+    p.weight = g.weight, p.eps = g.eps;
+    p.weight16 = (reinterpret_cast<uintptr_t>(g.weight) & 15u) == 0;
+    p.dx = static_cast<T *>(g.grad_x), p.ld_dx = g.ld_gx;
+    p.parts = g.grad_weight ? static_cast<float *>(scratch) : nullptr;
+    const bool vec = pieces16(g.grad_y, g.ld_gy, per16) && pieces16(g.x, g.ldx, per16) &&
+                     pieces16(g.grad_sum, g.ld_gs, per16) && pieces16(g.grad_x, g.ld_gx, per16);
+    return with_shape(g.cols, [&](auto w, auto k) {
+        constexpr int W = decltype(w)::value, P = decltype(k)::value;
+        const unsigned grid = backward_blocks<W>(g);
+        // Warps add their weight gradients up in shared memory.
+        const int bytes = !vec || (W == 1 && p.parts) ? staging_bytes(g.cols, Team<W>::ROWS) : 0;
+        cudaError_t e = grid == 0 ? cudaSuccess
+                        : vec ? launch(rms_norm_backward_kernel<T, W, P, true>, grid, Team<W>::THREADS, bytes, &p, stream)
+                            : launch(rms_norm_backward_kernel<T, W, P, false>, grid, Team<W>::THREADS, bytes, &p, stream);
+        if (e != cudaSuccess || !g.grad_weight) return e;
+        add_parts_kernel<<<(unsigned)((g.cols + 31) / 32), 256, 0, stream>>>(p.parts, (int)grid, (int)g.cols, g.grad_weight);
+        return cudaGetLastError();
+    });
+}
+
+}  // namespace
+
+cudaError_t launch_rms_norm(const RmsNormArgs &g, cudaStream_t stream)
+{
+    return g.bf16 ? norm_of<__nv_bfloat16>(g, stream) : norm_of<float>(g, stream);
+}
+
+size_t rms_norm_backward_scratch_bytes(const RmsNormBackwardArgs &g)
+{
+    if (!g.grad_weight) return 0;
+    size_t bytes = 0;
+    with_shape(g.cols, [&](auto w, auto) {
+        bytes = (size_t)backward_blocks<decltype(w)::value>(g) * (size_t)g.cols * 4;
+        return cudaSuccess;
+    });
+    return bytes;
+}
+
+cudaError_t launch_rms_norm_backward(const RmsNormBackwardArgs &g, void *scratch, cudaStream_t stream)
+{
+    return g.bf16 ? norm_backward_of<__nv_bfloat16>(g, scratch, stream) : norm_backward_of<float>(g, scratch, stream);
+}
+
+}  // namespace sgemm_gb300

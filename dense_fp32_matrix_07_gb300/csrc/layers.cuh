@@ -1,0 +1,153 @@
+// Shared definitions of the operators of layers in 16 bits: products with an
+// epilogue (dense and over experts), the epilogue's gradient, and the
+// root-mean-square norm (declared in include/sgemm_layers.h).
+#pragma once
+
+#include "experts.cuh"
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+namespace sgemm_gb300 {
+
+enum Activation : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
+enum Join : int { kJoinNone = 0, kJoinAdd = 1, kJoinMul = 2 };
+
+// ----------------------------------------------------------- 16-bit products
+
+enum Bf16Mode : int {
+    kBf16Dense = 0,      // C = op(A) . op(B)
+    kBf16GroupRows = 1,  // rows [offsets[g], offsets[g+1]) of A meet B_g
+    kBf16GroupK = 2      // C_g = A^T . B over the rows of group g
+};
+
+struct Bf16Args {
+    int mode;
+    int op_a, op_b;            // as stored: A M x K (0) or K x M (1), B K x N (0) or N x K (1)
+    int64_t M, N, K;           // rows and columns of C (one group's under GroupK), shared length
+    const void *A;
+    int64_t lda;
+    const void *B;
+    int64_t ldb, stride_b;
+    int groups;
+    const int32_t *offsets;
+    const float *bias;         // N values (of group g at g * stride_bias), or null
+    int64_t stride_bias;
+    int act, join;
+    void *pre;                 // the sums before the activation, or null
+    int64_t ld_pre;
+    const void *D;
+    int64_t ldd;
+    void *C;
+    int c_bf16;                // C, pre and D are bfloat16, else float
+    int64_t ldc, stride_c;     // GroupK: C (and D) of group g at g * stride_c
+    unsigned int *status;
+    int num_sms;
+};
+
+// The kernel shape of a product: `cols` accumulator columns per tile, `pair` =
+// two CTAs on a 256-lane tile, `swap` = the lanes hold columns of C, `split`
+// CTAs of a cluster sharing each tile's K blocks.
+struct Bf16Plan {
+    int cols;
+    bool pair, swap;
+    int split;
+    int64_t grid;
+};
+Bf16Plan plan_bf16(const Bf16Args &g);
+cudaError_t prepare_bf16();
+cudaError_t launch_bf16(const Bf16Args &g, cudaStream_t stream);
+
+// ------------------------------------------------------ gradient of the epilogue
+
+struct EpilogueBackwardArgs {
+    int64_t rows, cols;
+    bool bf16;
+    const void *grad_out;
+    int64_t ld_go;
+    const void *pre;
+    int64_t ld_pre;
+    int act, join;
+    const void *D;
+    int64_t ldd;
+    int groups;
+    const int32_t *offsets;    // null: one group of all rows
+    void *grad_pre;
+    int64_t ld_gp;
+    void *grad_D;
+    int64_t ld_gd;
+    float *grad_bias;
+    int64_t stride_gb;
+    int num_sms;
+};
+size_t epilogue_backward_scratch_bytes(const EpilogueBackwardArgs &g);
+cudaError_t launch_epilogue_backward(const EpilogueBackwardArgs &g, void *scratch, cudaStream_t stream);
+
+// --------------------------------------------------------- root-mean-square norm
+
+constexpr int64_t kMaxNormCols = 16384;   // a row is held in registers by its block
+
+struct RmsNormArgs {
+    int64_t rows, cols;
+    bool bf16;
+    const void *x;
+    int64_t ldx;
+    const void *residual;
+    int64_t ld_res;
+    const float *weight;
+    float eps;
+    void *sum;
+    int64_t ld_sum;
+    void *y;
+    int64_t ldy;
+    uint8_t *q;
+    int64_t ldq;
+    float *scales;
+    int64_t lds;
+    int num_sms;
+};
+cudaError_t launch_rms_norm(const RmsNormArgs &g, cudaStream_t stream);
+
+struct RmsNormBackwardArgs {
+    int64_t rows, cols;
+    bool bf16;
+    const void *grad_y;
+    int64_t ld_gy;
+    const void *x;
+    int64_t ldx;
+    const float *weight;
+    float eps;
+    const void *grad_sum;
+    int64_t ld_gs;
+    void *grad_x;
+    int64_t ld_gx;
+    float *grad_weight;
+    int num_sms;
+};
+size_t rms_norm_backward_scratch_bytes(const RmsNormBackwardArgs &g);
+cudaError_t launch_rms_norm_backward(const RmsNormBackwardArgs &g, void *scratch, cudaStream_t stream);
+
+// ------------------------------------------------------------ device helpers
+
+// N values of T as one access of up to 16 bytes.
+template <class T, int N>
+struct alignas(sizeof(T) * N) Values {
+    T v[N];
+};
+
+// The activations, in FP32: relu (a NaN stays one), z Phi(z), its form with
+// tanh, and z sigmoid(z). Where exp(-z) passes 2^126 the quotient is 0, which
+// is z sigmoid(z) to within 1e-36.
+__device__ __forceinline__ float activate(float z, int act)
+{
+    switch (act) {
+    case kActRelu: return z < 0.0f ? 0.0f : z;
+    case kActGelu: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+    case kActGeluTanh: return 0.5f * z * (1.0f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
+    case kActSilu: return __fdividef(z, 1.0f + expf(-z));
+    default: return z;
+    }
+}
+
+}  // namespace sgemm_gb300

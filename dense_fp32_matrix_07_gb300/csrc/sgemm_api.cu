@@ -6,6 +6,7 @@
 #include "common.cuh"
 #include "configs.cuh"
 #include "experts.cuh"
+#include "layers.cuh"
 #include "schedule.cuh"
 
 #include <atomic>
@@ -29,7 +30,7 @@ struct DeviceState {
     int num_sms = 0;
     unsigned int *status = nullptr;   // device address of g_status_word
     cudaMemPool_t pool = nullptr;     // scratch for packed operands
-    bool experts_ready = false;       // the kernels of sgemm_experts.h are set up
+    bool experts_ready = false;       // the kernels of sgemm_experts.h and sgemm_layers.h are set up
 };
 
 std::mutex g_mutex;
@@ -153,7 +154,8 @@ int device_info(DeviceInfo *out)
     {
         std::lock_guard<std::mutex> lock(g_mutex);
         if (!dev->experts_ready) {
-            if (take_test_failure(g_fail_setups) || prepare_fp8() != cudaSuccess || prepare_route() != cudaSuccess) {
+            if (take_test_failure(g_fail_setups) || prepare_fp8() != cudaSuccess || prepare_route() != cudaSuccess ||
+                prepare_bf16() != cudaSuccess) {
                 cudaGetLastError();
                 return SGEMM_ERR_CUDA;
             }
