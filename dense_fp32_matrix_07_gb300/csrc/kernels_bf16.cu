@@ -355,46 +355,45 @@ __device__ __forceinline__ void store_one(const Bf16Params &p, const Place<T> &q
 {
     if (q.bias) z += __ldg(q.bias + n);
     if (q.pre) store_from_float(q.pre + m * p.ld_pre + n, z);
-    float y = activate(z, p.act);
+    float y = z;
+    with_activation(p.act, [&](auto a) { y = activate<decltype(a)::value>(z); });
     if (q.D) y = joined(y, load_as_float(q.D + m * p.ldd + n), p.join);
     store_from_float(q.C + m * p.ldc + n, y);
 }
 
-// Staging of R x COLS sums of C, rows of 128 bytes, their 16-byte pieces
+// Staging of a chunk of C's sums: rows of 32 floats, their 16-byte pieces
 // exchanged by row: element (r, c).
 __device__ __forceinline__ uint32_t staged(uint32_t st, int r, int c)
 {
     return st + 128 * r + 16 * ((c >> 2) ^ (r & 7)) + 4 * (c & 3);
 }
 
-// Staged values z to act(z), 4 at a time.
-template <int R, int COLS>
-__device__ __forceinline__ void activate_staged(uint32_t st, int lane, int act)
+// A chunk of the warp's accumulators, v[j] column j of this lane, to staging:
+// the lane is a row of C, or (swap) the column is.
+template <int CHUNK>
+__device__ __forceinline__ void stage(uint32_t st, int lane, bool swap, const float *v)
 {
-    constexpr int PER_ROW = COLS / 4, PER_PASS = 32 / PER_ROW;
-#pragma unroll 2
-    for (int r = lane / PER_ROW; r < R; r += PER_PASS) {
-        const uint32_t at = staged(st, r, 4 * (lane % PER_ROW));
-        uint4 u = ld_shared_u32x4(at);
-        float z[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
+    if (swap) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) z[e] = activate(z[e], act);
-        st_shared_u32x4(at, make_uint4(__float_as_uint(z[0]), __float_as_uint(z[1]), __float_as_uint(z[2]),
-                                       __float_as_uint(z[3])));
+        for (int j = 0; j < CHUNK; ++j)
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(staged(st, j, lane)), "f"(v[j]) : "memory");
+    } else {
+#pragma unroll
+        for (int j = 0; j < CHUNK; j += 4)
+            st_shared_u32x4(staged(st, lane, j), make_uint4(__float_as_uint(v[j]), __float_as_uint(v[j + 1]),
+                                                            __float_as_uint(v[j + 2]), __float_as_uint(v[j + 3])));
     }
 }
 
-// A chunk of the warp's sums, which get() gives (column j of this lane in
-// v[j]): through staging to rows m .. of C, columns n .. (`rows` and `cols` of
-// them exist), V values of a row per access. D is requested before the sums.
-template <class T, int CHUNK, bool SWAP, int V, class Get>
-__device__ __forceinline__ void store_chunk(const Bf16Params &p, const Place<T> &q, uint32_t st, int lane, Get get, int64_t m,
+// Staged sums to R rows of C from m on, 32 columns from n on (`rows` and
+// `cols` of them exist), V values of a row per access; put() stages them.
+// What of D a lane needs is requested before that.
+template <class T, int R, int V, class Put>
+__device__ __forceinline__ void store_chunk(const Bf16Params &p, const Place<T> &q, uint32_t st, int lane, Put put, int64_t m,
                                             int rows, int n, int cols)
 {
-    constexpr int R = SWAP ? CHUNK : 32, COLS = SWAP ? 32 : CHUNK;
-    constexpr int PER_ROW = COLS / V, PER_PASS = 32 / PER_ROW, PASSES = R / PER_PASS;
-    constexpr int MOST = sizeof(T) == 4 && V > 1 ? 4 : 8;
-    constexpr int AHEAD = PASSES < MOST ? PASSES : MOST;      // accesses of D under way
+    constexpr int PER_ROW = 32 / V, PER_PASS = 32 / PER_ROW, PASSES = R / PER_PASS;
+    constexpr int AHEAD = PASSES < 8 ? PASSES : 8;      // accesses of D under way
     const int r0 = lane / PER_ROW, c0 = (lane % PER_ROW) * V;
     const bool whole = V == 1 ? c0 < cols : c0 + V <= cols;
     Values<T, V> d[AHEAD];
@@ -405,115 +404,99 @@ __device__ __forceinline__ void store_chunk(const Bf16Params &p, const Place<T> 
             if (whole && r < rows) d[i] = *reinterpret_cast<const Values<T, V> *>(q.D + (m + r) * p.ldd + n + c0);
         }
     };
-    auto read = [&](int r, float (&z)[V]) {
-        if constexpr (V == 1) {
-            z[0] = ld_shared_f32(staged(st, r, c0));
-        } else {
-#pragma unroll
-            for (int e = 0; e < V; e += 4) {
-                const uint4 u = ld_shared_u32x4(staged(st, r, c0 + e));
-                z[e] = __uint_as_float(u.x), z[e + 1] = __uint_as_float(u.y);
-                z[e + 2] = __uint_as_float(u.z), z[e + 3] = __uint_as_float(u.w);
-            }
-        }
-    };
     if (q.D) fetch(0);
-    // The bias of column n + lane.
-    float b = 0.0f;
-    if (q.bias && lane < (COLS < cols ? COLS : cols)) b = __ldg(q.bias + n + lane);
-    {
-        uint32_t v[CHUNK];
-        get(v);
-        if constexpr (SWAP) {
+    float b[V];
 #pragma unroll
-            for (int j = 0; j < CHUNK; ++j)
-                asm volatile("st.shared.f32 [%0], %1;" ::"r"(staged(st, j, lane)), "f"(__uint_as_float(v[j]) + b) : "memory");
-        } else {
-            if (q.bias) {
+    for (int e = 0; e < V; ++e) b[e] = 0.0f;
+    if (q.bias) {
 #pragma unroll
-                for (int j = 0; j < CHUNK; ++j)
-                    v[j] = __float_as_uint(__uint_as_float(v[j]) + __shfl_sync(kAll, b, j));
-            }
-#pragma unroll
-            for (int j = 0; j < CHUNK; j += 4)
-                st_shared_u32x4(staged(st, lane, j), make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]));
-        }
+        for (int e = 0; e < V; ++e)
+            if (c0 + e < cols) b[e] = __ldg(q.bias + n + c0 + e);
     }
+    put();
     __syncwarp();
-    if (q.pre) {
-#pragma unroll 4
-        for (int r = r0; r < R; r += PER_PASS) {
-            if (r >= rows) break;
-            T *to = q.pre + (m + r) * p.ld_pre + n + c0;
-            if (whole) {
-                float z[V];
-                read(r, z);
-                Values<T, V> o;
-#pragma unroll
-                for (int e = 0; e < V; ++e) store_from_float(&o.v[e], z[e]);
-                *reinterpret_cast<Values<T, V> *>(to) = o;
-            } else {
+    if (!whole) {
+        // The columns where C ends inside an access.
 #pragma unroll 1
-                for (int e = 0; e < cols - c0; ++e) store_from_float(to + e, ld_shared_f32(staged(st, r, c0 + e)));
-            }
+        for (int i = 0; i < PASSES * (V > 1 ? cols - c0 : 0); ++i) {
+            const int r = r0 + i % PASSES * PER_PASS, c = c0 + i / PASSES;
+            if (r < rows) store_one(p, q, m + r, n + c, ld_shared_f32(staged(st, r, c)));
         }
-    }
-    if (p.act != kActNone) {
-        __syncwarp();
-        activate_staged<R, COLS>(st, lane, p.act);
-        __syncwarp();
-    }
+    } else {
+        with_activation(p.act, [&](auto a) {
 #pragma unroll 1
-    for (int i0 = 0; i0 < PASSES; i0 += AHEAD) {
-        if (i0 > 0 && q.D) fetch(i0);
+            for (int i0 = 0; i0 < PASSES; i0 += AHEAD) {
+                if (i0 > 0 && q.D) fetch(i0);
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            const int r = r0 + (i0 + i) * PER_PASS;
-            if (r >= rows) continue;
-            T *to = q.C + (m + r) * p.ldc + n + c0;
-            if (whole) {
-                float z[V];
-                read(r, z);
-                if (q.D) {
+                for (int i = 0; i < AHEAD; ++i) {
+                    const int r = r0 + (i0 + i) * PER_PASS;
+                    if (r >= rows) continue;
+                    float z[V];
+                    if constexpr (V == 1) {
+                        z[0] = ld_shared_f32(staged(st, r, c0));
+                    } else {
 #pragma unroll
-                    for (int e = 0; e < V; ++e) z[e] = joined(z[e], load_as_float(&d[i].v[e]), p.join);
-                }
-                Values<T, V> o;
+                        for (int e = 0; e < V; e += 4) {
+                            const uint4 u = ld_shared_u32x4(staged(st, r, c0 + e));
+                            z[e] = __uint_as_float(u.x), z[e + 1] = __uint_as_float(u.y);
+                            z[e + 2] = __uint_as_float(u.z), z[e + 3] = __uint_as_float(u.w);
+                        }
+                    }
+                    Values<T, V> o;
 #pragma unroll
-                for (int e = 0; e < V; ++e) store_from_float(&o.v[e], z[e]);
-                *reinterpret_cast<Values<T, V> *>(to) = o;
-            } else {
-                const T *from = q.D ? q.D + (m + r) * p.ldd + n + c0 : nullptr;
-#pragma unroll 1
-                for (int e = 0; e < cols - c0; ++e) {
-                    const float y = ld_shared_f32(staged(st, r, c0 + e));
-                    store_from_float(to + e, from ? joined(y, load_as_float(from + e), p.join) : y);
+                    for (int e = 0; e < V; ++e) z[e] += b[e];
+                    if (q.pre) {
+#pragma unroll
+                        for (int e = 0; e < V; ++e) store_from_float(&o.v[e], z[e]);
+                        *reinterpret_cast<Values<T, V> *>(q.pre + (m + r) * p.ld_pre + n + c0) = o;
+                    }
+#pragma unroll
+                    for (int e = 0; e < V; ++e) z[e] = activate<decltype(a)::value>(z[e]);
+                    if (q.D) {
+#pragma unroll
+                        for (int e = 0; e < V; ++e) z[e] = joined(z[e], load_as_float(&d[i].v[e]), p.join);
+                    }
+#pragma unroll
+                    for (int e = 0; e < V; ++e) store_from_float(&o.v[e], z[e]);
+                    *reinterpret_cast<Values<T, V> *>(q.C + (m + r) * p.ldc + n + c0) = o;
                 }
             }
-        }
+        });
     }
     __syncwarp();
 }
 
-// A warp's part of a tile: CW columns from the tile's column col0 on. get(c, v)
-// gives the chunk from its column c on.
-template <class T, class Cfg, bool SWAP, class Get>
+// A warp's part of a tile: CW columns from the tile's column col0 on; put(c)
+// stages the chunk from its column c on.
+template <class T, class Cfg, class Put>
 __device__ __forceinline__ void store_part(const Bf16Params &p, const Item &w, uint32_t st, int lane, int lane0, int col0,
-                                           Get get)
+                                           Put put)
 {
     constexpr int CHUNK = Cfg::CHUNK, V = 16 / (int)sizeof(T);
     const Place<T> q = place_of<T>(p, w.group);
 #pragma unroll 1
     for (int c = 0; c < Cfg::CW; c += CHUNK) {
-        const int m = w.m + (SWAP ? col0 + c : lane0), n = w.n + (SWAP ? lane0 : col0 + c);
+        const int m = w.m + (p.swap ? col0 + c : lane0), n = w.n + (p.swap ? lane0 : col0 + c);
         const int rows = w.m_end - m, cols = p.N - n;
         if (rows <= 0 || cols <= 0) continue;
-        auto chunk = [&](uint32_t (&v)[CHUNK]) { get(c, v); };
+        auto chunk = [&]() { put(c); };
         if (p.vec)
-            store_chunk<T, CHUNK, SWAP, V>(p, q, st, lane, chunk, m, rows, n, cols);
+            store_chunk<T, CHUNK, V>(p, q, st, lane, chunk, m, rows, n, cols);
         else
-            store_chunk<T, CHUNK, SWAP, 1>(p, q, st, lane, chunk, m, rows, n, cols);
+            store_chunk<T, CHUNK, 1>(p, q, st, lane, chunk, m, rows, n, cols);
     }
+}
+
+// Asks for a warp's part of D, so that it is in L2 when the sums are there.
+template <class T, class Cfg>
+__device__ __forceinline__ void prefetch_part(const Bf16Params &p, const Item &w, int lane, int lane0, int col0)
+{
+    const T *D = static_cast<const T *>(p.D) + (p.mode == kBf16GroupK ? w.group * p.stride_c : 0);
+    const int rows = p.swap ? Cfg::CW : 32, cols = p.swap ? 32 : Cfg::CW;
+    const int m = w.m + (p.swap ? col0 : lane0), n = w.n + (p.swap ? lane0 : col0);
+    for (int r = lane; r < rows && m + r < w.m_end; r += 32)
+        for (int c = 0; c < cols && n + c < p.N; c += 128 / (int)sizeof(T))
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(D + (m + r) * p.ldd + n + c));
 }
 
 template <class Cfg>
@@ -848,20 +831,23 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
                 break;
             }
             const Item w = load_item(item_at(n));
+            if (p.join != kJoinNone && split == 1) {
+                if (p.c_bf16) prefetch_part<__nv_bfloat16, Cfg>(p, w, lane, lane0, col0);
+                else prefetch_part<float, Cfg>(p, w, lane, lane0, col0);
+            }
             uint32_t from;
             if (part == INT32_MAX) {
                 // bfloat16 C: from tensor memory.
                 if (!take(from)) break;
-                auto get = [&](int c, uint32_t (&v)[CHUNK]) {
+                store_part<__nv_bfloat16, Cfg>(p, w, st, lane, lane0, col0, [&](int c) {
+                    uint32_t v[CHUNK];
+                    float z[CHUNK];
                     tmem_ld_chunk<CHUNK>(from + c, v);
                     tmem_ld_wait_for<CHUNK>(v);
-                    if (w.k0 >= w.k1) {
 #pragma unroll
-                        for (int j = 0; j < CHUNK; ++j) v[j] = 0;
-                    }
-                };
-                if (p.swap) store_part<__nv_bfloat16, Cfg, true>(p, w, st, lane, lane0, col0, get);
-                else store_part<__nv_bfloat16, Cfg, false>(p, w, st, lane, lane0, col0, get);
+                    for (int j = 0; j < CHUNK; ++j) z[j] = w.k0 < w.k1 ? __uint_as_float(v[j]) : 0.0f;
+                    stage<CHUNK>(st, lane, p.swap, z);
+                });
                 give_back();
                 done_with(n);
                 continue;
@@ -888,16 +874,11 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
             } while (k < w.k1);
             if (!ok) break;
             if (split == 1) {
-                auto get = [&](int c, uint32_t (&v)[CHUNK]) {
+                store_part<float, Cfg>(p, w, st, lane, lane0, col0, [&](int c) {
 #pragma unroll
                     for (int i = 0; i < CW; i += CHUNK)
-                        if (c == i) {
-#pragma unroll
-                            for (int j = 0; j < CHUNK; ++j) v[j] = __float_as_uint(sum[i + j]);
-                        }
-                };
-                if (p.swap) store_part<float, Cfg, true>(p, w, st, lane, lane0, col0, get);
-                else store_part<float, Cfg, false>(p, w, st, lane, lane0, col0, get);
+                        if (c == i) stage<CHUNK>(st, lane, p.swap, sum + i);
+                });
             } else if constexpr (Cfg::CAN_SPLIT) {
                 // To the CTA that adds column j over the cluster: j % split.
                 const int per = BN / split, shift = __ffs(split) - 1;
@@ -1104,7 +1085,8 @@ Bf16Plan plan_bf16(const Bf16Args &g)
     };
     for (int cols = 16; cols <= 128; cols *= 2) {
         consider(cols, false, true, 1);
-        if (g.mode == kBf16Dense) consider(cols, false, false, 1);
+        // 16 columns are for few rows: their chunks have 16 rows of C.
+        if (g.mode == kBf16Dense && cols > 16) consider(cols, false, false, 1);
         if (g.mode != kBf16GroupK)
             for (int split = 2; split <= 8; split *= 2)
                 if (nk >= 4 * split && tiles_of(cols, 128) * split <= sms) consider(cols, false, true, split);

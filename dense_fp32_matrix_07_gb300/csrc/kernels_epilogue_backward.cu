@@ -21,7 +21,7 @@ struct Params {
     int64_t rows, cols;
     const T *g, *z, *D;
     int64_t ld_g, ld_z, ldd;
-    int act, join;
+    int join;
     int groups;
     const int32_t *offsets;
     T *dz, *dD;
@@ -77,28 +77,26 @@ __device__ void fill_table(int *table, const int32_t *offsets, int groups, int64
     __syncthreads();
 }
 
-// act(z) and its slope.
-__device__ __forceinline__ float2 act_and_slope(float z, int act)
+// act(z) and its slope. (Where gelu_tanh's sigmoid is 0 or 1 the polynomial
+// beside it may be infinite.)
+template <int ACT>
+__device__ __forceinline__ float2 act_and_slope(float z)
 {
-    switch (act) {
-    case kActRelu: return make_float2(z < 0.0f ? 0.0f : z, z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z);
-    case kActGelu: {
-        const float phi = 0.5f * (1.0f + erff(z * 0.70710678118654752f));
-        return make_float2(z * phi, phi + z * (0.39894228040143268f * expf(-0.5f * z * z)));
-    }
-    case kActGeluTanh: {
-        constexpr float c = 0.79788456080286536f;
-        const float z2 = z * z, t = tanhf(c * (z + 0.044715f * z2 * z));
-        const float half = 0.5f * (1.0f + t);
-        // Where 1 - t^2 is 0 the polynomial beside it may be infinite.
-        const float edge = 1.0f - t * t;
-        return make_float2(z * half, half + (edge > 0.0f ? 0.5f * z * edge * (c * (1.0f + 0.134145f * z2)) : edge));
-    }
-    case kActSilu: {
-        const float s = __fdividef(1.0f, 1.0f + expf(-z));
-        return make_float2(z * s, s * (1.0f + z * (1.0f - s)));
-    }
-    default: return make_float2(z, 1.0f);
+    if constexpr (ACT == kActRelu) {
+        return make_float2(z < 0.0f ? 0.0f : z, z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z);
+    } else if constexpr (ACT == kActGelu) {
+        float e;
+        const float phi = normal_integral(z, e);
+        return make_float2(z * phi, fmaf(0.39894228040143268f * z, e, phi));
+    } else if constexpr (ACT == kActGeluTanh) {
+        const float s = sigmoid(tanh_argument(z)), edge = s * (1.0f - s);
+        const float rise = 1.59576912160573071f * fmaf(0.134145f * z, z, 1.0f);
+        return make_float2(z * s, edge > 0.0f ? fmaf(z * edge, rise, s) : s + edge);
+    } else if constexpr (ACT == kActSilu) {
+        const float s = sigmoid(z);
+        return make_float2(z * s, s * fmaf(z, 1.0f - s, 1.0f));
+    } else {
+        return make_float2(z, 1.0f);
     }
 }
 
@@ -148,7 +146,7 @@ __device__ __forceinline__ void store8(T *row, int lane, int cols, const float (
     }
 }
 
-template <class T, bool VEC>
+template <class T, bool VEC, int ACT>
 __global__ void __launch_bounds__(256)
 epilogue_backward_kernel(const __grid_constant__ Params<T> p)
 {
@@ -187,9 +185,9 @@ epilogue_backward_kernel(const __grid_constant__ Params<T> p)
             if (p.join == kJoinMul) load8<T, VEC>(p.D + r * p.ldd + c0, lane, cols, d);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float2 a = act_and_slope(z[e], p.act);
+                const float2 a = act_and_slope<ACT>(z[e]);
                 o[e] = g[e] * a.x;
-                if (p.act != kActNone) g[e] *= a.y;
+                if constexpr (ACT != kActNone) g[e] *= a.y;
                 if (p.join == kJoinMul) g[e] *= d[e];
                 sum[e] += g[e];
             }
@@ -261,7 +259,7 @@ cudaError_t backward_of(const EpilogueBackwardArgs &g, void *scratch, cudaStream
     const bool uses_z = g.act != kActNone || g.grad_D;
     p.z = uses_z ? static_cast<const T *>(g.pre) : nullptr, p.ld_z = g.ld_pre;
     p.D = static_cast<const T *>(g.D), p.ldd = g.ldd;
-    p.act = g.act, p.join = g.join;
+    p.join = g.join;
     p.groups = g.groups, p.offsets = g.offsets;
     p.dz = static_cast<T *>(g.grad_pre), p.ld_dz = g.ld_gp;
     p.dD = static_cast<T *>(g.grad_D), p.ld_dD = g.ld_gd;
@@ -273,8 +271,18 @@ cudaError_t backward_of(const EpilogueBackwardArgs &g, void *scratch, cudaStream
     if (p.units > 0) {
         const int64_t all = (int64_t)p.units * p.strips, most = (int64_t)g.num_sms * 8;
         const unsigned grid = (unsigned)(all < most ? all : most);
-        if (vec) epilogue_backward_kernel<T, true><<<grid, 256, 0, stream>>>(p);
-        else epilogue_backward_kernel<T, false><<<grid, 256, 0, stream>>>(p);
+        auto launch = [&](auto a) {
+            if (vec) epilogue_backward_kernel<T, true, decltype(a)::value><<<grid, 256, 0, stream>>>(p);
+            else epilogue_backward_kernel<T, false, decltype(a)::value><<<grid, 256, 0, stream>>>(p);
+        };
+        using std::integral_constant;
+        switch (g.act) {
+        case kActRelu: launch(integral_constant<int, kActRelu>{}); break;
+        case kActGelu: launch(integral_constant<int, kActGelu>{}); break;
+        case kActGeluTanh: launch(integral_constant<int, kActGeluTanh>{}); break;
+        case kActSilu: launch(integral_constant<int, kActSilu>{}); break;
+        default: launch(integral_constant<int, kActNone>{});
+        }
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }

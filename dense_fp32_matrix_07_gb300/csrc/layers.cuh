@@ -8,6 +8,7 @@
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <type_traits>
 
 namespace sgemm_gb300 {
 
@@ -136,17 +137,59 @@ struct alignas(sizeof(T) * N) Values {
     T v[N];
 };
 
-// The activations, in FP32: relu (a NaN stays one), z Phi(z), its form with
-// tanh, and z sigmoid(z). Where exp(-z) passes 2^126 the quotient is 0, which
-// is z sigmoid(z) to within 1e-36.
-__device__ __forceinline__ float activate(float z, int act)
+// exp(x) by one multiplication and the hardware's 2^x: 2^-22 relative, and
+// |x| 2^-24 from the rounded argument, which matters where exp(x) itself is
+// small beside what it is added to.
+__device__ __forceinline__ float fast_exp(float x) { return __expf(x); }
+
+// 1 / (1 + exp(-x)); 0 where exp(-x) passes 2^126 (1e-38 at most is lost).
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.0f, 1.0f + fast_exp(-x)); }
+
+// The normal distribution's integral at z, and exp(-z^2 / 2) on the way:
+// formula 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical Functions,
+// for 1 - erf (absolute error 1.5e-7), without branches.
+__device__ __forceinline__ float normal_integral(float z, float &e)
+{
+    const float x = fabsf(z) * 0.70710678118654752f;
+    const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
+    e = fast_exp(-0.5f * z * z);
+    float q = fmaf(1.061405429f, t, -1.453152027f);
+    q = fmaf(q, t, 1.421413741f);
+    q = fmaf(q, t, -0.284496736f);
+    q = fmaf(q, t, 0.254829592f);
+    q = 0.5f * q * t * e;
+    return z < 0.0f ? q : 1.0f - q;
+}
+
+// 2 sqrt(2/pi) (z + 0.044715 z^3): gelu_tanh is z times the sigmoid of it, as
+// 1 + tanh(u) is twice the sigmoid of 2 u.
+__device__ __forceinline__ float tanh_argument(float z)
+{
+    return 1.59576912160573071f * fmaf(0.044715f * z * z, z, z);
+}
+
+// The activations, in FP32 (a NaN stays one).
+template <int ACT>
+__device__ __forceinline__ float activate(float z)
+{
+    float e;
+    if constexpr (ACT == kActRelu) return z < 0.0f ? 0.0f : z;
+    else if constexpr (ACT == kActGelu) return z * normal_integral(z, e);
+    else if constexpr (ACT == kActGeluTanh) return z * sigmoid(tanh_argument(z));
+    else if constexpr (ACT == kActSilu) return z * sigmoid(z);
+    else return z;
+}
+
+// f(integral_constant) of the activation that the host gave as a number.
+template <class F>
+__device__ __forceinline__ void with_activation(int act, F f)
 {
     switch (act) {
-    case kActRelu: return z < 0.0f ? 0.0f : z;
-    case kActGelu: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
-    case kActGeluTanh: return 0.5f * z * (1.0f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
-    case kActSilu: return __fdividef(z, 1.0f + expf(-z));
-    default: return z;
+    case kActRelu: return f(std::integral_constant<int, kActRelu>{});
+    case kActGelu: return f(std::integral_constant<int, kActGelu>{});
+    case kActGeluTanh: return f(std::integral_constant<int, kActGeluTanh>{});
+    case kActSilu: return f(std::integral_constant<int, kActSilu>{});
+    default: return f(std::integral_constant<int, kActNone>{});
     }
 }
 
