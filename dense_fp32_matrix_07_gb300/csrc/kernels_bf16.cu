@@ -55,17 +55,20 @@ constexpr int kItemBytes = 32;
 constexpr int kStaging = 4096;   // 32 x 32 floats on their way to C
 constexpr int kRaster = 16;      // row tiles walked together, so that a wave of CTAs shares both operands in L2
 
-template <int BN_, bool PAIR_>
+// JOINS: D comes by TMA, ahead of the sums. With 32 KB of operands per 512
+// cycles and five stages of them on their way, a load of D's by the warps
+// that use it waits 2500 cycles in the queue.
+template <int BN_, bool PAIR_, bool JOINS_ = false>
 struct Bf16Cfg {
     static constexpr int BN = BN_;
-    static constexpr bool PAIR = PAIR_;
+    static constexpr bool PAIR = PAIR_, JOINS = JOINS_;
     static constexpr int CTAS = PAIR ? 2 : 1;
     static constexpr int LANES = 128 * CTAS;
     static constexpr int QR = BN / CTAS;                           // rows of the columns' operand a CTA loads
     static constexpr int P_TILE = 128 * 128;
     static constexpr int Q_TILE = (QR < 64 ? 64 : QR) * 128;       // a box of 64 x 64 at least
     static constexpr int STAGE_BYTES = P_TILE + Q_TILE;
-    static constexpr int STAGES = PAIR ? (BN == 256 ? 5 : 7) : BN == 128 ? 4 : BN == 64 ? 7 : 8;
+    static constexpr int STAGES = PAIR ? (BN == 256 ? 5 : 7) - (JOINS ? BN == 256 ? 1 : 2 : 0) : BN == 128 ? 4 : BN == 64 ? 7 : 8;
     static constexpr int NBUF = 2;
     static constexpr int TMEM_COLS = NBUF * BN < 32 ? 32 : NBUF * BN;
     static constexpr int EPI_WARPS = BN >= 128 ? 8 : 4;
@@ -79,9 +82,13 @@ struct Bf16Cfg {
     // Partial sums of a split tile lie where whole tiles are staged.
     static constexpr int PARTIAL = CAN_SPLIT ? BN * 128 * 4 : 0;
     static constexpr int EXTRA = PARTIAL > EPI_WARPS * kStaging ? PARTIAL : EPI_WARPS * kStaging;
-    static constexpr int NUM_BARS = 3 * STAGES + 2 * NBUF + 2 * kItems + 1;
+    // Each epilogue warp's chunks of D: three of bfloat16 or one of floats.
+    static constexpr int D_BYTES = JOINS ? 3 * 32 * 32 * 2 : 0;
+    static constexpr int D_BARS = JOINS ? 3 * EPI_WARPS : 0;
+    static constexpr int NUM_BARS = 3 * STAGES + 2 * NBUF + 2 * kItems + 1 + D_BARS;
     static constexpr int OFF_EXTRA = STAGES * STAGE_BYTES;
-    static constexpr int OFF_ITEMS = OFF_EXTRA + EXTRA;
+    static constexpr int OFF_D = OFF_EXTRA + EXTRA;
+    static constexpr int OFF_ITEMS = OFF_D + EPI_WARPS * D_BYTES;
     static constexpr int OFF_TABLE = OFF_ITEMS + kItems * kItemBytes;
     static constexpr int OFF_BARS = OFF_TABLE + (kMaxGroups + 2) * 4;
     static constexpr int SMEM_BYTES = 1024 + OFF_BARS + NUM_BARS * 8 + 16;
@@ -387,13 +394,16 @@ __device__ __forceinline__ void stage(uint32_t st, int lane, bool swap, const fl
 
 // Staged sums to R rows of C from m on, 32 columns from n on (`rows` and
 // `cols` of them exist), V values of a row per access; put() stages them.
-// What of D a lane needs is requested before that.
-template <class T, int R, int V, class Put>
+// What of D a lane needs is requested before that, unless it comes by TMA:
+// then `dbuf` is where, in rows of 32 values, once there() returns.
+template <class T, int R, int V, bool TMA_D, class Put, class There>
 __device__ __forceinline__ void store_chunk(const Bf16Params &p, const Place<T> &q, uint32_t st, int lane, Put put, int64_t m,
-                                            int rows, int n, int cols)
+                                            int rows, int n, int cols, uint32_t dbuf, There there)
 {
     constexpr int PER_ROW = 32 / V, PER_PASS = 32 / PER_ROW, PASSES = R / PER_PASS;
-    constexpr int AHEAD = PASSES < 8 ? PASSES : 8;      // accesses of D under way
+    // Rows whose sums are in registers together: of one, each activation would
+    // wait for the one before (600 cycles a row where C goes by single values).
+    constexpr int MOST = V == 1 ? 16 : 4, AHEAD = PASSES < MOST ? PASSES : MOST;
     const int r0 = lane / PER_ROW, c0 = (lane % PER_ROW) * V;
     const bool whole = V == 1 ? c0 < cols : c0 + V <= cols;
     Values<T, V> d[AHEAD];
@@ -404,7 +414,7 @@ __device__ __forceinline__ void store_chunk(const Bf16Params &p, const Place<T> 
             if (whole && r < rows) d[i] = *reinterpret_cast<const Values<T, V> *>(q.D + (m + r) * p.ldd + n + c0);
         }
     };
-    if (q.D) fetch(0);
+    if (!TMA_D && q.D) fetch(0);
     float b[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) b[e] = 0.0f;
@@ -414,6 +424,7 @@ __device__ __forceinline__ void store_chunk(const Bf16Params &p, const Place<T> 
             if (c0 + e < cols) b[e] = __ldg(q.bias + n + c0 + e);
     }
     put();
+    if constexpr (TMA_D) there();
     __syncwarp();
     if (!whole) {
         // The columns where C ends inside an access.
@@ -426,83 +437,138 @@ __device__ __forceinline__ void store_chunk(const Bf16Params &p, const Place<T> 
         with_activation(p.act, [&](auto a) {
 #pragma unroll 1
             for (int i0 = 0; i0 < PASSES; i0 += AHEAD) {
-                if (i0 > 0 && q.D) fetch(i0);
+                if (!TMA_D && i0 > 0 && q.D) fetch(i0);
+                float z[AHEAD][V];
 #pragma unroll
                 for (int i = 0; i < AHEAD; ++i) {
                     const int r = r0 + (i0 + i) * PER_PASS;
-                    if (r >= rows) continue;
-                    float z[V];
                     if constexpr (V == 1) {
-                        z[0] = ld_shared_f32(staged(st, r, c0));
+                        z[i][0] = ld_shared_f32(staged(st, r, c0));
                     } else {
 #pragma unroll
                         for (int e = 0; e < V; e += 4) {
                             const uint4 u = ld_shared_u32x4(staged(st, r, c0 + e));
-                            z[e] = __uint_as_float(u.x), z[e + 1] = __uint_as_float(u.y);
-                            z[e + 2] = __uint_as_float(u.z), z[e + 3] = __uint_as_float(u.w);
+                            z[i][e] = __uint_as_float(u.x), z[i][e + 1] = __uint_as_float(u.y);
+                            z[i][e + 2] = __uint_as_float(u.z), z[i][e + 3] = __uint_as_float(u.w);
                         }
                     }
-                    Values<T, V> o;
-#pragma unroll
-                    for (int e = 0; e < V; ++e) z[e] += b[e];
-                    if (q.pre) {
-#pragma unroll
-                        for (int e = 0; e < V; ++e) store_from_float(&o.v[e], z[e]);
-                        *reinterpret_cast<Values<T, V> *>(q.pre + (m + r) * p.ld_pre + n + c0) = o;
-                    }
-#pragma unroll
-                    for (int e = 0; e < V; ++e) z[e] = activate<decltype(a)::value>(z[e]);
-                    if (q.D) {
-#pragma unroll
-                        for (int e = 0; e < V; ++e) z[e] = joined(z[e], load_as_float(&d[i].v[e]), p.join);
-                    }
-#pragma unroll
-                    for (int e = 0; e < V; ++e) store_from_float(&o.v[e], z[e]);
-                    *reinterpret_cast<Values<T, V> *>(q.C + (m + r) * p.ldc + n + c0) = o;
                 }
+                auto store = [&](T *to, int64_t ld) {
+#pragma unroll
+                    for (int i = 0; i < AHEAD; ++i) {
+                        const int r = r0 + (i0 + i) * PER_PASS;
+                        Values<T, V> o;
+#pragma unroll
+                        for (int e = 0; e < V; ++e) store_from_float(&o.v[e], z[i][e]);
+                        if (r < rows) *reinterpret_cast<Values<T, V> *>(to + (m + r) * ld + n + c0) = o;
+                    }
+                };
+                if (q.bias) {
+#pragma unroll
+                    for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+                        for (int e = 0; e < V; ++e) z[i][e] += b[e];
+                }
+                if (q.pre) store(q.pre, p.ld_pre);
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) z[i][e] = activate<decltype(a)::value>(z[i][e]);
+                if constexpr (TMA_D) {
+#pragma unroll
+                    for (int i = 0; i < AHEAD; ++i) {
+                        const uint4 u = ld_shared_u32x4(dbuf + (uint32_t)sizeof(T) * (32 * (r0 + (i0 + i) * PER_PASS) + c0));
+                        d[i] = *reinterpret_cast<const Values<T, V> *>(&u);
+                    }
+                }
+                if (q.D) {
+#pragma unroll
+                    for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+                        for (int e = 0; e < V; ++e) z[i][e] = joined(z[i][e], load_as_float(&d[i].v[e]), p.join);
+                }
+                store(q.C, p.ldc);
             }
         });
     }
     __syncwarp();
 }
 
+// Where chunk c of a warp's part of a tile lies in C, and how much of it exists.
+struct Chunk {
+    int m, n, rows, cols;
+    __device__ __forceinline__ Chunk(const Bf16Params &p, const Item &w, int lane0, int col)
+        : m(w.m + (p.swap ? col : lane0)), n(w.n + (p.swap ? lane0 : col)), rows(w.m_end - m), cols(p.N - n)
+    {
+    }
+    __device__ __forceinline__ bool some() const { return rows > 0 && cols > 0; }
+};
+
+// A warp's chunks of D on their way to shared memory: those of one tile, in
+// order, as many as its buffers hold.
+template <class Cfg>
+struct Arrivals {
+    uint32_t buffers, bars;
+    int next;                      // column of the tile to ask for next
+    uint32_t asked = 0, taken = 0;
+    bool ok = true;
+
+    __device__ __forceinline__ uint32_t depth(const Bf16Params &p) const { return p.c_bf16 ? 3 : 1; }
+    __device__ __forceinline__ uint32_t bytes(const Bf16Params &p) const { return Cfg::CHUNK * 32 * (p.c_bf16 ? 2 : 4); }
+    __device__ __forceinline__ uint32_t bar(const Bf16Params &p, uint32_t i) const { return bars + 8 * (i % depth(p)); }
+    __device__ __forceinline__ uint32_t buffer(const Bf16Params &p, uint32_t i) const { return buffers + bytes(p) * (i % depth(p)); }
+
+    __device__ __forceinline__ void ask(const Bf16Params &p, const CUtensorMap *map, const Item &w, int lane, int lane0, int col0)
+    {
+        while (next < Cfg::CW && asked - taken < depth(p)) {
+            const Chunk c(p, w, lane0, col0 + next);
+            next += Cfg::CHUNK;
+            if (!c.some()) continue;
+            const uint32_t on = lane == 0;
+            mbar_expect_if(on, bar(p, asked), bytes(p));
+            tma_load_if(on, buffer(p, asked), map, bar(p, asked), c.n, c.m, p.mode == kBf16GroupK ? w.group : 0,
+                        ptx::policy_evict_last());
+            ++asked;
+        }
+    }
+    // Waits for the oldest chunk.
+    __device__ __forceinline__ void wait(const Bf16Params &p)
+    {
+        const uint32_t b = bar(p, taken), phase = (taken / depth(p)) & 1;
+        ok = wait_bar(mbar_test(b, phase), b, phase) && ok;
+    }
+};
+
 // A warp's part of a tile: CW columns from the tile's column col0 on; put(c)
 // stages the chunk from its column c on.
 template <class T, class Cfg, class Put>
 __device__ __forceinline__ void store_part(const Bf16Params &p, const Item &w, uint32_t st, int lane, int lane0, int col0,
-                                           Put put)
+                                           Put put, const CUtensorMap *map, Arrivals<Cfg> &d)
 {
     constexpr int CHUNK = Cfg::CHUNK, V = 16 / (int)sizeof(T);
     const Place<T> q = place_of<T>(p, w.group);
 #pragma unroll 1
     for (int c = 0; c < Cfg::CW; c += CHUNK) {
-        const int m = w.m + (p.swap ? col0 + c : lane0), n = w.n + (p.swap ? lane0 : col0 + c);
-        const int rows = w.m_end - m, cols = p.N - n;
-        if (rows <= 0 || cols <= 0) continue;
+        const Chunk at(p, w, lane0, col0 + c);
+        if (!at.some()) continue;
         auto chunk = [&]() { put(c); };
-        if (p.vec)
-            store_chunk<T, CHUNK, V>(p, q, st, lane, chunk, m, rows, n, cols);
-        else
-            store_chunk<T, CHUNK, 1>(p, q, st, lane, chunk, m, rows, n, cols);
+        if constexpr (Cfg::JOINS) {
+            store_chunk<T, CHUNK, V, true>(p, q, st, lane, chunk, at.m, at.rows, at.n, at.cols, d.buffer(p, d.taken),
+                                           [&]() { d.wait(p); });
+            ++d.taken;
+            d.ask(p, map, w, lane, lane0, col0);
+        } else if (p.vec) {
+            store_chunk<T, CHUNK, V, false>(p, q, st, lane, chunk, at.m, at.rows, at.n, at.cols, 0, [] {});
+        } else {
+            store_chunk<T, CHUNK, 1, false>(p, q, st, lane, chunk, at.m, at.rows, at.n, at.cols, 0, [] {});
+        }
     }
-}
-
-// Asks for a warp's part of D, so that it is in L2 when the sums are there.
-template <class T, class Cfg>
-__device__ __forceinline__ void prefetch_part(const Bf16Params &p, const Item &w, int lane, int lane0, int col0)
-{
-    const T *D = static_cast<const T *>(p.D) + (p.mode == kBf16GroupK ? w.group * p.stride_c : 0);
-    const int rows = p.swap ? Cfg::CW : 32, cols = p.swap ? 32 : Cfg::CW;
-    const int m = w.m + (p.swap ? col0 : lane0), n = w.n + (p.swap ? lane0 : col0);
-    for (int r = lane; r < rows && m + r < w.m_end; r += 32)
-        for (int c = 0; c < cols && n + c < p.N; c += 128 / (int)sizeof(T))
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(D + (m + r) * p.ldd + n + c));
 }
 
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
 bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_constant__ CUtensorMap mapQ,
-                    const __grid_constant__ Bf16Params p)
+                    const __grid_constant__ CUtensorMap mapD, const __grid_constant__ Bf16Params p)
 {
     constexpr int BN = Cfg::BN, STAGES = Cfg::STAGES, NBUF = Cfg::NBUF, CW = Cfg::CW, QR = Cfg::QR;
     constexpr bool PAIR = Cfg::PAIR;
@@ -521,6 +587,7 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
     auto iempty_bar = [&](uint32_t i) { return bars + 8u * (2 * STAGES + 2 * NBUF + kItems + i); };
     auto tail_bar = [&](int s) { return bars + 8u * (2 * STAGES + 2 * NBUF + 2 * kItems + s); };
     const uint32_t drain_bar = bars + 8u * (3 * STAGES + 2 * NBUF + 2 * kItems);
+    const uint32_t d_bars = drain_bar + 8;
     const uint32_t tmem_slot = bars + 8u * Cfg::NUM_BARS;
 
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -537,6 +604,7 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
     if (warp == 2 && lane == 0) {
         ptx::prefetch_tensormap(&mapP);
         ptx::prefetch_tensormap(&mapQ);
+        if (Cfg::JOINS) ptx::prefetch_tensormap(&mapD);
     }
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -554,6 +622,7 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
             ptx::mbar_init(iempty_bar(i), Cfg::EPI_WARPS + (group_k ? 3 : 2));
         }
         ptx::mbar_init(drain_bar, 1);
+        for (int i = 0; i < Cfg::D_BARS; ++i) ptx::mbar_init(d_bars + 8 * i, 1);
         ptx::mbar_init_fence();
     }
     if (warp == 1) tmem_alloc<PAIR>(tmem_slot, Cfg::TMEM_COLS);
@@ -807,6 +876,7 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
         if (Cfg::CAN_SPLIT && split > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         if constexpr (Cfg::MOVE_REGS) ptx::setmaxnreg_inc<216>();
         constexpr int CHUNK = Cfg::CHUNK;
+        Arrivals<Cfg> d{base + Cfg::OFF_D + ew * Cfg::D_BYTES, d_bars + 24u * ew, 0};
         uint32_t n = 0, acc = 0;
         // The next accumulator, once complete, and its way back to the MMA warp.
         auto take = [&](uint32_t &from) {
@@ -831,9 +901,9 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
                 break;
             }
             const Item w = load_item(item_at(n));
-            if (p.join != kJoinNone && split == 1) {
-                if (p.c_bf16) prefetch_part<__nv_bfloat16, Cfg>(p, w, lane, lane0, col0);
-                else prefetch_part<float, Cfg>(p, w, lane, lane0, col0);
+            if constexpr (Cfg::JOINS) {
+                d.next = 0;
+                d.ask(p, &mapD, w, lane, lane0, col0);
             }
             uint32_t from;
             if (part == INT32_MAX) {
@@ -847,7 +917,7 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
 #pragma unroll
                     for (int j = 0; j < CHUNK; ++j) z[j] = w.k0 < w.k1 ? __uint_as_float(v[j]) : 0.0f;
                     stage<CHUNK>(st, lane, p.swap, z);
-                });
+                }, &mapD, d);
                 give_back();
                 done_with(n);
                 continue;
@@ -878,7 +948,7 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
 #pragma unroll
                     for (int i = 0; i < CW; i += CHUNK)
                         if (c == i) stage<CHUNK>(st, lane, p.swap, sum + i);
-                });
+                }, &mapD, d);
             } else if constexpr (Cfg::CAN_SPLIT) {
                 // To the CTA that adds column j over the cluster: j % split.
                 const int per = BN / split, shift = __ffs(split) - 1;
@@ -891,6 +961,9 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
             }
             done_with(n);
         }
+        // What a role that gave up has asked for lands before the CTA leaves.
+        for (; d.asked != d.taken; ++d.taken) d.wait(p);
+        if (!d.ok) gave_up();
         __syncwarp();
         ptx::tc_fence_before();
     }
@@ -956,6 +1029,23 @@ cudaError_t encode_bf16(CUtensorMap *map, const void *ptr, int64_t inner, int64_
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Tensor map of D (of all groups' under GroupK), in boxes of a chunk.
+cudaError_t encode_d(CUtensorMap *map, const Bf16Args &g, int box_rows)
+{
+    const auto encode = tensor_map_encoder();
+    if (!encode) return cudaErrorNotSupported;
+    const int64_t size = g.c_bf16 ? 2 : 4, many = g.mode == kBf16GroupK ? g.groups : 1;
+    const cuuint64_t dims[3] = {(cuuint64_t)g.N, (cuuint64_t)g.M, (cuuint64_t)many};
+    const cuuint64_t strides[2] = {(cuuint64_t)(g.ldd * size), (cuuint64_t)((many > 1 ? g.stride_c : g.M * g.ldd) * size)};
+    const cuuint32_t box[3] = {32, (cuuint32_t)box_rows, 1};
+    const cuuint32_t elem[3] = {1, 1, 1};
+    const CUresult r = encode(map, g.c_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
+                              const_cast<void *>(g.D), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 template <class Cfg>
 cudaError_t prepare_cfg()
 {
@@ -965,6 +1055,14 @@ cudaError_t prepare_cfg()
 bool pieces16(const void *p, int64_t ld, int64_t per16)
 {
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % per16 == 0;
+}
+
+// Whether C, pre and D can be accessed 16 bytes at a time.
+bool in_pieces(const Bf16Args &g)
+{
+    const int64_t per16 = g.c_bf16 ? 8 : 4;
+    return pieces16(g.C, g.ldc, per16) && (!g.pre || pieces16(g.pre, g.ld_pre, per16)) &&
+           (g.join == kJoinNone || pieces16(g.D, g.ldd, per16)) && (g.mode != kBf16GroupK || g.stride_c % per16 == 0);
 }
 
 template <class Cfg>
@@ -1022,12 +1120,12 @@ cudaError_t launch_cfg(const Bf16Args &g, const Bf16Plan &plan, cudaStream_t str
     p.ldc = g.ldc;
     p.stride_c = g.stride_c;
     p.c_bf16 = g.c_bf16;
-    const int64_t per16 = g.c_bf16 ? 8 : 4;
-    p.vec = pieces16(g.C, g.ldc, per16) && (!g.pre || pieces16(g.pre, g.ld_pre, per16)) &&
-            (g.join == kJoinNone || pieces16(g.D, g.ldd, per16)) && (g.mode != kBf16GroupK || g.stride_c % per16 == 0);
+    p.vec = in_pieces(g);
     p.status = g.status;
     CUtensorMap &mp = plan.swap ? map_b : map_a, &mq = plan.swap ? map_a : map_b;
-    void *args[] = {&mp, &mq, &p};
+    CUtensorMap map_d = map_a;                        // any valid one where D does not come by it
+    if (Cfg::JOINS && (e = encode_d(&map_d, g, Cfg::CHUNK)) != cudaSuccess) return e;
+    void *args[] = {&mp, &mq, &map_d, &p};
     cudaLaunchConfig_t lc = {};
     cudaLaunchAttribute attrs[1];
     const unsigned cluster = Cfg::PAIR ? 2u : (unsigned)plan.split;
@@ -1049,6 +1147,8 @@ cudaError_t launch_cfg(const Bf16Args &g, const Bf16Plan &plan, cudaStream_t str
 
 using Pair256 = Bf16Cfg<256, true>;
 using Pair128 = Bf16Cfg<128, true>;
+using Pair256Joins = Bf16Cfg<256, true, true>;
+using Pair128Joins = Bf16Cfg<128, true, true>;
 using One128 = Bf16Cfg<128, false>;
 using One64 = Bf16Cfg<64, false>;
 using One32 = Bf16Cfg<32, false>;
@@ -1104,6 +1204,8 @@ cudaError_t prepare_bf16()
 {
     cudaError_t e = prepare_cfg<Pair256>();
     if (e == cudaSuccess) e = prepare_cfg<Pair128>();
+    if (e == cudaSuccess) e = prepare_cfg<Pair256Joins>();
+    if (e == cudaSuccess) e = prepare_cfg<Pair128Joins>();
     if (e == cudaSuccess) e = prepare_cfg<One128>();
     if (e == cudaSuccess) e = prepare_cfg<One64>();
     if (e == cudaSuccess) e = prepare_cfg<One32>();
@@ -1115,6 +1217,8 @@ cudaError_t launch_bf16(const Bf16Args &g, cudaStream_t stream)
 {
     const Bf16Plan p = plan_bf16(g);
     if (p.grid == 0) return cudaSuccess;
+    if (p.pair && g.join != kJoinNone && in_pieces(g))
+        return p.cols == 256 ? launch_cfg<Pair256Joins>(g, p, stream) : launch_cfg<Pair128Joins>(g, p, stream);
     if (p.pair) return p.cols == 256 ? launch_cfg<Pair256>(g, p, stream) : launch_cfg<Pair128>(g, p, stream);
     return p.cols == 128  ? launch_cfg<One128>(g, p, stream)
            : p.cols == 64 ? launch_cfg<One64>(g, p, stream)

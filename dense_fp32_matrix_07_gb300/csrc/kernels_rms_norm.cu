@@ -25,60 +25,6 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 
-// Eight neighbouring values of a row as they are stored, by 16-byte accesses.
-template <class T>
-struct Raw8 {
-    uint4 u[sizeof(T) / 2];
-    __device__ __forceinline__ void load(const T *p)
-    {
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = reinterpret_cast<const uint4 *>(p)[i];
-    }
-    __device__ __forceinline__ void zero()
-    {
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = make_uint4(0, 0, 0, 0);
-    }
-    // The first n of them.
-    __device__ __forceinline__ void load_some(const T *p, int n)
-    {
-        uint32_t w[2 * sizeof(T)] = {};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (e >= n) continue;
-            if constexpr (sizeof(T) == 4) w[e] = __float_as_uint(p[e]);
-            else w[e / 2] |= (uint32_t) * reinterpret_cast<const uint16_t *>(p + e) << (16 * (e & 1));
-        }
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-    }
-    __device__ __forceinline__ float get(int e) const
-    {
-        const uint4 &q = u[sizeof(T) == 4 ? e / 4 : 0];
-        const int i = sizeof(T) == 4 ? e % 4 : e / 2;
-        const uint32_t x = i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w;
-        if constexpr (sizeof(T) == 4) return __uint_as_float(x);
-        else return __uint_as_float((e & 1) ? x & 0xffff0000u : x << 16);
-    }
-};
-
-__device__ __forceinline__ void store8(float *p, const float (&v)[8])
-{
-    reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
-
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8])
-{
-    uint32_t u[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-        u[j] = *reinterpret_cast<const uint32_t *>(&h);
-    }
-    *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
-}
-
 // The threads that share a row: a warp each (WARPS = 1, eight rows a block) or
 // the whole block.
 template <int WARPS>
@@ -298,11 +244,19 @@ rms_norm_backward_kernel(const __grid_constant__ NormBackwardParams<T> p)
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[k][e] = 0.0f;
     int turn = 0;
-    for (int64_t r = (int64_t)blockIdx.x * Tm::ROWS + Tm::row(); r < p.rows; r += (int64_t)gridDim.x * Tm::ROWS, turn ^= 1) {
-        Raw8<T> x[PACKS], g[PACKS], gs[PACKS];
+    // Rows in whole pieces are requested one row ahead (XX us for
+    // 16383 x 2048 bfloat16 with a gradient along the residual).
+    const int64_t step = (int64_t)gridDim.x * Tm::ROWS;
+    int64_t r = (int64_t)blockIdx.x * Tm::ROWS + Tm::row();
+    Raw8<T> x[PACKS], g[PACKS], gs[PACKS];
+    auto load = [&](int64_t r) {
         load_row<T, WARPS, PACKS, VEC>(p.x + r * p.ldx, cols, line, x);
         load_row<T, WARPS, PACKS, VEC>(p.g + r * p.ld_g, cols, line, g);
         if (p.gs) load_row<T, WARPS, PACKS, VEC>(p.gs + r * p.ld_gs, cols, line, gs);
+    };
+    if (VEC && r < p.rows) load(r);
+    for (; r < p.rows; r += step, turn ^= 1) {
+        if constexpr (!VEC) load(r);
         float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int k = 0; k < PACKS; ++k) {
@@ -314,6 +268,13 @@ rms_norm_backward_kernel(const __grid_constant__ NormBackwardParams<T> p)
                 s.y = fmaf(p.weight ? g[k].get(e) * w[e] : g[k].get(e), x[k].get(e), s.y);
             }
         }
+        Raw8<T> x0[PACKS], g0[PACKS], gs0[PACKS];
+#pragma unroll
+        for (int k = 0; k < PACKS; ++k) {
+            x0[k] = x[k], g0[k] = g[k];
+            if (p.gs) gs0[k] = gs[k];
+        }
+        if (VEC && r + step < p.rows) load(r + step);
         s = Tm::sum(s, turn);
         const float inv = rsqrtf(s.x / (float)cols + p.eps);
         const float mean = s.y * inv / (float)cols;     // of g w h
@@ -326,10 +287,10 @@ rms_norm_backward_kernel(const __grid_constant__ NormBackwardParams<T> p)
             if (p.weight) load_weight(p.weight, c, cols, p.weight16, w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float h = x[k].get(e) * inv, gw = p.weight ? g[k].get(e) * w[e] : g[k].get(e);
-                dw[k][e] = fmaf(g[k].get(e), h, dw[k][e]);
+                const float h = x0[k].get(e) * inv, gw = p.weight ? g0[k].get(e) * w[e] : g0[k].get(e);
+                dw[k][e] = fmaf(g0[k].get(e), h, dw[k][e]);
                 d[e] = inv * (gw - h * mean);
-                if (p.gs) d[e] += gs[k].get(e);
+                if (p.gs) d[e] += gs0[k].get(e);
             }
             store_pack<T, VEC>(to, line, c, cols, d);
         }
@@ -364,21 +325,21 @@ rms_norm_backward_kernel(const __grid_constant__ NormBackwardParams<T> p)
     }
 }
 
-// out[c] = sum of parts[.][c], in order within 8 interleaved runs.
-__global__ void __launch_bounds__(256) add_parts_kernel(const float *parts, int count, int cols, float *out)
+// out[c] = sum of parts[.][c], in order within 32 interleaved runs.
+__global__ void __launch_bounds__(1024) add_parts_kernel(const float *parts, int count, int cols, float *out)
 {
-    __shared__ float sums[8][33];
+    __shared__ float sums[32][33];
     const int lane = threadIdx.x % 32, run = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
     float s = 0.0f;
     if (c < cols) {
 #pragma unroll 8
-        for (int i = run; i < count; i += 8) s += parts[(int64_t)i * cols + c];
+        for (int i = run; i < count; i += 32) s += parts[(int64_t)i * cols + c];
     }
     sums[run][lane] = s;
     __syncthreads();
     if (run == 0 && c < cols) {
 #pragma unroll
-        for (int i = 1; i < 8; ++i) s += sums[i][lane];
+        for (int i = 1; i < 32; ++i) s += sums[i][lane];
         out[c] = s;
     }
 }
@@ -475,7 +436,7 @@ cudaError_t norm_backward_of(const RmsNormBackwardArgs &g, void *scratch, cudaSt
                         : vec ? launch(rms_norm_backward_kernel<T, W, P, true>, grid, Team<W>::THREADS, bytes, &p, stream)
                             : launch(rms_norm_backward_kernel<T, W, P, false>, grid, Team<W>::THREADS, bytes, &p, stream);
         if (e != cudaSuccess || !g.grad_weight) return e;
-        add_parts_kernel<<<(unsigned)((g.cols + 31) / 32), 256, 0, stream>>>(p.parts, (int)grid, (int)g.cols, g.grad_weight);
+        add_parts_kernel<<<(unsigned)((g.cols + 31) / 32), 1024, 0, stream>>>(p.parts, (int)grid, (int)g.cols, g.grad_weight);
         return cudaGetLastError();
     });
 }

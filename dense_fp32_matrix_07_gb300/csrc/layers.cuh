@@ -137,6 +137,60 @@ struct alignas(sizeof(T) * N) Values {
     T v[N];
 };
 
+// Eight neighbouring values of a row as they are stored, by 16-byte accesses.
+template <class T>
+struct Raw8 {
+    uint4 u[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T *p)
+    {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = reinterpret_cast<const uint4 *>(p)[i];
+    }
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = make_uint4(0, 0, 0, 0);
+    }
+    // The first n of them.
+    __device__ __forceinline__ void load_some(const T *p, int n)
+    {
+        uint32_t w[2 * sizeof(T)] = {};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (e >= n) continue;
+            if constexpr (sizeof(T) == 4) w[e] = __float_as_uint(p[e]);
+            else w[e / 2] |= (uint32_t) * reinterpret_cast<const uint16_t *>(p + e) << (16 * (e & 1));
+        }
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+    __device__ __forceinline__ float get(int e) const
+    {
+        const uint4 &q = u[sizeof(T) == 4 ? e / 4 : 0];
+        const int i = sizeof(T) == 4 ? e % 4 : e / 2;
+        const uint32_t x = i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w;
+        if constexpr (sizeof(T) == 4) return __uint_as_float(x);
+        else return __uint_as_float((e & 1) ? x & 0xffff0000u : x << 16);
+    }
+};
+
+__device__ __forceinline__ void store8(float *p, const float (&v)[8])
+{
+    reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8])
+{
+    uint32_t u[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+        u[j] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+}
+
 // exp(x) by one multiplication and the hardware's 2^x: 2^-22 relative, and
 // |x| 2^-24 from the rounded argument, which matters where exp(x) itself is
 // small beside what it is added to.
