@@ -403,7 +403,7 @@ __device__ __forceinline__ void store_chunk(const Bf16Params &p, const Place<T> 
     constexpr int PER_ROW = 32 / V, PER_PASS = 32 / PER_ROW, PASSES = R / PER_PASS;
     // Rows whose sums are in registers together: of one, each activation would
     // wait for the one before (600 cycles a row where C goes by single values).
-    constexpr int MOST = V == 1 ? 16 : 4, AHEAD = PASSES < MOST ? PASSES : MOST;
+    constexpr int MOST = V == 1 ? 8 : V == 4 ? 2 : 4, AHEAD = PASSES < MOST ? PASSES : MOST;
     const int r0 = lane / PER_ROW, c0 = (lane % PER_ROW) * V;
     const bool whole = V == 1 ? c0 < cols : c0 + V <= cols;
     Values<T, V> d[AHEAD];
@@ -983,15 +983,53 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
                 const uint32_t part = base + Cfg::OFF_EXTRA;
                 const int per = BN / split;
                 auto add = [&](auto q) {
-                    for (int i = threadIdx.x; i < per * 128; i += Cfg::THREADS) {
-                        const int m = w.m + (i >> 7) * split + rank, n = w.n + (i & 127);
-                        if (m < w.m_end && n < p.N) {
-                            float v = 0.0f;
+                    using T = std::remove_reference_t<decltype(*q.C)>;
+                    constexpr int V = 16 / (int)sizeof(T), PER_COL = 128 / V;
+                    for (int i = threadIdx.x; i < per * PER_COL; i += Cfg::THREADS) {
+                        const int col = i / PER_COL, at = i % PER_COL * V;
+                        const int m = w.m + col * split + rank, n = w.n + at;
+                        if (m >= w.m_end || n >= p.N) continue;
+                        const bool whole = p.vec && n + V <= p.N;
+                        Values<T, V> d;
+                        if (whole && q.D) d = *reinterpret_cast<const Values<T, V> *>(q.D + m * p.ldd + n);
+                        float z[V] = {};
 #pragma unroll
-                            for (int r = 0; r < 8; ++r)
-                                if (r < split) v += ld_shared_f32(part + 4 * (r * per * 128 + i));
-                            store_one(p, q, m, n, v);
+                        for (int r = 0; r < 8; ++r) {
+                            if (r >= split) continue;
+#pragma unroll
+                            for (int e = 0; e < V; e += 4) {
+                                const uint4 u = ld_shared_u32x4(part + 4 * ((r * per + col) * 128 + at + e));
+                                z[e] += __uint_as_float(u.x), z[e + 1] += __uint_as_float(u.y);
+                                z[e + 2] += __uint_as_float(u.z), z[e + 3] += __uint_as_float(u.w);
+                            }
                         }
+                        if (!whole) {
+#pragma unroll
+                            for (int e = 0; e < V; ++e)
+                                if (n + e < p.N) store_one(p, q, m, n + e, z[e]);
+                            continue;
+                        }
+                        if (q.bias) {
+#pragma unroll
+                            for (int e = 0; e < V; ++e) z[e] += __ldg(q.bias + n + e);
+                        }
+                        Values<T, V> o;
+                        if (q.pre) {
+#pragma unroll
+                            for (int e = 0; e < V; ++e) store_from_float(&o.v[e], z[e]);
+                            *reinterpret_cast<Values<T, V> *>(q.pre + m * p.ld_pre + n) = o;
+                        }
+                        with_activation(p.act, [&](auto a) {
+#pragma unroll
+                            for (int e = 0; e < V; ++e) z[e] = activate<decltype(a)::value>(z[e]);
+                        });
+                        if (q.D) {
+#pragma unroll
+                            for (int e = 0; e < V; ++e) z[e] = joined(z[e], load_as_float(&d.v[e]), p.join);
+                        }
+#pragma unroll
+                        for (int e = 0; e < V; ++e) store_from_float(&o.v[e], z[e]);
+                        *reinterpret_cast<Values<T, V> *>(q.C + m * p.ldc + n) = o;
                     }
                 };
                 if (p.c_bf16) add(place_of<__nv_bfloat16>(p, w.group));
