@@ -126,16 +126,17 @@ struct Bf16Params {
 // bring it there where the compiler cannot tell).
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(kAll, x, 0); }
 
-// One tile: its group, rows [m, m_end) and first column of C, its range of K.
+// One tile: its group, rows [m, m_end) and first column of C, its range of K,
+// and the accumulator's columns that it needs.
 struct Item {
-    int group, m, m_end, n, k0, k1, more;
+    int group, m, m_end, n, k0, k1, cols;
 };
 
 __device__ __forceinline__ void store_item(uint32_t at, const Item &w)
 {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w.group), "r"(w.m), "r"(w.m_end), "r"(w.n)
                  : "memory");
-    asm volatile("st.shared.v4.u32 [%0+16], {%1,%2,%3,%3};" ::"r"(at), "r"(w.k0), "r"(w.k1), "r"(w.more) : "memory");
+    asm volatile("st.shared.v4.u32 [%0+16], {%1,%2,%3,%3};" ::"r"(at), "r"(w.k0), "r"(w.k1), "r"(w.cols) : "memory");
 }
 
 __device__ __forceinline__ Item load_item(uint32_t at)
@@ -146,20 +147,30 @@ __device__ __forceinline__ Item load_item(uint32_t at)
                  : "r"(at)
                  : "memory");
     asm volatile("{\n\t.reg .u32 x;\n\tld.shared.v4.u32 {%0,%1,%2,x}, [%3+16];\n\t}"
-                 : "=r"(w.k0), "=r"(w.k1), "=r"(w.more)
+                 : "=r"(w.k0), "=r"(w.k1), "=r"(w.cols)
                  : "r"(at)
                  : "memory");
     w.group = uniform(w.group), w.m = uniform(w.m), w.m_end = uniform(w.m_end), w.n = uniform(w.n);
-    w.k0 = uniform(w.k0), w.k1 = uniform(w.k1), w.more = uniform(w.more);
+    w.k0 = uniform(w.k0), w.k1 = uniform(w.k1), w.cols = uniform(w.cols);
     return w;
 }
 
 __device__ __forceinline__ int slabs(int k0, int k1) { return (int)(((uint32_t)(k1 - k0) + kSlab - 1) / kSlab); }
 
+// An MMA's columns come in 16s, in 32s by a pair.
+template <class Cfg>
+__device__ __forceinline__ int whole_columns(int n)
+{
+    constexpr int unit = Cfg::PAIR ? 32 : 16;
+    const int up = (n + unit - 1) / unit * unit;
+    return up < unit ? unit : up < Cfg::BN ? up : Cfg::BN;
+}
+
+template <class Cfg>
 __device__ __forceinline__ Item find_item(const Bf16Params &p, const int *table, uint32_t t, int rank)
 {
     Item it;
-    it.group = it.more = 0;
+    it.group = 0;
     int rows = p.row_tiles;
     if (p.mode == kBf16GroupRows) rows = table[p.groups];
     if (p.mode == kBf16GroupK) {
@@ -179,13 +190,22 @@ __device__ __forceinline__ Item find_item(const Bf16Params &p, const int *table,
         it.group = find_group(table, p.groups, rt);
         int lo, hi;
         group_range(p.offsets, it.group, p.M, lo, hi);
-        it.m = lo + (rt - table[it.group]) * p.tm;
-        it.m_end = hi;
+        int tall = p.tm;
+        if (p.swap) {
+            // The group's rows evenly over its tiles: of 273, 160 and 113
+            // columns take less than 256 and 17.
+            const int tiles = (int)(((uint32_t)(hi - lo) + p.tm - 1) / (uint32_t)p.tm);
+            tall = whole_columns<Cfg>(tiles > 1 ? (hi - lo + tiles - 1) / tiles : hi - lo);
+        }
+        it.m = lo + (rt - table[it.group]) * tall;
+        it.m = it.m < hi ? it.m : hi;
+        it.m_end = hi - it.m < tall ? hi : it.m + tall;
     } else {
         it.m = rt * p.tm;
-        it.m_end = p.M;
+        it.m_end = p.M - it.m < p.tm ? p.M : it.m + p.tm;
         if (p.mode == kBf16GroupK) group_range(p.offsets, it.group, p.K, it.k0, it.k1);
     }
+    it.cols = whole_columns<Cfg>(p.swap ? it.m_end - it.m : p.N - it.n);
     if (p.split > 1) {
         const int n = slabs(0, p.K);
         const int64_t k1 = (int64_t)((int64_t)n * (rank + 1) / p.split) * kSlab;
@@ -477,8 +497,13 @@ __device__ __forceinline__ void store_chunk(const Bf16Params &p, const Place<T> 
                 if constexpr (TMA_D) {
 #pragma unroll
                     for (int i = 0; i < AHEAD; ++i) {
-                        const uint4 u = ld_shared_u32x4(dbuf + (uint32_t)sizeof(T) * (32 * (r0 + (i0 + i) * PER_PASS) + c0));
-                        d[i] = *reinterpret_cast<const Values<T, V> *>(&u);
+                        const uint32_t from = dbuf + (uint32_t)sizeof(T) * (32 * (r0 + (i0 + i) * PER_PASS) + c0);
+                        if constexpr (V == 1) {
+                            store_from_float(&d[i].v[0], ld_shared_f32(from));
+                        } else {
+                            const uint4 u = ld_shared_u32x4(from);
+                            d[i] = *reinterpret_cast<const Values<T, V> *>(&u);
+                        }
                     }
                 }
                 if (q.D) {
@@ -518,12 +543,24 @@ struct Arrivals {
     __device__ __forceinline__ uint32_t bar(const Bf16Params &p, uint32_t i) const { return bars + 8 * (i % depth(p)); }
     __device__ __forceinline__ uint32_t buffer(const Bf16Params &p, uint32_t i) const { return buffers + bytes(p) * (i % depth(p)); }
 
+    // (Floats that TMA cannot address: copied one by one, as asynchronously.)
     __device__ __forceinline__ void ask(const Bf16Params &p, const CUtensorMap *map, const Item &w, int lane, int lane0, int col0)
     {
         while (next < Cfg::CW && asked - taken < depth(p)) {
             const Chunk c(p, w, lane0, col0 + next);
             next += Cfg::CHUNK;
             if (!c.some()) continue;
+            if (!p.vec) {
+                const float *from = static_cast<const float *>(p.D) + (p.mode == kBf16GroupK ? w.group * p.stride_c : 0) +
+                                    c.m * p.ldd + c.n + lane;
+                const uint32_t to = buffer(p, asked) + 4 * lane;
+#pragma unroll 8
+                for (int r = 0; r < Cfg::CHUNK; ++r)
+                    if (r < c.rows && lane < c.cols)
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + 128 * r), "l"(from + r * p.ldd) : "memory");
+                ++asked;
+                continue;
+            }
             const uint32_t on = lane == 0;
             mbar_expect_if(on, bar(p, asked), bytes(p));
             tma_load_if(on, buffer(p, asked), map, bar(p, asked), c.n, c.m, p.mode == kBf16GroupK ? w.group : 0,
@@ -534,6 +571,10 @@ struct Arrivals {
     // Waits for the oldest chunk.
     __device__ __forceinline__ void wait(const Bf16Params &p)
     {
+        if (!p.vec) {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            return;
+        }
         const uint32_t b = bar(p, taken), phase = (taken / depth(p)) & 1;
         ok = wait_bar(mbar_test(b, phase), b, phase) && ok;
     }
@@ -553,8 +594,12 @@ __device__ __forceinline__ void store_part(const Bf16Params &p, const Item &w, u
         if (!at.some()) continue;
         auto chunk = [&]() { put(c); };
         if constexpr (Cfg::JOINS) {
-            store_chunk<T, CHUNK, V, true>(p, q, st, lane, chunk, at.m, at.rows, at.n, at.cols, d.buffer(p, d.taken),
-                                           [&]() { d.wait(p); });
+            const uint32_t from = d.buffer(p, d.taken);
+            auto there = [&]() { d.wait(p); };
+            if (sizeof(T) == 2 || p.vec)
+                store_chunk<T, CHUNK, V, true>(p, q, st, lane, chunk, at.m, at.rows, at.n, at.cols, from, there);
+            else
+                store_chunk<T, CHUNK, 1, true>(p, q, st, lane, chunk, at.m, at.rows, at.n, at.cols, from, there);
             ++d.taken;
             d.ask(p, map, w, lane, lane0, col0);
         } else if (p.vec) {
@@ -699,16 +744,16 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
         // ------------------------------ TMA producer ------------------------------
         const uint32_t on = elect_one();
         const uint64_t policy = ptx::policy_evict_last();
-        // Boxes of 64 rows (or columns of C) by 64 along K, or fewer rows for
-        // a narrow operand whose K is contiguous: the same number of copies
-        // whichever is, so that the loop has no branches but its own.
-        constexpr int Q_BOXES = QR > 64 ? QR / 64 : 1;
-        const uint32_t bytes = Cfg::P_TILE + (p.q_mn || QR >= 64 ? Q_BOXES * 8192 : QR * 128);
+        // Boxes of 64 along K by 64 rows (or columns of C), of the columns'
+        // operand, where its K is contiguous, 32 rows: as many as the tile
+        // needs, without branches.
+        constexpr int Q_BOXES = QR > 32 ? QR / 32 : 1;
+        const int q_rows = p.q_mn ? 64 : QR < 32 ? QR : 32, q_bytes = 128 * q_rows;
         const bool p_mn = p.p_mn, q_mn = p.q_mn;
-        auto load = [&](uint32_t dst, const CUtensorMap *map, uint32_t bar, bool mn, int row, int k, int z) {
+        auto load = [&](uint32_t yes, uint32_t dst, const CUtensorMap *map, uint32_t bar, bool mn, int row, int k, int z) {
             const int x = mn ? row : k, y = mn ? k : row;
-            if constexpr (PAIR) tma_load_pair_if(on, dst, map, bar, x, y, z, policy);
-            else tma_load_if(on, dst, map, bar, x, y, z, policy);
+            if constexpr (PAIR) tma_load_pair_if(on & yes, dst, map, bar, x, y, z, policy);
+            else tma_load_if(on & yes, dst, map, bar, x, y, z, policy);
         };
         uint32_t it = 0, n = 0, early = 1;
         bool ok = true;
@@ -721,7 +766,9 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
             done_with(n);
             const int z = p.mode == kBf16GroupRows ? w.group : 0;
             const int pz = p.swap ? z : 0, qz = p.swap ? 0 : z;
-            const int p_row = (p.swap ? w.n : w.m) + 128 * pair_rank, q_row = (p.swap ? w.m : w.n) + QR * pair_rank;
+            const int need = PAIR ? w.cols / 2 : w.cols;     // rows of the columns' operand here
+            const int p_row = (p.swap ? w.n : w.m) + 128 * pair_rank, q_row = (p.swap ? w.m : w.n) + need * pair_rank;
+            const uint32_t bytes = Cfg::P_TILE + (need + q_rows - 1) / q_rows * q_bytes;
             for (int k = w.k0; k < w.k1; k += kSlab, ++it) {
                 const int s = (int)(it % STAGES);
                 if (!wait_bar(early, done_bar(s), ((it / STAGES) & 1) ^ 1)) {
@@ -739,9 +786,10 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
                     mbar_expect_if(on, bar, bytes);
                 }
 #pragma unroll
-                for (int c = 0; c < 2; ++c) load(stage_p(s) + 8192 * c, &mapP, bar, p_mn, p_row + 64 * c, k, pz);
+                for (int c = 0; c < 2; ++c) load(1, stage_p(s) + 8192 * c, &mapP, bar, p_mn, p_row + 64 * c, k, pz);
 #pragma unroll
-                for (int c = 0; c < Q_BOXES; ++c) load(stage_q(s) + 8192 * c, &mapQ, bar, q_mn, q_row + 64 * c, k, qz);
+                for (int c = 0; c < Q_BOXES; ++c)
+                    load(c * q_rows < need, stage_q(s) + q_bytes * c, &mapQ, bar, q_mn, q_row + q_rows * c, k, qz);
                 const uint32_t next = it + 1;
                 early = mbar_test(done_bar((int)(next % STAGES)), ((next / STAGES) & 1) ^ 1);
             }
@@ -754,7 +802,6 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
         }
     } else if (warp == 1) {
         // ------------------------------ MMA issuer ------------------------------
-        const uint32_t idesc = idesc_bf16(Cfg::LANES, BN, p.p_mn, p.q_mn);
         const uint64_t desc_p = p.p_mn ? sdesc_rows(stage_p(0)) : ptx::sdesc_kmajor(stage_p(0), 128);
         const uint64_t desc_q = p.q_mn ? sdesc_rows(stage_q(0)) : ptx::sdesc_kmajor(stage_q(0), 128);
         const uint32_t upper = (uint32_t)(desc_p >> 32);   // stride, version, swizzle: 1024 bytes either way
@@ -773,6 +820,7 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
             const Item w = load_item(item_at(n));
             done_with(n);
             if (!leader) continue;
+            const uint32_t idesc = idesc_bf16(Cfg::LANES, w.cols, p.p_mn, p.q_mn);
             int k = w.k0;
             do {
                 const int b = (int)(acc % NBUF), first = k, end = w.k1 - k > part ? k + part : w.k1;
@@ -823,8 +871,7 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
         // ------------------------------ tiles ------------------------------
         uint32_t n = 0;
         for (uint32_t t = t_first; t < tiles; t += t_step, ++n) {
-            Item w = find_item(p, table, t, split > 1 ? rank : 0);
-            w.more = t + t_step < tiles;
+            const Item w = find_item<Cfg>(p, table, t, split > 1 ? rank : 0);
             // The place is free when the tile kItems before is stored.
             if (!wait_tile(iempty_bar(n % kItems), ((n / kItems) & 1) ^ 1, longest)) {
                 gave_up();
@@ -979,7 +1026,7 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
             // swapped). Nothing reaches into another CTA after this barrier.
             ptx::cluster_sync_all();
             if (t_first < tiles) {
-                const Item w = find_item(p, table, t_first, rank);
+                const Item w = find_item<Cfg>(p, table, t_first, rank);
                 const uint32_t part = base + Cfg::OFF_EXTRA;
                 const int per = BN / split;
                 auto add = [&](auto q) {
@@ -1118,7 +1165,7 @@ cudaError_t launch_cfg(const Bf16Args &g, const Bf16Plan &plan, cudaStream_t str
     p.q_mn = plan.swap ? a_mn : b_mn;
     CUtensorMap map_a, map_b;
     const int64_t bg = g.mode == kBf16GroupRows ? g.groups : 1;
-    const int q_rows = Cfg::QR < 64 ? Cfg::QR : 64, a_rows = plan.swap ? q_rows : 64, b_rows = plan.swap ? 64 : q_rows;
+    const int q_rows = Cfg::QR < 32 ? Cfg::QR : 32, a_rows = plan.swap ? q_rows : 64, b_rows = plan.swap ? 64 : q_rows;
     cudaError_t e;
     if (g.K > 0) {
         const int64_t a_outer = a_mn ? g.K : g.M, b_outer = b_mn ? g.K : g.N;
@@ -1162,7 +1209,7 @@ cudaError_t launch_cfg(const Bf16Args &g, const Bf16Plan &plan, cudaStream_t str
     p.status = g.status;
     CUtensorMap &mp = plan.swap ? map_b : map_a, &mq = plan.swap ? map_a : map_b;
     CUtensorMap map_d = map_a;                        // any valid one where D does not come by it
-    if (Cfg::JOINS && (e = encode_d(&map_d, g, Cfg::CHUNK)) != cudaSuccess) return e;
+    if (Cfg::JOINS && p.vec && (e = encode_d(&map_d, g, Cfg::CHUNK)) != cudaSuccess) return e;
     void *args[] = {&mp, &mq, &map_d, &p};
     cudaLaunchConfig_t lc = {};
     cudaLaunchAttribute attrs[1];
@@ -1255,7 +1302,7 @@ cudaError_t launch_bf16(const Bf16Args &g, cudaStream_t stream)
 {
     const Bf16Plan p = plan_bf16(g);
     if (p.grid == 0) return cudaSuccess;
-    if (p.pair && g.join != kJoinNone && in_pieces(g))
+    if (p.pair && g.join != kJoinNone && (in_pieces(g) || !g.c_bf16))
         return p.cols == 256 ? launch_cfg<Pair256Joins>(g, p, stream) : launch_cfg<Pair128Joins>(g, p, stream);
     if (p.pair) return p.cols == 256 ? launch_cfg<Pair256>(g, p, stream) : launch_cfg<Pair128>(g, p, stream);
     return p.cols == 128  ? launch_cfg<One128>(g, p, stream)
