@@ -82,16 +82,16 @@ struct Bf16Cfg {
     // Partial sums of a split tile lie where whole tiles are staged.
     static constexpr int PARTIAL = CAN_SPLIT ? BN * 128 * 4 : 0;
     static constexpr int EXTRA = PARTIAL > EPI_WARPS * kStaging ? PARTIAL : EPI_WARPS * kStaging;
-    // Each epilogue warp's chunks of D: three of bfloat16 or one of floats.
-    static constexpr int D_BYTES = JOINS ? 3 * 32 * 32 * 2 : 0;
-    static constexpr int D_BARS = JOINS ? 3 * EPI_WARPS : 0;
+    // Each epilogue warp's chunks of D: four of bfloat16 or two of floats.
+    static constexpr int D_BYTES = JOINS ? 4 * 32 * 32 * 2 : 0;
+    static constexpr int D_BARS = JOINS ? 4 * EPI_WARPS : 0;
     static constexpr int NUM_BARS = 3 * STAGES + 2 * NBUF + 2 * kItems + 1 + D_BARS;
     static constexpr int OFF_EXTRA = STAGES * STAGE_BYTES;
     static constexpr int OFF_D = OFF_EXTRA + EXTRA;
     static constexpr int OFF_ITEMS = OFF_D + EPI_WARPS * D_BYTES;
     static constexpr int OFF_TABLE = OFF_ITEMS + kItems * kItemBytes;
     static constexpr int OFF_BARS = OFF_TABLE + (kMaxGroups + 2) * 4;
-    static constexpr int SMEM_BYTES = 1024 + OFF_BARS + NUM_BARS * 8 + 16;
+    static constexpr int SMEM_BYTES = OFF_BARS + NUM_BARS * 8 + 16;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
     static_assert(TMEM_COLS <= 512 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "tensor memory columns");
     static_assert(OFF_BARS % 8 == 0 && STAGE_BYTES % 1024 == 0, "alignment");
@@ -166,11 +166,31 @@ __device__ __forceinline__ int whole_columns(int n)
     return up < unit ? unit : up < Cfg::BN ? up : Cfg::BN;
 }
 
+// How a grid of `units` pairs walks `tiles`: where the last wave would leave
+// half of them (or three quarters) idle, its tiles are cut into two (four)
+// pieces along the accumulator's columns.
+struct Walk {
+    uint32_t whole, pieces, steps;   // tiles that are not cut, pieces of the others, all in all
+    __device__ __forceinline__ Walk(uint32_t tiles, uint32_t units, bool cut)
+    {
+        const uint32_t last = tiles % units;
+        pieces = !cut || last == 0 || 2 * last > units ? 1 : 4 * last > units ? 2 : 4;
+        whole = tiles - last;
+        steps = whole + last * pieces;
+    }
+};
+
 template <class Cfg>
-__device__ __forceinline__ Item find_item(const Bf16Params &p, const int *table, uint32_t t, int rank)
+__device__ __forceinline__ Item find_item(const Bf16Params &p, const int *table, const Walk &walk, uint32_t t, int rank)
 {
     Item it;
     it.group = 0;
+    int piece = 0;
+    if (Cfg::PAIR && t >= walk.whole) {
+        const uint32_t over = t - walk.whole, shift = walk.pieces >> 1;   // of 1, 2 or 4
+        piece = (int)(over & (walk.pieces - 1));
+        t = walk.whole + (over >> shift);
+    }
     int rows = p.row_tiles;
     if (p.mode == kBf16GroupRows) rows = table[p.groups];
     if (p.mode == kBf16GroupK) {
@@ -206,6 +226,19 @@ __device__ __forceinline__ Item find_item(const Bf16Params &p, const int *table,
         if (p.mode == kBf16GroupK) group_range(p.offsets, it.group, p.K, it.k0, it.k1);
     }
     it.cols = whole_columns<Cfg>(p.swap ? it.m_end - it.m : p.N - it.n);
+    if (Cfg::PAIR && t >= walk.whole && walk.pieces > 1) {
+        const int wide = whole_columns<Cfg>((it.cols + (int)walk.pieces - 1) / (int)walk.pieces);
+        it.cols = wide;
+        if (p.swap) {
+            it.m = it.m_end - it.m < piece * wide ? it.m_end : it.m + piece * wide;
+            it.m_end = it.m_end - it.m < wide ? it.m_end : it.m + wide;
+        } else {
+            // Columns past the tile's: this piece has none.
+            const int end = it.n + Cfg::BN;
+            it.n += piece * wide;
+            if (it.n >= end) it.m_end = it.m;
+        }
+    }
     if (p.split > 1) {
         const int n = slabs(0, p.K);
         const int64_t k1 = (int64_t)((int64_t)n * (rank + 1) / p.split) * kSlab;
@@ -525,6 +558,7 @@ struct Chunk {
     __device__ __forceinline__ Chunk(const Bf16Params &p, const Item &w, int lane0, int col)
         : m(w.m + (p.swap ? col : lane0)), n(w.n + (p.swap ? lane0 : col)), rows(w.m_end - m), cols(p.N - n)
     {
+        if (!p.swap && cols > w.cols - col) cols = w.cols - col;
     }
     __device__ __forceinline__ bool some() const { return rows > 0 && cols > 0; }
 };
@@ -538,10 +572,10 @@ struct Arrivals {
     uint32_t asked = 0, taken = 0;
     bool ok = true;
 
-    __device__ __forceinline__ uint32_t depth(const Bf16Params &p) const { return p.c_bf16 ? 3 : 1; }
+    __device__ __forceinline__ uint32_t depth(const Bf16Params &p) const { return p.c_bf16 ? 4 : 2; }
     __device__ __forceinline__ uint32_t bytes(const Bf16Params &p) const { return Cfg::CHUNK * 32 * (p.c_bf16 ? 2 : 4); }
-    __device__ __forceinline__ uint32_t bar(const Bf16Params &p, uint32_t i) const { return bars + 8 * (i % depth(p)); }
-    __device__ __forceinline__ uint32_t buffer(const Bf16Params &p, uint32_t i) const { return buffers + bytes(p) * (i % depth(p)); }
+    __device__ __forceinline__ uint32_t bar(const Bf16Params &p, uint32_t i) const { return bars + 8 * (i & (depth(p) - 1)); }
+    __device__ __forceinline__ uint32_t buffer(const Bf16Params &p, uint32_t i) const { return buffers + bytes(p) * (i & (depth(p) - 1)); }
 
     // (Floats that TMA cannot address: copied one by one, as asynchronously.)
     __device__ __forceinline__ void ask(const Bf16Params &p, const CUtensorMap *map, const Item &w, int lane, int lane0, int col0)
@@ -575,7 +609,7 @@ struct Arrivals {
             asm volatile("cp.async.wait_all;" ::: "memory");
             return;
         }
-        const uint32_t b = bar(p, taken), phase = (taken / depth(p)) & 1;
+        const uint32_t b = bar(p, taken), phase = (taken >> (p.c_bf16 ? 2 : 1)) & 1;
         ok = wait_bar(mbar_test(b, phase), b, phase) && ok;
     }
 };
@@ -617,10 +651,10 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
 {
     constexpr int BN = Cfg::BN, STAGES = Cfg::STAGES, NBUF = Cfg::NBUF, CW = Cfg::CW, QR = Cfg::QR;
     constexpr bool PAIR = Cfg::PAIR;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = ptx::smem_addr(smem_raw);
-    const uint32_t base = (raw + 1023u) & ~1023u;
-    int *const table = reinterpret_cast<int *>(smem_raw + (base - raw) + Cfg::OFF_TABLE);
+    // The swizzle goes by the address: stages begin on 1024 bytes.
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t base = ptx::smem_addr(smem);
+    int *const table = reinterpret_cast<int *>(smem + Cfg::OFF_TABLE);
     const uint32_t bars = base + Cfg::OFF_BARS;
     auto stage_p = [&](int s) { return base + s * Cfg::STAGE_BYTES; };
     auto stage_q = [&](int s) { return base + s * Cfg::STAGE_BYTES + Cfg::P_TILE; };
@@ -639,7 +673,7 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
     const int split = Cfg::CAN_SPLIT ? p.split : 1;
     const int cluster = PAIR ? 2 : split;
     const int rank = cluster > 1 ? (int)ptx::cluster_ctarank() : 0;
-    if (cluster > 1 && ptx::cluster_nctarank() != (uint32_t)cluster) {
+    if ((base & 1023u) != 0 || (cluster > 1 && ptx::cluster_nctarank() != (uint32_t)cluster)) {
         // Launched without its cluster, it would reach for peers that do not exist.
         if (threadIdx.x == 0) atomicOr(p.status, kStatusLaunchConfig);
         return;
@@ -710,13 +744,15 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
     // The CTAs of a split tile write into each other's shared memory in the
     // end: each says that it has begun, and waits for the others before that.
     if (Cfg::CAN_SPLIT && split > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-    const uint32_t taddr = *reinterpret_cast<uint32_t *>(smem_raw + (tmem_slot - raw));
+    const uint32_t taddr = *reinterpret_cast<uint32_t *>(smem + (tmem_slot - base));
 
     const uint32_t t_first = blockIdx.x / cluster, t_step = gridDim.x / cluster;
     uint32_t tiles = (uint32_t)p.col_tiles * (uint32_t)(p.mode == kBf16Dense       ? p.row_tiles
                                                         : p.mode == kBf16GroupRows ? table[p.groups]
                                                                                    : p.row_tiles * p.groups);
     if (split > 1 && tiles > t_step) tiles = t_step;   // a split grid has one tile per cluster
+    const Walk walk(tiles, t_step, PAIR);
+    if (PAIR) tiles = walk.steps;
 
     // The CTA's nth tile, once warp 2 has found it; not to be read after done_with().
     const int longest = slabs(0, p.K);
@@ -871,7 +907,7 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
         // ------------------------------ tiles ------------------------------
         uint32_t n = 0;
         for (uint32_t t = t_first; t < tiles; t += t_step, ++n) {
-            const Item w = find_item<Cfg>(p, table, t, split > 1 ? rank : 0);
+            const Item w = find_item<Cfg>(p, table, walk, t, split > 1 ? rank : 0);
             // The place is free when the tile kItems before is stored.
             if (!wait_tile(iempty_bar(n % kItems), ((n / kItems) & 1) ^ 1, longest)) {
                 gave_up();
@@ -923,7 +959,7 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
         if (Cfg::CAN_SPLIT && split > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         if constexpr (Cfg::MOVE_REGS) ptx::setmaxnreg_inc<216>();
         constexpr int CHUNK = Cfg::CHUNK;
-        Arrivals<Cfg> d{base + Cfg::OFF_D + ew * Cfg::D_BYTES, d_bars + 24u * ew, 0};
+        Arrivals<Cfg> d{base + Cfg::OFF_D + ew * Cfg::D_BYTES, d_bars + 32u * ew, 0};
         uint32_t n = 0, acc = 0;
         // The next accumulator, once complete, and its way back to the MMA warp.
         auto take = [&](uint32_t &from) {
@@ -1026,7 +1062,7 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
             // swapped). Nothing reaches into another CTA after this barrier.
             ptx::cluster_sync_all();
             if (t_first < tiles) {
-                const Item w = find_item<Cfg>(p, table, t_first, rank);
+                const Item w = find_item<Cfg>(p, table, walk, t_first, rank);
                 const uint32_t part = base + Cfg::OFF_EXTRA;
                 const int per = BN / split;
                 auto add = [&](auto q) {
