@@ -10,7 +10,7 @@
 // cores cut the sums off after each 16 of K instead of rounding them, which
 // adds up along K (relative errors of 1.7e-6 at K = 2049, 4.4e-6 at 4096); it
 // is far below a bfloat16 C's rounding, but an FP32 C is summed in tensor
-// memory over 512 of K at a time, and these sums in FP32 registers.
+// memory over 768 of K at a time, and these sums in FP32 registers.
 //
 // A tile has 128 (or, by a pair of CTAs, 256) lanes of tensor memory, which
 // hold rows of C, and BN columns, which hold columns of C; with `swap` it is
@@ -49,7 +49,7 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kSlab = 64;        // K values per stage: 128 bytes of a row
-constexpr int kPart = 8;         // slabs that an FP32 C is summed over in tensor memory
+constexpr int kPart = 12;        // slabs that an FP32 C is summed over in tensor memory
 constexpr int kItems = 4;        // tiles found ahead of their sums
 constexpr int kItemBytes = 32;
 constexpr int kStaging = 4096;   // 32 x 32 floats on their way to C
@@ -1013,13 +1013,16 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
             do {
                 if (!(ok = take(from))) break;
                 if (k < w.k1) {
+                    // One load ahead of the additions.
+                    uint32_t v[2][16];
+                    tmem_ld_chunk<16>(from, v[0]);
 #pragma unroll
-                    for (int c = 0; c < CW; c += CHUNK) {
-                        uint32_t v[CHUNK];
-                        tmem_ld_chunk<CHUNK>(from + c, v);
-                        tmem_ld_wait_for<CHUNK>(v);
+                    for (int c = 0; c < CW; c += 16) {
+                        const int at = c / 16 % 2;
+                        tmem_ld_wait_for<16>(v[at]);
+                        if (c + 16 < CW) tmem_ld_chunk<16>(from + c + 16, v[at ^ 1]);
 #pragma unroll
-                        for (int j = 0; j < CHUNK; ++j) sum[c + j] += __uint_as_float(v[j]);
+                        for (int j = 0; j < 16; ++j) sum[c + j] += __uint_as_float(v[at][j]);
                     }
                 }
                 give_back();

@@ -116,7 +116,7 @@ __device__ __forceinline__ void load8(const T *row, int lane, int cols, Raw8<T> 
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             store_from_float(&x[e], lane + 32 * e < cols ? load_as_float(row + lane + 32 * e) : 0.0f);
-        v.load_some(x, 8);
+        v.load_some(x, 0, 8);
     }
 }
 

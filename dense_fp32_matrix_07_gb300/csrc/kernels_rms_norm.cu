@@ -12,8 +12,11 @@
 // stored value is rounded once. The gradient takes s as it was stored and
 // finds i again from it.
 //
-// Rows that are not in whole 16-byte pieces pass through shared memory, which
-// turns accesses of single neighbouring values into the threads' eights.
+// Rows that do not begin on 16 bytes (an odd number of columns): where all
+// matrices' rows lie alike, the threads' eights are shifted so that they begin
+// on 16 bytes, and only the row's ends are single values (4097 x 3001 floats
+// 32.6 -> XX us). Else, and for 8-bit values, whose blocks of 128 columns are
+// 16 lanes', rows pass through shared memory.
 #include "fp8_values.cuh"
 #include "layers.cuh"
 
@@ -63,11 +66,24 @@ struct Team {
     }
 };
 
-// Columns of a thread's pack k: 8 from here on.
+// How a row's eights lie: kWhole on 16 bytes, kShifted on 16 bytes from a
+// column before the first on, kStaged through shared memory.
+enum Layout : int { kStaged = 0, kShifted = 1, kWhole = 2 };
+
+// Columns of a thread's pack k: 8 from here on, `shift` before where they
+// would begin.
 template <int WARPS>
-__device__ __forceinline__ int column(int k)
+__device__ __forceinline__ int column(int k, int shift)
 {
-    return 8 * (Team<WARPS>::rank() + k * Team<WARPS>::SIZE);
+    return 8 * (Team<WARPS>::rank() + k * Team<WARPS>::SIZE) - shift;
+}
+
+// Values of a row before its first that lies on 16 bytes, taken from the 16
+// bytes before.
+template <class T, int LAYOUT>
+__device__ __forceinline__ int shift_of(const T *row)
+{
+    return LAYOUT == kShifted ? (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T)) : 0;
 }
 
 template <class T>
@@ -84,23 +100,33 @@ struct NormParams {
     int weight16;      // the weights lie on 16 bytes
 };
 
+// Eight weights from column c on, zeros outside the row.
 __device__ __forceinline__ void load_weight(const float *w, int c, int cols, bool whole16, float (&v)[8])
 {
-    if (whole16 && c + 8 <= cols) {
-        const float4 a = __ldg(reinterpret_cast<const float4 *>(w + c)), b = __ldg(reinterpret_cast<const float4 *>(w + c) + 1);
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    const int off = c & 3;
+    if (whole16 && c >= 0 && c + (off ? 12 - off : 8) <= cols) {
+        const float4 *at = reinterpret_cast<const float4 *>(w + (c - off));
+        const float4 a = __ldg(at), b = __ldg(at + 1);
+        float f[12] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        if (off) {
+            const float4 d = __ldg(at + 2);
+            f[8] = d.x, f[9] = d.y, f[10] = d.z, f[11] = d.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = off == 0 ? f[e] : off == 1 ? f[e + 1] : off == 2 ? f[e + 2] : f[e + 3 < 12 ? e + 3 : 0];
         return;
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? __ldg(w + c + e) : 0.0f;
+    for (int e = 0; e < 8; ++e) v[e] = c + e >= 0 && c + e < cols ? __ldg(w + c + e) : 0.0f;
 }
 
-// A thread's eights of a row, zeros past the end; !VEC: through `line`.
-template <class T, int WARPS, int PACKS, bool VEC>
-__device__ __forceinline__ void load_row(const T *row, int cols, T *line, Raw8<T> (&v)[PACKS])
+// A thread's eights of a row, zeros outside it; kStaged: through `line`.
+template <class T, int WARPS, int PACKS, int LAYOUT>
+__device__ __forceinline__ void load_row(const T *row, int cols, int shift, T *line, Raw8<T> (&v)[PACKS])
 {
     using Tm = Team<WARPS>;
-    if constexpr (!VEC) {
+    if constexpr (LAYOUT == kStaged) {
         Tm::sync();
 #pragma unroll 4
         for (int c = Tm::rank(); c < (cols + 7) / 8 * 8; c += Tm::SIZE) store_from_float(line + c, c < cols ? load_as_float(row + c) : 0.0f);
@@ -108,10 +134,10 @@ __device__ __forceinline__ void load_row(const T *row, int cols, T *line, Raw8<T
     }
 #pragma unroll
     for (int k = 0; k < PACKS; ++k) {
-        const int c = column<WARPS>(k);
-        if constexpr (VEC) {
-            if (c + 8 <= cols) v[k].load(row + c);
-            else v[k].load_some(row + c, cols - c);
+        const int c = column<WARPS>(k, shift);
+        if constexpr (LAYOUT != kStaged) {
+            if (c >= 0 && c + 8 <= cols) v[k].load(row + c);
+            else v[k].load_some(row + c, -c, cols - c);
         } else {
             if (c < cols) v[k].load(line + c);
             else v[k].zero();
@@ -119,22 +145,22 @@ __device__ __forceinline__ void load_row(const T *row, int cols, T *line, Raw8<T
     }
 }
 
-// A thread's eight from column c on to a row (!VEC: to `line`).
-template <class T, bool VEC>
+// A thread's eight from column c on to a row (kStaged: to `line`).
+template <class T, int LAYOUT>
 __device__ __forceinline__ void store_pack(T *row, T *line, int c, int cols, const float (&v)[8])
 {
-    if constexpr (!VEC) {
+    if constexpr (LAYOUT == kStaged) {
         if (c < cols) store8(line + c, v);
-    } else if (c + 8 <= cols) {
+    } else if (c >= 0 && c + 8 <= cols) {
         store8(row + c, v);
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            if (c + e < cols) store_from_float(row + c + e, v[e]);
+            if (c + e >= 0 && c + e < cols) store_from_float(row + c + e, v[e]);
     }
 }
 
-// !VEC: `line`, as the team has stored it, to a row.
+// kStaged: `line`, as the team has stored it, to a row.
 template <class T, int WARPS>
 __device__ __forceinline__ void store_line(T *row, const T *line, int cols)
 {
@@ -144,7 +170,7 @@ __device__ __forceinline__ void store_line(T *row, const T *line, int cols)
     for (int c = Tm::rank(); c < cols; c += Tm::SIZE) row[c] = line[c];
 }
 
-template <class T, int WARPS, int PACKS, bool VEC>
+template <class T, int WARPS, int PACKS, int LAYOUT>
 __global__ void __launch_bounds__(Team<WARPS>::THREADS)
 rms_norm_kernel(const __grid_constant__ NormParams<T> p)
 {
@@ -152,13 +178,13 @@ rms_norm_kernel(const __grid_constant__ NormParams<T> p)
     extern __shared__ uint4 staging[];
     const int64_t r = (int64_t)blockIdx.x * Tm::ROWS + Tm::row();
     if (r >= p.rows) return;          // whole teams
-    const int cols = p.cols;
+    const int cols = p.cols, shift = shift_of<T, LAYOUT>(p.x + r * p.ldx);
     T *const line = reinterpret_cast<T *>(staging) + Tm::row() * ((cols + 7) / 8 * 8);
     float v[PACKS][8];
     {
         Raw8<T> x[PACKS], a[PACKS];
-        load_row<T, WARPS, PACKS, VEC>(p.x + r * p.ldx, cols, line, x);
-        if (p.residual) load_row<T, WARPS, PACKS, VEC>(p.residual + r * p.ld_res, cols, line, a);
+        load_row<T, WARPS, PACKS, LAYOUT>(p.x + r * p.ldx, cols, shift, line, x);
+        if (p.residual) load_row<T, WARPS, PACKS, LAYOUT>(p.residual + r * p.ld_res, cols, shift, line, a);
 #pragma unroll
         for (int k = 0; k < PACKS; ++k)
 #pragma unroll
@@ -174,17 +200,17 @@ rms_norm_kernel(const __grid_constant__ NormParams<T> p)
 
     if (p.sum) {
         T *const to = p.sum + r * p.ld_sum;
-        if constexpr (!VEC) Tm::sync();
+        if constexpr (LAYOUT == kStaged) Tm::sync();
 #pragma unroll
-        for (int k = 0; k < PACKS; ++k) store_pack<T, VEC>(to, line, column<WARPS>(k), cols, v[k]);
-        if constexpr (!VEC) {
+        for (int k = 0; k < PACKS; ++k) store_pack<T, LAYOUT>(to, line, column<WARPS>(k, shift), cols, v[k]);
+        if constexpr (LAYOUT == kStaged) {
             store_line<T, WARPS>(to, line, cols);
             Tm::sync();
         }
     }
 #pragma unroll
     for (int k = 0; k < PACKS; ++k) {
-        const int c = column<WARPS>(k);
+        const int c = column<WARPS>(k, shift);
         if (p.weight) {
             float w[8];
             load_weight(p.weight, c, cols, p.weight16, w);
@@ -194,8 +220,8 @@ rms_norm_kernel(const __grid_constant__ NormParams<T> p)
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[k][e] *= inv;
         }
-        if (p.y) store_pack<T, VEC>(p.y + r * p.ldy, line, c, cols, v[k]);
-        if (p.q) {
+        if (p.y) store_pack<T, LAYOUT>(p.y + r * p.ldy, line, c, cols, v[k]);
+        if (LAYOUT != kShifted && p.q) {
             // A block of 128 columns lies in 16 neighbouring lanes.
             uint32_t most = 0;
 #pragma unroll
@@ -212,7 +238,7 @@ rms_norm_kernel(const __grid_constant__ NormParams<T> p)
             }
         }
     }
-    if constexpr (!VEC) {
+    if constexpr (LAYOUT == kStaged) {
         if (p.y) store_line<T, WARPS>(p.y + r * p.ldy, line, cols);
     }
 }
@@ -230,7 +256,7 @@ struct NormBackwardParams {
     int weight16;
 };
 
-template <class T, int WARPS, int PACKS, bool VEC>
+template <class T, int WARPS, int PACKS, int LAYOUT>
 __global__ void __launch_bounds__(Team<WARPS>::THREADS)
 rms_norm_backward_kernel(const __grid_constant__ NormBackwardParams<T> p)
 {
@@ -238,63 +264,78 @@ rms_norm_backward_kernel(const __grid_constant__ NormBackwardParams<T> p)
     extern __shared__ uint4 staging[];
     const int cols = p.cols, padded = (cols + 7) / 8 * 8;
     T *const line = reinterpret_cast<T *>(staging) + Tm::row() * padded;
+    // Shifted eights are other columns in every row: their weight gradients
+    // are summed in shared memory, a row of them per team, column by column.
+    float *const columns = reinterpret_cast<float *>(staging) + Tm::row() * padded;
     float dw[PACKS][8];
 #pragma unroll
     for (int k = 0; k < PACKS; ++k)
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[k][e] = 0.0f;
+    if (LAYOUT == kShifted && p.parts) {
+        for (int c = Tm::rank(); c < padded; c += Tm::SIZE) columns[c] = 0.0f;
+        Tm::sync();
+    }
     int turn = 0;
-    // Rows in whole pieces are requested one row ahead (XX us for
-    // 16383 x 2048 bfloat16 with a gradient along the residual).
+    // Rows are requested one ahead (63 -> 57 us for 16383 x 2048 bfloat16 with
+    // a gradient along the residual).
+    constexpr bool AHEAD = LAYOUT != kStaged;
     const int64_t step = (int64_t)gridDim.x * Tm::ROWS;
     int64_t r = (int64_t)blockIdx.x * Tm::ROWS + Tm::row();
     Raw8<T> x[PACKS], g[PACKS], gs[PACKS];
     auto load = [&](int64_t r) {
-        load_row<T, WARPS, PACKS, VEC>(p.x + r * p.ldx, cols, line, x);
-        load_row<T, WARPS, PACKS, VEC>(p.g + r * p.ld_g, cols, line, g);
-        if (p.gs) load_row<T, WARPS, PACKS, VEC>(p.gs + r * p.ld_gs, cols, line, gs);
+        const int shift = shift_of<T, LAYOUT>(p.x + r * p.ldx);
+        load_row<T, WARPS, PACKS, LAYOUT>(p.x + r * p.ldx, cols, shift, line, x);
+        load_row<T, WARPS, PACKS, LAYOUT>(p.g + r * p.ld_g, cols, shift, line, g);
+        if (p.gs) load_row<T, WARPS, PACKS, LAYOUT>(p.gs + r * p.ld_gs, cols, shift, line, gs);
     };
-    if (VEC && r < p.rows) load(r);
+    if (AHEAD && r < p.rows) load(r);
     for (; r < p.rows; r += step, turn ^= 1) {
-        if constexpr (!VEC) load(r);
+        if (!AHEAD) load(r);
+        const int shift = shift_of<T, LAYOUT>(p.x + r * p.ldx);
         float2 s = make_float2(0.0f, 0.0f);
+        Raw8<T> x0[PACKS], g0[PACKS], gs0[PACKS];
 #pragma unroll
         for (int k = 0; k < PACKS; ++k) {
             float w[8];
-            if (p.weight) load_weight(p.weight, column<WARPS>(k), cols, p.weight16, w);
+            if (p.weight) load_weight(p.weight, column<WARPS>(k, shift), cols, p.weight16, w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 s.x = fmaf(x[k].get(e), x[k].get(e), s.x);
                 s.y = fmaf(p.weight ? g[k].get(e) * w[e] : g[k].get(e), x[k].get(e), s.y);
             }
-        }
-        Raw8<T> x0[PACKS], g0[PACKS], gs0[PACKS];
-#pragma unroll
-        for (int k = 0; k < PACKS; ++k) {
             x0[k] = x[k], g0[k] = g[k];
             if (p.gs) gs0[k] = gs[k];
         }
-        if (VEC && r + step < p.rows) load(r + step);
+        if (AHEAD && r + step < p.rows) load(r + step);
         s = Tm::sum(s, turn);
         const float inv = rsqrtf(s.x / (float)cols + p.eps);
         const float mean = s.y * inv / (float)cols;     // of g w h
         T *const to = p.dx + r * p.ld_dx;
-        if constexpr (!VEC) Tm::sync();
+        if constexpr (LAYOUT == kStaged) Tm::sync();
 #pragma unroll
         for (int k = 0; k < PACKS; ++k) {
-            const int c = column<WARPS>(k);
+            const int c = column<WARPS>(k, shift);
             float w[8], d[8];
             if (p.weight) load_weight(p.weight, c, cols, p.weight16, w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float h = x0[k].get(e) * inv, gw = p.weight ? g0[k].get(e) * w[e] : g0[k].get(e);
-                dw[k][e] = fmaf(g0[k].get(e), h, dw[k][e]);
+                if constexpr (LAYOUT == kShifted) dw[k][e] = g0[k].get(e) * h;
+                else dw[k][e] = fmaf(g0[k].get(e), h, dw[k][e]);
                 d[e] = inv * (gw - h * mean);
                 if (p.gs) d[e] += gs0[k].get(e);
             }
-            store_pack<T, VEC>(to, line, c, cols, d);
+            store_pack<T, LAYOUT>(to, line, c, cols, d);
+            if (LAYOUT == kShifted && p.parts) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (c + e >= 0 && c + e < cols) columns[c + e] += dw[k][e];
+            }
         }
-        if constexpr (!VEC) store_line<T, WARPS>(to, line, cols);
+        // The next row's sums are behind a barrier of the team's (in sum()).
+        if constexpr (LAYOUT == kStaged) store_line<T, WARPS>(to, line, cols);
+        if (LAYOUT == kShifted && WARPS == 1) __syncwarp();
     }
     if (!p.parts) return;
     float *const to = p.parts + (int64_t)blockIdx.x * cols;
@@ -302,22 +343,27 @@ rms_norm_backward_kernel(const __grid_constant__ NormBackwardParams<T> p)
         // The eight rows' warps, in order.
         float *const all = reinterpret_cast<float *>(staging);
         __syncthreads();
+        if constexpr (LAYOUT != kShifted) {
 #pragma unroll
-        for (int k = 0; k < PACKS; ++k) {
-            const int c = column<WARPS>(k);
-            if (c < cols) store8(all + Tm::row() * padded + c, dw[k]);
+            for (int k = 0; k < PACKS; ++k) {
+                const int c = column<WARPS>(k, 0);
+                if (c < cols) store8(all + Tm::row() * padded + c, dw[k]);
+            }
+            __syncthreads();
         }
-        __syncthreads();
         for (int c = threadIdx.x; c < cols; c += Tm::THREADS) {
             float s = 0.0f;
 #pragma unroll
             for (int i = 0; i < Tm::ROWS; ++i) s += all[i * padded + c];
             to[c] = s;
         }
+    } else if constexpr (LAYOUT == kShifted) {
+        __syncthreads();
+        for (int c = threadIdx.x; c < cols; c += Tm::THREADS) to[c] = columns[c];
     } else {
 #pragma unroll
         for (int k = 0; k < PACKS; ++k) {
-            const int c = column<WARPS>(k);
+            const int c = column<WARPS>(k, 0);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 if (c + e < cols) to[c + e] = dw[k][e];
@@ -344,9 +390,26 @@ __global__ void __launch_bounds__(1024) add_parts_kernel(const float *parts, int
     }
 }
 
-bool pieces16(const void *p, int64_t ld, int64_t per16)
+struct Rows {
+    const void *p;
+    int64_t ld;
+};
+
+// How the rows of these matrices (null: none) can be accessed together.
+template <class T, int N>
+Layout layout_of(const Rows (&all)[N], bool shiftable)
 {
-    return !p || ((reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % per16 == 0);
+    constexpr uint64_t per16 = 16 / sizeof(T);
+    uint64_t phase = 0, ld = 0;
+    bool first = true, alike = true;
+    for (const Rows &m : all) {
+        if (!m.p) continue;
+        const uint64_t at = reinterpret_cast<uintptr_t>(m.p) / sizeof(T) % per16, step = (uint64_t)m.ld % per16;
+        if (first) phase = at, ld = step;
+        alike = alike && at == phase && step == ld;
+        first = false;
+    }
+    return !alike ? kStaged : phase == 0 && ld == 0 ? kWhole : shiftable ? kShifted : kStaged;
 }
 
 // Calls f(Warps, Packs) with the shape of `cols` columns.
@@ -382,7 +445,6 @@ cudaError_t launch(K kernel, unsigned grid, int threads, int bytes, const void *
 template <class T>
 cudaError_t norm_of(const RmsNormArgs &g, cudaStream_t stream)
 {
-    constexpr int64_t per16 = 16 / (int64_t)sizeof(T);
     NormParams<T> p{};
     p.rows = g.rows, p.cols = (int)g.cols;
     p.x = static_cast<const T *>(g.x), p.ldx = g.ldx;
@@ -392,13 +454,14 @@ cudaError_t norm_of(const RmsNormArgs &g, cudaStream_t stream)
     p.sum = static_cast<T *>(g.sum), p.ld_sum = g.ld_sum;
     p.y = static_cast<T *>(g.y), p.ldy = g.ldy;
     p.q = g.q, p.ldq = g.ldq, p.scales = g.scales, p.lds = g.lds;
-    const bool vec = pieces16(g.x, g.ldx, per16) && pieces16(g.residual, g.ld_res, per16) &&
-                     pieces16(g.sum, g.ld_sum, per16) && pieces16(g.y, g.ldy, per16);
-    return with_shape(g.cols, [&](auto w, auto k) {
+    const Rows all[] = {{g.x, g.ldx}, {g.residual, g.ld_res}, {g.sum, g.ld_sum}, {g.y, g.ldy}};
+    const Layout layout = layout_of<T>(all, !g.q && g.cols + 7 <= kMaxNormCols);
+    return with_shape(layout == kShifted ? g.cols + 7 : g.cols, [&](auto w, auto k) {
         constexpr int W = decltype(w)::value, P = decltype(k)::value;
         const unsigned grid = (unsigned)((g.rows + Team<W>::ROWS - 1) / Team<W>::ROWS);
-        if (vec) return launch(rms_norm_kernel<T, W, P, true>, grid, Team<W>::THREADS, 0, &p, stream);
-        return launch(rms_norm_kernel<T, W, P, false>, grid, Team<W>::THREADS, staging_bytes(g.cols, Team<W>::ROWS), &p,
+        if (layout == kWhole) return launch(rms_norm_kernel<T, W, P, kWhole>, grid, Team<W>::THREADS, 0, &p, stream);
+        if (layout == kShifted) return launch(rms_norm_kernel<T, W, P, kShifted>, grid, Team<W>::THREADS, 0, &p, stream);
+        return launch(rms_norm_kernel<T, W, P, kStaged>, grid, Team<W>::THREADS, staging_bytes(g.cols, Team<W>::ROWS), &p,
                       stream);
     });
 }
@@ -413,9 +476,22 @@ unsigned backward_blocks(const RmsNormBackwardArgs &g)
 }
 
 template <class T>
+Layout backward_layout(const RmsNormBackwardArgs &g)
+{
+    const Rows all[] = {{g.grad_y, g.ld_gy}, {g.x, g.ldx}, {g.grad_sum, g.ld_gs}, {g.grad_x, g.ld_gx}};
+    return layout_of<T>(all, g.cols + 7 <= kMaxNormCols);
+}
+
+// The columns that a row's eights reach over.
+template <class T>
+int64_t backward_cols(const RmsNormBackwardArgs &g)
+{
+    return backward_layout<T>(g) == kShifted ? g.cols + 7 : g.cols;
+}
+
+template <class T>
 cudaError_t norm_backward_of(const RmsNormBackwardArgs &g, void *scratch, cudaStream_t stream)
 {
-    constexpr int64_t per16 = 16 / (int64_t)sizeof(T);
     NormBackwardParams<T> p{};
     p.rows = g.rows, p.cols = (int)g.cols;
     p.g = static_cast<const T *>(g.grad_y), p.ld_g = g.ld_gy;
@@ -425,16 +501,19 @@ cudaError_t norm_backward_of(const RmsNormBackwardArgs &g, void *scratch, cudaSt
     p.weight16 = (reinterpret_cast<uintptr_t>(g.weight) & 15u) == 0;
     p.dx = static_cast<T *>(g.grad_x), p.ld_dx = g.ld_gx;
     p.parts = g.grad_weight ? static_cast<float *>(scratch) : nullptr;
-    const bool vec = pieces16(g.grad_y, g.ld_gy, per16) && pieces16(g.x, g.ldx, per16) &&
-                     pieces16(g.grad_sum, g.ld_gs, per16) && pieces16(g.grad_x, g.ld_gx, per16);
-    return with_shape(g.cols, [&](auto w, auto k) {
+    const Layout layout = backward_layout<T>(g);
+    return with_shape(backward_cols<T>(g), [&](auto w, auto k) {
         constexpr int W = decltype(w)::value, P = decltype(k)::value;
         const unsigned grid = backward_blocks<W>(g);
-        // Warps add their weight gradients up in shared memory.
-        const int bytes = !vec || (W == 1 && p.parts) ? staging_bytes(g.cols, Team<W>::ROWS) : 0;
-        cudaError_t e = grid == 0 ? cudaSuccess
-                        : vec ? launch(rms_norm_backward_kernel<T, W, P, true>, grid, Team<W>::THREADS, bytes, &p, stream)
-                            : launch(rms_norm_backward_kernel<T, W, P, false>, grid, Team<W>::THREADS, bytes, &p, stream);
+        // Warps add their weight gradients up in shared memory, shifted rows theirs.
+        const bool adds = p.parts && (W == 1 || layout == kShifted);
+        const int bytes = layout == kStaged || adds ? staging_bytes(g.cols, Team<W>::ROWS) : 0;
+        cudaError_t e = cudaSuccess;
+        if (grid > 0)
+            e = layout == kWhole ? launch(rms_norm_backward_kernel<T, W, P, kWhole>, grid, Team<W>::THREADS, bytes, &p, stream)
+                : layout == kShifted
+                    ? launch(rms_norm_backward_kernel<T, W, P, kShifted>, grid, Team<W>::THREADS, bytes, &p, stream)
+                    : launch(rms_norm_backward_kernel<T, W, P, kStaged>, grid, Team<W>::THREADS, bytes, &p, stream);
         if (e != cudaSuccess || !g.grad_weight) return e;
         add_parts_kernel<<<(unsigned)((g.cols + 31) / 32), 1024, 0, stream>>>(p.parts, (int)grid, (int)g.cols, g.grad_weight);
         return cudaGetLastError();
@@ -452,7 +531,7 @@ size_t rms_norm_backward_scratch_bytes(const RmsNormBackwardArgs &g)
 {
     if (!g.grad_weight) return 0;
     size_t bytes = 0;
-    with_shape(g.cols, [&](auto w, auto) {
+    with_shape(g.bf16 ? backward_cols<__nv_bfloat16>(g) : backward_cols<float>(g), [&](auto w, auto) {
         bytes = (size_t)backward_blocks<decltype(w)::value>(g) * (size_t)g.cols * 4;
         return cudaSuccess;
     });

@@ -151,13 +151,13 @@ struct Raw8 {
 #pragma unroll
         for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = make_uint4(0, 0, 0, 0);
     }
-    // The first n of them.
-    __device__ __forceinline__ void load_some(const T *p, int n)
+    // Those from lo on, below hi; the others are zeros.
+    __device__ __forceinline__ void load_some(const T *p, int lo, int hi)
     {
         uint32_t w[2 * sizeof(T)] = {};
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            if (e >= n) continue;
+            if (e < lo || e >= hi) continue;
             if constexpr (sizeof(T) == 4) w[e] = __float_as_uint(p[e]);
             else w[e / 2] |= (uint32_t) * reinterpret_cast<const uint16_t *>(p + e) << (16 * (e & 1));
         }
