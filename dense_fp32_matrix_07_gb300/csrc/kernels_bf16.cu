@@ -68,7 +68,7 @@ struct Bf16Cfg {
     static constexpr int P_TILE = 128 * 128;
     static constexpr int Q_TILE = (QR < 64 ? 64 : QR) * 128;       // a box of 64 x 64 at least
     static constexpr int STAGE_BYTES = P_TILE + Q_TILE;
-    static constexpr int STAGES = PAIR ? (BN == 256 ? 5 : 7) - (JOINS ? BN == 256 ? 1 : 2 : 0) : BN == 128 ? 4 : BN == 64 ? 7 : 8;
+    static constexpr int STAGES = PAIR ? (BN == 256 ? 6 : 8) - (JOINS ? BN == 256 ? 2 : 3 : 0) : BN == 128 ? 5 : BN == 64 ? 8 : 8;
     static constexpr int NBUF = 2;
     static constexpr int TMEM_COLS = NBUF * BN < 32 ? 32 : NBUF * BN;
     static constexpr int EPI_WARPS = BN >= 128 ? 8 : 4;
@@ -104,9 +104,10 @@ struct Bf16Params {
     int groups;
     const int32_t *offsets;
     int tm, tn;                  // rows and columns of C per tile
-    int row_tiles, col_tiles;    // (grouped rows: row tiles from the table)
-    FastDiv by_cols, by_group;   // col_tiles; tiles of one group (GroupK)
+    int row_tiles, col_tiles;    // (grouped rows: row tiles by group)
+    FastDiv by_cols;             // col_tiles
     int split;
+    int even;                    // GroupK: extra tiles go to the CTAs with the least work so far
     const float *bias;
     int64_t stride_bias;
     int act, join;
@@ -127,7 +128,7 @@ struct Bf16Params {
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(kAll, x, 0); }
 
 // One tile: its group, rows [m, m_end) and first column of C, its range of K,
-// and the accumulator's columns that it needs.
+// and the accumulator's columns that it needs (0: no tile, all are done).
 struct Item {
     int group, m, m_end, n, k0, k1, cols;
 };
@@ -180,53 +181,47 @@ struct Walk {
     }
 };
 
-template <class Cfg>
-__device__ __forceinline__ Item find_item(const Bf16Params &p, const int *table, const Walk &walk, uint32_t t, int rank)
+// Row tile and column tile t of `rows` by col_tiles: bands of kRaster row
+// tiles, the row tile fastest.
+__device__ __forceinline__ int2 raster(const Bf16Params &p, int rows, uint32_t t)
 {
-    Item it;
-    it.group = 0;
-    int piece = 0;
-    if (Cfg::PAIR && t >= walk.whole) {
-        const uint32_t over = t - walk.whole, shift = walk.pieces >> 1;   // of 1, 2 or 4
-        piece = (int)(over & (walk.pieces - 1));
-        t = walk.whole + (over >> shift);
-    }
-    int rows = p.row_tiles;
-    if (p.mode == kBf16GroupRows) rows = table[p.groups];
-    if (p.mode == kBf16GroupK) {
-        it.group = (int)div(t, p.by_group);
-        t -= it.group * p.by_group.d;
-    }
-    // Bands of kRaster row tiles, the row tile fastest.
     const uint32_t band = div(t / kRaster, p.by_cols), first = band * kRaster;
     const uint32_t r = t - first * p.col_tiles;
     const uint32_t high = rows - first < (uint32_t)kRaster ? rows - first : kRaster;
     const uint32_t ct = high == kRaster ? r / kRaster : r / high;
-    const int rt = (int)(first + r - ct * high);
-    it.n = (int)ct * p.tn;
+    return make_int2((int)(first + r - ct * high), (int)ct);
+}
+
+// The CTA's part of K, where a cluster shares a tile.
+__device__ __forceinline__ void split_range(const Bf16Params &p, int rank, Item &it)
+{
+    if (p.split == 1) return;
+    const int n = slabs(0, p.K);
+    const int64_t k1 = (int64_t)((int64_t)n * (rank + 1) / p.split) * kSlab;
+    it.k0 = (int)((int64_t)n * rank / p.split) * kSlab;
+    it.k1 = k1 < p.K ? (int)k1 : p.K;
+}
+
+template <class Cfg>
+__device__ __forceinline__ Item dense_item(const Bf16Params &p, const Walk &walk, uint32_t t, int rank)
+{
+    int piece = 0;
+    const bool cut = Cfg::PAIR && t >= walk.whole && walk.pieces > 1;
+    if (cut) {
+        const uint32_t over = t - walk.whole, shift = walk.pieces >> 1;   // of 2 or 4
+        piece = (int)(over & (walk.pieces - 1));
+        t = walk.whole + (over >> shift);
+    }
+    const int2 at = raster(p, p.row_tiles, t);
+    Item it;
+    it.group = 0;
+    it.m = at.x * p.tm;
+    it.m_end = p.M - it.m < p.tm ? p.M : it.m + p.tm;
+    it.n = at.y * p.tn;
     it.k0 = 0;
     it.k1 = p.K;
-    if (p.mode == kBf16GroupRows) {
-        it.group = find_group(table, p.groups, rt);
-        int lo, hi;
-        group_range(p.offsets, it.group, p.M, lo, hi);
-        int tall = p.tm;
-        if (p.swap) {
-            // The group's rows evenly over its tiles: of 273, 160 and 113
-            // columns take less than 256 and 17.
-            const int tiles = (int)(((uint32_t)(hi - lo) + p.tm - 1) / (uint32_t)p.tm);
-            tall = whole_columns<Cfg>(tiles > 1 ? (hi - lo + tiles - 1) / tiles : hi - lo);
-        }
-        it.m = lo + (rt - table[it.group]) * tall;
-        it.m = it.m < hi ? it.m : hi;
-        it.m_end = hi - it.m < tall ? hi : it.m + tall;
-    } else {
-        it.m = rt * p.tm;
-        it.m_end = p.M - it.m < p.tm ? p.M : it.m + p.tm;
-        if (p.mode == kBf16GroupK) group_range(p.offsets, it.group, p.K, it.k0, it.k1);
-    }
     it.cols = whole_columns<Cfg>(p.swap ? it.m_end - it.m : p.N - it.n);
-    if (Cfg::PAIR && t >= walk.whole && walk.pieces > 1) {
+    if (cut) {
         const int wide = whole_columns<Cfg>((it.cols + (int)walk.pieces - 1) / (int)walk.pieces);
         it.cols = wide;
         if (p.swap) {
@@ -239,14 +234,119 @@ __device__ __forceinline__ Item find_item(const Bf16Params &p, const int *table,
             if (it.n >= end) it.m_end = it.m;
         }
     }
-    if (p.split > 1) {
-        const int n = slabs(0, p.K);
-        const int64_t k1 = (int64_t)((int64_t)n * (rank + 1) / p.split) * kSlab;
-        it.k0 = (int)((int64_t)n * rank / p.split) * kSlab;
-        it.k1 = k1 < p.K ? (int)k1 : p.K;
-    }
+    split_range(p, rank, it);
     return it;
 }
+
+// A group's rows of C, and how many of them a tile takes.
+struct Group {
+    int lo, hi, tiles, tall;
+};
+
+template <class Cfg>
+__device__ __forceinline__ Group group_of(const Bf16Params &p, int g)
+{
+    Group o;
+    group_range(p.offsets, g, p.M, o.lo, o.hi);
+    o.tiles = (int)(((uint32_t)(o.hi - o.lo) + (uint32_t)p.tm - 1) / (uint32_t)p.tm);
+    // The columns' rows evenly over the tiles: of 273, 160 and 113 take less
+    // than 256 and 17.
+    const int each = o.tiles > 1 ? (o.hi - o.lo + o.tiles - 1) / o.tiles : o.hi - o.lo;
+    o.tall = p.swap ? whole_columns<Cfg>(each) : p.tm;
+    return o;
+}
+
+// Tile t of the groups' rows: table[g] row tiles are in the groups before g.
+template <class Cfg>
+__device__ __forceinline__ Item rows_item(const Bf16Params &p, const int *table, uint32_t t, int rank)
+{
+    const int2 at = raster(p, table[p.groups], t);
+    Item it;
+    it.group = find_group(table, p.groups, at.x);
+    const Group o = group_of<Cfg>(p, it.group);
+    it.m = o.lo + (at.x - table[it.group]) * o.tall;
+    it.m = it.m < o.hi ? it.m : o.hi;
+    it.m_end = o.hi - it.m < o.tall ? o.hi : it.m + o.tall;
+    it.n = at.y * p.tn;
+    it.k0 = 0;
+    it.k1 = p.K;
+    it.cols = whole_columns<Cfg>(p.swap ? it.m_end - it.m : p.N - it.n);
+    split_range(p, rank, it);
+    return it;
+}
+
+// Tile t of group g's product over its rows.
+template <class Cfg>
+__device__ __forceinline__ Item k_item(const Bf16Params &p, int g, uint32_t t)
+{
+    const int2 at = raster(p, p.row_tiles, t);
+    Item it;
+    it.group = g;
+    it.m = at.x * p.tm;
+    it.m_end = p.M - it.m < p.tm ? p.M : it.m + p.tm;
+    it.n = at.y * p.tn;
+    group_range(p.offsets, g, p.K, it.k0, it.k1);
+    it.cols = whole_columns<Cfg>(p.swap ? it.m_end - it.m : p.N - it.n);
+    return it;
+}
+
+// What the CTAs (pairs) have been given, for groups of uneven length: the
+// tiles of a group that are left over after each has had the same number go to
+// those that have the least so far. (Every units-th tile instead leaves 16
+// groups' weight gradients of 2048 x 2048 from 16383 rows at 119 us for 93
+// with even groups; shares of neighbouring tiles, even in their work, at 158:
+// CTAs that are at different groups share no operands in L2.) A warp's lanes
+// hold the work of walkers lane, lane + 32, ..; all warps find the same.
+constexpr int kWalkers = 5;    // per lane: up to 160
+
+struct Shares {
+    uint32_t work[kWalkers] = {};
+
+    // Gives a group's tiles, `cost` each: `rounds` to all of the `units`
+    // walkers and `extra` (below units) to those with the least work, by their
+    // numbers where that is equal. Which of the extra ones walker `unit` gets
+    // (`extra`: none).
+    __device__ __forceinline__ uint32_t give(uint32_t units, uint32_t unit, uint32_t rounds, uint32_t extra, uint32_t cost, int lane)
+    {
+        // The least limit that `extra` walkers are within, by bisection.
+        uint32_t low = ~0u, high = 0;
+#pragma unroll
+        for (int i = 0; i < kWalkers; ++i) {
+            if ((uint32_t)(lane + 32 * i) >= units) continue;
+            low = work[i] < low ? work[i] : low;
+            high = work[i] > high ? work[i] : high;
+        }
+        low = __reduce_min_sync(kAll, low);
+        high = __reduce_max_sync(kAll, high);
+        while (low < high) {
+            const uint32_t mid = low + (high - low) / 2;
+            uint32_t within = 0;
+#pragma unroll
+            for (int i = 0; i < kWalkers; ++i)
+                within += __popc(__ballot_sync(kAll, (uint32_t)(lane + 32 * i) < units && work[i] <= mid));
+            if (within >= extra) high = mid;
+            else low = mid + 1;
+        }
+        uint32_t left = extra;          // for those at the limit
+#pragma unroll
+        for (int i = 0; i < kWalkers; ++i)
+            left -= __popc(__ballot_sync(kAll, (uint32_t)(lane + 32 * i) < units && work[i] < low));
+        const uint32_t below = (1u << lane) - 1;
+        uint32_t mine = extra, given = 0, at_limit = 0;
+#pragma unroll
+        for (int i = 0; i < kWalkers; ++i) {
+            const bool there = (uint32_t)(lane + 32 * i) < units, equal = there && work[i] == low;
+            const uint32_t equals = __ballot_sync(kAll, equal);
+            const bool gets = there && (work[i] < low || (equal && at_limit + __popc(equals & below) < left));
+            at_limit += __popc(equals);
+            const uint32_t all = __ballot_sync(kAll, gets);
+            if (unit / 32 == (uint32_t)i && ((all >> (unit % 32)) & 1)) mine = given + __popc(all & ((1u << (unit % 32)) - 1));
+            given += __popc(all);
+            work[i] += (rounds + (gets ? 1u : 0u)) * cost;
+        }
+        return mine;
+    }
+};
 
 // The address of `addr` in the shared memory of the cluster's CTA `rank`.
 __device__ __forceinline__ uint32_t map_shared(uint32_t addr, uint32_t rank)
@@ -281,6 +381,15 @@ __device__ __forceinline__ void mbar_arrive_cluster_if(uint32_t on, uint32_t bar
     asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
                  "@q mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar),
                  "r"(on)
+                 : "memory");
+}
+
+// Takes over what came before the arrivals, from the pair's other CTA too, at
+// a phase that is known to be complete. (A fence instead costs 1000 cycles.)
+__device__ __forceinline__ void mbar_seen_cluster(uint32_t bar, uint32_t parity)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}" ::"r"(bar),
+                 "r"(parity)
                  : "memory");
 }
 
@@ -707,11 +816,7 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
     if (warp == 1) tmem_alloc<PAIR>(tmem_slot, Cfg::TMEM_COLS);
     if (p.mode == kBf16GroupRows) {
         // table[g] = row tiles of the groups before g.
-        for (int g = threadIdx.x; g < p.groups; g += Cfg::THREADS) {
-            int lo, hi;
-            group_range(p.offsets, g, p.M, lo, hi);
-            table[g] = (int)(((uint32_t)(hi - lo) + (uint32_t)p.tm - 1) / (uint32_t)p.tm);
-        }
+        for (int g = threadIdx.x; g < p.groups; g += Cfg::THREADS) table[g] = group_of<Cfg>(p, g).tiles;
         __syncthreads();
         if (warp == 0) {
             // Offsets that are not a partition may sum to anything: no entry
@@ -746,13 +851,7 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
     if (Cfg::CAN_SPLIT && split > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     const uint32_t taddr = *reinterpret_cast<uint32_t *>(smem + (tmem_slot - base));
 
-    const uint32_t t_first = blockIdx.x / cluster, t_step = gridDim.x / cluster;
-    uint32_t tiles = (uint32_t)p.col_tiles * (uint32_t)(p.mode == kBf16Dense       ? p.row_tiles
-                                                        : p.mode == kBf16GroupRows ? table[p.groups]
-                                                                                   : p.row_tiles * p.groups);
-    if (split > 1 && tiles > t_step) tiles = t_step;   // a split grid has one tile per cluster
-    const Walk walk(tiles, t_step, PAIR);
-    if (PAIR) tiles = walk.steps;
+    const uint32_t unit = blockIdx.x / cluster, units = gridDim.x / cluster;
 
     // The CTA's nth tile, once warp 2 has found it; not to be read after done_with().
     const int longest = slabs(0, p.K);
@@ -793,13 +892,14 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
         };
         uint32_t it = 0, n = 0, early = 1;
         bool ok = true;
-        for (uint32_t t = t_first; ok && t < tiles; t += t_step, ++n) {
+        for (; ok; ++n) {
             if (!item_there(n)) {
                 gave_up();
                 break;
             }
             const Item w = load_item(item_at(n));
             done_with(n);
+            if (w.cols == 0) break;
             const int z = p.mode == kBf16GroupRows ? w.group : 0;
             const int pz = p.swap ? z : 0, qz = p.swap ? 0 : z;
             const int need = PAIR ? w.cols / 2 : w.cols;     // rows of the columns' operand here
@@ -812,8 +912,8 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
                     ok = false;
                     break;
                 }
-                // A group's last rows go to warp 3 first.
-                const bool tail = group_k && w.k1 - k < kSlab;
+                // A group's last rows go to warp 3 first, unless they are whole 16s.
+                const bool tail = group_k && w.k1 - k < kSlab && (w.k1 - k) % 16 != 0;
                 uint32_t bar = tail ? tail_bar(s) : full_bar(s);
                 if constexpr (PAIR) {
                     bar = map_shared(bar, tail ? rank : 0);
@@ -848,13 +948,14 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
         const uint32_t on = elect_one();
         uint32_t it = 0, n = 0, acc = 0, early = 0;
         bool ok = true;
-        for (uint32_t t = t_first; ok && t < tiles; t += t_step, ++n) {
+        for (; ok; ++n) {
             if (!item_there(n)) {
                 gave_up();
                 break;
             }
             const Item w = load_item(item_at(n));
             done_with(n);
+            if (w.cols == 0) break;
             if (!leader) continue;
             const uint32_t idesc = idesc_bf16(Cfg::LANES, w.cols, p.p_mn, p.q_mn);
             int k = w.k0;
@@ -875,7 +976,7 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
                         break;
                     }
                     // What warp 3 of the other CTA zeroed there is seen here too.
-                    if (PAIR && group_k && w.k1 - k < kSlab) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                    if (PAIR && group_k && w.k1 - k < kSlab) mbar_seen_cluster(full_bar(s), (it / STAGES) & 1);
                     ptx::tc_fence_after();
                     const uint32_t off = (uint32_t)(s * (Cfg::STAGE_BYTES / 16));
 #pragma unroll
@@ -906,32 +1007,66 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
     } else if (warp == 2) {
         // ------------------------------ tiles ------------------------------
         uint32_t n = 0;
-        for (uint32_t t = t_first; t < tiles; t += t_step, ++n) {
-            const Item w = find_item<Cfg>(p, table, walk, t, split > 1 ? rank : 0);
-            // The place is free when the tile kItems before is stored.
+        // The place is free when the tile kItems before is stored.
+        auto give = [&](const Item &w) {
             if (!wait_tile(iempty_bar(n % kItems), ((n / kItems) & 1) ^ 1, longest)) {
                 gave_up();
-                break;
+                return false;
             }
             if (lane == 0) store_item(item_at(n), w);
             __syncwarp();
             mbar_arrive_if(lane == 0, ifull_bar(n % kItems));
+            ++n;
+            return true;
+        };
+        bool ok = true;
+        if (p.mode == kBf16Dense) {
+            const Walk walk((uint32_t)p.col_tiles * (uint32_t)p.row_tiles, units, PAIR);
+            for (uint32_t t = unit; ok && t < walk.steps; t += units) ok = give(dense_item<Cfg>(p, walk, t, rank));
+        } else if (p.mode == kBf16GroupRows) {
+            const uint32_t tiles = (uint32_t)p.col_tiles * (uint32_t)table[p.groups];
+            for (uint32_t t = unit; ok && t < tiles; t += units) {
+                ok = give(rows_item<Cfg>(p, table, t, rank));
+                if (split > 1) break;      // one tile per cluster
+            }
+        } else if (p.even) {
+            const uint32_t tiles = (uint32_t)p.col_tiles * (uint32_t)p.row_tiles, rounds = tiles / units;
+            Shares shares;
+            for (int g = 0; ok && g < p.groups; ++g) {
+                for (uint32_t i = 0; ok && i < rounds; ++i) ok = give(k_item<Cfg>(p, g, i * units + unit));
+                int lo, hi;
+                group_range(p.offsets, g, p.K, lo, hi);
+                // A tile's work: its slabs, and what it takes besides.
+                const uint32_t extra = tiles - rounds * units;
+                const uint32_t place = shares.give(units, unit, rounds, extra, (uint32_t)slabs(lo, hi) + 4, lane);
+                if (ok && place < extra) ok = give(k_item<Cfg>(p, g, rounds * units + place));
+            }
+        } else {
+            const uint32_t tiles = (uint32_t)p.col_tiles * (uint32_t)p.row_tiles;
+            int g = 0;
+            for (uint32_t t = unit; ok; t += units) {
+                for (; g < p.groups && t >= tiles; ++g) t -= tiles;
+                if (g >= p.groups) break;
+                ok = give(k_item<Cfg>(p, g, t));
+            }
         }
+        if (ok) give(Item{});
     } else if (warp == 3) {
         // --------------------- the ends of groups along K ---------------------
         // Both operands have K along the rows of their boxes here.
         // A stage's next such slab comes after this one's MMAs: one phase each.
         uint32_t it = 0, n = 0, phases = 0;
-        for (uint32_t t = t_first; group_k && t < tiles; t += t_step, ++n) {
+        for (; group_k; ++n) {
             if (!item_there(n)) {
                 gave_up();
                 break;
             }
             const Item w = load_item(item_at(n));
             done_with(n);
+            if (w.cols == 0) break;
             const int nk = slabs(w.k0, w.k1), valid = (w.k1 - w.k0) % kSlab;
             it += nk;
-            if (valid == 0) continue;
+            if (valid % 16 == 0) continue;
             const int s = (int)((it - 1) % STAGES);
             if (!wait_tile(tail_bar(s), (phases >> s) & 1, longest)) {
                 gave_up();
@@ -940,10 +1075,11 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
             phases ^= 1u << s;
             const int end = (valid + 15) / 16 * 16;
             constexpr int boxes = 2 + (QR + 63) / 64;
-            const int pieces = (end - valid) * 8;   // 16 bytes each, per box
-            for (int i = lane; i < boxes * pieces; i += 32) {
-                const int box = i / pieces, at = i - box * pieces;
-                st_shared_u32x4(stage_p(s) + 8192 * box + 128 * valid + 16 * at, make_uint4(0, 0, 0, 0));
+            // Four rows of 128 bytes at a time.
+            for (int r = valid + lane / 8; r < end; r += 4) {
+#pragma unroll
+                for (int box = 0; box < boxes; ++box)
+                    st_shared_u32x4(stage_p(s) + 8192 * box + 128 * r + 16 * (lane % 8), make_uint4(0, 0, 0, 0));
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
@@ -978,12 +1114,13 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
             else mbar_arrive_if(lane == 0, acce_bar(b));
             ++acc;
         };
-        for (uint32_t t = t_first; t < tiles; t += t_step, ++n) {
+        for (;; ++n) {
             if (!item_there(n)) {
                 gave_up();
                 break;
             }
             const Item w = load_item(item_at(n));
+            if (w.cols == 0) break;
             if constexpr (Cfg::JOINS) {
                 d.next = 0;
                 d.ask(p, &mapD, w, lane, lane0, col0);
@@ -1064,8 +1201,14 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
             // in rank order (of lanes that hold columns of C: a split tile is
             // swapped). Nothing reaches into another CTA after this barrier.
             ptx::cluster_sync_all();
-            if (t_first < tiles) {
-                const Item w = find_item<Cfg>(p, table, walk, t_first, rank);
+            Item w{};
+            if (p.mode == kBf16Dense) {
+                const Walk walk((uint32_t)p.col_tiles * (uint32_t)p.row_tiles, units, false);
+                if (unit < walk.steps) w = dense_item<Cfg>(p, walk, unit, rank);
+            } else if (unit < (uint32_t)p.col_tiles * (uint32_t)table[p.groups]) {
+                w = rows_item<Cfg>(p, table, unit, rank);
+            }
+            if (w.cols > 0) {
                 const uint32_t part = base + Cfg::OFF_EXTRA;
                 const int per = BN / split;
                 auto add = [&](auto q) {
@@ -1230,7 +1373,11 @@ cudaError_t launch_cfg(const Bf16Args &g, const Bf16Plan &plan, cudaStream_t str
                                                     : (int64_t)p.row_tiles * g.groups;
     if (rows + 2 * kRaster > INT32_MAX / p.col_tiles - 2 * kRaster) return cudaErrorInvalidValue;
     p.by_cols = fast_div((uint32_t)p.col_tiles);
-    p.by_group = fast_div((uint32_t)((int64_t)p.row_tiles * p.col_tiles));
+    // Worth it where a group's tiles are about a wave of CTAs: with many more
+    // the rest matters little, with few (and many groups) the finding does.
+    const int64_t units = plan.grid / (Cfg::PAIR ? 2 : 1), each = (int64_t)p.row_tiles * p.col_tiles;
+    p.even = g.mode == kBf16GroupK && g.groups > 1 && g.groups <= 128 && units <= 32 * kWalkers && 4 * each >= units &&
+             each <= 16 * units && each % units != 0;
     p.split = plan.split;
     p.bias = g.bias;
     p.stride_bias = g.stride_bias;
