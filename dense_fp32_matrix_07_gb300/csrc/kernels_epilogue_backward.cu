@@ -8,6 +8,7 @@
 // scratch, and a second launch adds each group's in order (no atomics: the
 // result does not depend on timing). db sums the unrounded dz, in FP32.
 #include "layers.cuh"
+#include "ptx.cuh"
 
 namespace sgemm_gb300 {
 
@@ -21,7 +22,6 @@ struct Params {
     int64_t rows, cols;
     const T *g, *z, *D;
     int64_t ld_g, ld_z, ldd;
-    int join;
     int groups;
     const int32_t *offsets;
     T *dz, *dD;
@@ -43,18 +43,19 @@ __device__ __forceinline__ void group_rows(const int32_t *offsets, int groups, i
 }
 
 // table[g] = units of the groups before g, held to `units` (offsets that are
-// not a partition may sum to anything). By one block of 256 threads.
+// not a partition may sum to anything). By one block of 256 threads or more.
 __device__ void fill_table(int *table, const int32_t *offsets, int groups, int64_t rows, int units)
 {
     __shared__ int sums[256];
-    const int per = (groups + 255) / 256, first = threadIdx.x * per;
+    const bool mine_too = threadIdx.x < 256;
+    const int per = (groups + 255) / 256, first = mine_too ? threadIdx.x * per : groups;
     int64_t mine = 0;
     for (int g = first; g < first + per && g < groups; ++g) {
         int64_t lo, hi;
         group_rows(offsets, groups, rows, g, lo, hi);
         mine += (hi - lo + kRows - 1) / kRows;
     }
-    sums[threadIdx.x] = (int)(mine < units ? mine : units);
+    if (mine_too) sums[threadIdx.x] = (int)(mine < units ? mine : units);
     __syncthreads();
     if (threadIdx.x == 0) {
         int64_t at = 0;
@@ -66,7 +67,7 @@ __device__ void fill_table(int *table, const int32_t *offsets, int groups, int64
         table[groups] = (int)at;
     }
     __syncthreads();
-    int64_t at = sums[threadIdx.x];
+    int64_t at = mine_too ? sums[threadIdx.x] : 0;
     for (int g = first; g < first + per && g < groups; ++g) {
         int64_t lo, hi;
         group_rows(offsets, groups, rows, g, lo, hi);
@@ -133,17 +134,16 @@ __device__ __forceinline__ void put8(T *row, int lane, int cols, const float (&v
 }
 
 // A warp's rows r, r + 8, .. below hi of a unit's columns from c0 on, and their sums.
-template <class T, bool VEC, int ACT>
+template <class T, bool VEC, int ACT, bool MUL>
 __device__ __forceinline__ void run_rows(const Params<T> &p, int64_t r, int64_t hi, int64_t c0, int cols, int lane,
                                          float (&sum)[8])
 {
     if (VEC && 8 * lane >= cols) return;
     // Rows requested together: of one at a time, most of the time is a wait
     // for memory (8191 x 4096 bfloat16, gelu: 89 us).
-    constexpr int BATCH = sizeof(T) == 2 ? 4 : 2;
-    const bool mul = p.join == kJoinMul;
+    constexpr int BATCH = VEC && sizeof(T) == 2 ? 4 : 2;
     const T *g_at = p.g + r * p.ld_g + c0, *z_at = p.z ? p.z + r * p.ld_z + c0 : nullptr,
-            *d_at = mul ? p.D + r * p.ldd + c0 : nullptr;
+            *d_at = MUL ? p.D + r * p.ldd + c0 : nullptr;
     T *dz_at = p.dz ? p.dz + r * p.ld_dz + c0 : nullptr, *dD_at = p.dD ? p.dD + r * p.ld_dD + c0 : nullptr;
 #pragma unroll 1
     for (; r < hi; r += 8 * BATCH) {
@@ -154,7 +154,7 @@ __device__ __forceinline__ void run_rows(const Params<T> &p, int64_t r, int64_t 
             load8<T, VEC>(g_at + 8 * i * p.ld_g, lane, cols, g[i]);
             if (z_at) load8<T, VEC>(z_at + 8 * i * p.ld_z, lane, cols, z[i]);
             else z[i].zero();
-            if (mul) load8<T, VEC>(d_at + 8 * i * p.ldd, lane, cols, d[i]);
+            if (MUL) load8<T, VEC>(d_at + 8 * i * p.ldd, lane, cols, d[i]);
         }
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
@@ -164,17 +164,17 @@ __device__ __forceinline__ void run_rows(const Params<T> &p, int64_t r, int64_t 
             for (int e = 0; e < 8; ++e) {
                 const float up = g[i].get(e);
                 const float2 a = act_and_slope<ACT>(z[i].get(e));
-                o[e] = up * a.x;
+                o[e] = MUL ? up * a.x : 0.0f;
                 v[e] = ACT != kActNone ? up * a.y : up;
-                if (mul) v[e] *= d[i].get(e);
+                if (MUL) v[e] *= d[i].get(e);
                 sum[e] += v[e];
             }
             if (dz_at) put8<T, VEC>(dz_at + 8 * i * p.ld_dz, lane, cols, v);
-            if (dD_at) put8<T, VEC>(dD_at + 8 * i * p.ld_dD, lane, cols, o);
+            if (MUL && dD_at) put8<T, VEC>(dD_at + 8 * i * p.ld_dD, lane, cols, o);
         }
         g_at += 8 * BATCH * p.ld_g;
         if (z_at) z_at += 8 * BATCH * p.ld_z;
-        if (mul) d_at += 8 * BATCH * p.ldd;
+        if (MUL) d_at += 8 * BATCH * p.ldd;
         if (dz_at) dz_at += 8 * BATCH * p.ld_dz;
         if (dD_at) dD_at += 8 * BATCH * p.ld_dD;
     }
@@ -182,7 +182,7 @@ __device__ __forceinline__ void run_rows(const Params<T> &p, int64_t r, int64_t 
 
 // vec: rows are in whole 16-byte pieces, which holds for a unit whose columns
 // are a multiple of eight.
-template <class T, int ACT>
+template <class T, int ACT, bool MUL>
 __global__ void __launch_bounds__(256, 2)
 epilogue_backward_kernel(const __grid_constant__ Params<T> p, const bool vec)
 {
@@ -212,8 +212,8 @@ epilogue_backward_kernel(const __grid_constant__ Params<T> p, const bool vec)
         const int cols = (int)(p.cols - c0 < kCols ? p.cols - c0 : kCols);
         float sum[8] = {};
         const bool whole = vec && cols % 8 == 0;
-        if (whole) run_rows<T, true, ACT>(p, lo + warp, hi, c0, cols, lane, sum);
-        else run_rows<T, false, ACT>(p, lo + warp, hi, c0, cols, lane, sum);
+        if (whole) run_rows<T, true, ACT, MUL>(p, lo + warp, hi, c0, cols, lane, sum);
+        else run_rows<T, false, ACT, MUL>(p, lo + warp, hi, c0, cols, lane, sum);
         if (p.parts) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) sums[warp][whole ? column<true>(lane, e) : column<false>(lane, e)] = sum[e];
@@ -229,14 +229,16 @@ epilogue_backward_kernel(const __grid_constant__ Params<T> p, const bool vec)
     }
 }
 
-// db[g][c] = sum of the parts of group g's units, in order within 8 runs.
-__global__ void __launch_bounds__(256)
+// db[g][c] = sum of the parts of group g's units, in order within 32 runs. Its
+// launch overlaps the end of the kernel before, for whose end it waits.
+__global__ void __launch_bounds__(1024)
 add_units_kernel(const float *parts, int64_t rows, int64_t cols, int groups, const int32_t *offsets, int units,
                  float *grad_bias, int64_t stride)
 {
     __shared__ int table[kMaxGroups + 1];
-    __shared__ float sums[8][33];
+    __shared__ float sums[32][33];
     const int lane = threadIdx.x % 32, run = threadIdx.x / 32, g = blockIdx.y;
+    ptx::grid_dependency_wait();
     int u0 = 0, u1 = units;
     if (offsets) {
         fill_table(table, offsets, groups, rows, units);
@@ -246,13 +248,13 @@ add_units_kernel(const float *parts, int64_t rows, int64_t cols, int groups, con
     float s = 0.0f;
     if (c < cols) {
 #pragma unroll 4
-        for (int u = u0 + run; u < u1; u += 8) s += parts[(int64_t)u * cols + c];
+        for (int u = u0 + run; u < u1; u += 32) s += parts[(int64_t)u * cols + c];
     }
     sums[run][lane] = s;
     __syncthreads();
     if (run == 0 && c < cols) {
 #pragma unroll
-        for (int i = 1; i < 8; ++i) s += sums[i][lane];
+        for (int i = 1; i < 32; ++i) s += sums[i][lane];
         grad_bias[g * stride + c] = s;
     }
 }
@@ -279,7 +281,6 @@ cudaError_t backward_of(const EpilogueBackwardArgs &g, void *scratch, cudaStream
     const bool uses_z = g.act != kActNone || g.grad_D;
     p.z = uses_z ? static_cast<const T *>(g.pre) : nullptr, p.ld_z = g.ld_pre;
     p.D = static_cast<const T *>(g.D), p.ldd = g.ldd;
-    p.join = g.join;
     p.groups = g.groups, p.offsets = g.offsets;
     p.dz = static_cast<T *>(g.grad_pre), p.ld_dz = g.ld_gp;
     p.dD = static_cast<T *>(g.grad_D), p.ld_dD = g.ld_gd;
@@ -292,7 +293,8 @@ cudaError_t backward_of(const EpilogueBackwardArgs &g, void *scratch, cudaStream
         const int64_t all = (int64_t)p.units * p.strips, most = (int64_t)g.num_sms * 8;
         const unsigned grid = (unsigned)(all < most ? all : most);
         auto launch = [&](auto a) {
-            epilogue_backward_kernel<T, decltype(a)::value><<<grid, 256, 0, stream>>>(p, vec);
+            if (g.join == kJoinMul) epilogue_backward_kernel<T, decltype(a)::value, true><<<grid, 256, 0, stream>>>(p, vec);
+            else epilogue_backward_kernel<T, decltype(a)::value, false><<<grid, 256, 0, stream>>>(p, vec);
         };
         using std::integral_constant;
         switch (g.act) {
@@ -307,9 +309,8 @@ cudaError_t backward_of(const EpilogueBackwardArgs &g, void *scratch, cudaStream
     }
     if (g.grad_bias) {
         const dim3 grid((unsigned)((g.cols + 31) / 32), (unsigned)g.groups);
-        add_units_kernel<<<grid, 256, 0, stream>>>(p.parts, g.rows, g.cols, g.groups, g.offsets, p.units, g.grad_bias,
-                                                   g.stride_gb);
-        return cudaGetLastError();
+        return launch_after(add_units_kernel, grid, dim3(1024), stream, (const float *)p.parts, g.rows, g.cols, g.groups,
+                            g.offsets, p.units, g.grad_bias, g.stride_gb);
     }
     return cudaSuccess;
 }

@@ -19,6 +19,7 @@
 // 16 lanes', rows pass through shared memory.
 #include "fp8_values.cuh"
 #include "layers.cuh"
+#include "ptx.cuh"
 
 #include <type_traits>
 
@@ -256,8 +257,16 @@ struct NormBackwardParams {
     int weight16;
 };
 
+// Blocks of the gradient's kernel in an SM: what their rows need in registers.
+template <class T>
+constexpr int backward_resident(int threads)
+{
+    const int all = sizeof(T) == 2 ? 768 : 512;
+    return threads < all ? all / threads : 1;
+}
+
 template <class T, int WARPS, int PACKS, int LAYOUT>
-__global__ void __launch_bounds__(Team<WARPS>::THREADS)
+__global__ void __launch_bounds__(Team<WARPS>::THREADS, backward_resident<T>(Team<WARPS>::THREADS))
 rms_norm_backward_kernel(const __grid_constant__ NormBackwardParams<T> p)
 {
     using Tm = Team<WARPS>;
@@ -371,12 +380,14 @@ rms_norm_backward_kernel(const __grid_constant__ NormBackwardParams<T> p)
     }
 }
 
-// out[c] = sum of parts[.][c], in order within 32 interleaved runs.
+// out[c] = sum of parts[.][c], in order within 32 interleaved runs. Its launch
+// overlaps the end of the kernel before, for whose end it waits.
 __global__ void __launch_bounds__(1024) add_parts_kernel(const float *parts, int count, int cols, float *out)
 {
     __shared__ float sums[32][33];
     const int lane = threadIdx.x % 32, run = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
     float s = 0.0f;
+    ptx::grid_dependency_wait();
     if (c < cols) {
 #pragma unroll 8
         for (int i = run; i < count; i += 32) s += parts[(int64_t)i * cols + c];
@@ -412,17 +423,26 @@ Layout layout_of(const Rows (&all)[N], bool shiftable)
     return !alike ? kStaged : phase == 0 && ld == 0 ? kWhole : shiftable ? kShifted : kStaged;
 }
 
-// Calls f(Warps, Packs) with the shape of `cols` columns.
-template <class F>
+// Calls f(Warps, Packs) with the shape of `cols` columns: forward few threads,
+// so that several rows' loads are under way in an SM; the gradient, which
+// holds several matrices' rows, one eight per thread.
+template <bool FORWARD, class F>
 cudaError_t with_shape(int64_t cols, F f)
 {
     using std::integral_constant;
     auto call = [&](auto w, auto k) { return f(w, k); };
     if (cols <= 256) return call(integral_constant<int, 1>{}, integral_constant<int, 1>{});
-    if (cols <= 1024) return call(integral_constant<int, 1>{}, integral_constant<int, 4>{});
-    if (cols <= 2048) return call(integral_constant<int, 4>{}, integral_constant<int, 2>{});
-    if (cols <= 4096) return call(integral_constant<int, 8>{}, integral_constant<int, 2>{});
-    if (cols <= 8192) return call(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+    if constexpr (FORWARD) {
+        if (cols <= 1024) return call(integral_constant<int, 1>{}, integral_constant<int, 4>{});
+        if (cols <= 2048) return call(integral_constant<int, 4>{}, integral_constant<int, 2>{});
+        if (cols <= 4096) return call(integral_constant<int, 8>{}, integral_constant<int, 2>{});
+        if (cols <= 8192) return call(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+    } else {
+        if (cols <= 1024) return call(integral_constant<int, 4>{}, integral_constant<int, 1>{});
+        if (cols <= 2048) return call(integral_constant<int, 8>{}, integral_constant<int, 1>{});
+        if (cols <= 4096) return call(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+        if (cols <= 8192) return call(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+    }
     return call(integral_constant<int, 32>{}, integral_constant<int, 2>{});
 }
 
@@ -456,7 +476,7 @@ cudaError_t norm_of(const RmsNormArgs &g, cudaStream_t stream)
     p.q = g.q, p.ldq = g.ldq, p.scales = g.scales, p.lds = g.lds;
     const Rows all[] = {{g.x, g.ldx}, {g.residual, g.ld_res}, {g.sum, g.ld_sum}, {g.y, g.ldy}};
     const Layout layout = layout_of<T>(all, !g.q && g.cols + 7 <= kMaxNormCols);
-    return with_shape(layout == kShifted ? g.cols + 7 : g.cols, [&](auto w, auto k) {
+    return with_shape<true>(layout == kShifted ? g.cols + 7 : g.cols, [&](auto w, auto k) {
         constexpr int W = decltype(w)::value, P = decltype(k)::value;
         const unsigned grid = (unsigned)((g.rows + Team<W>::ROWS - 1) / Team<W>::ROWS);
         if (layout == kWhole) return launch(rms_norm_kernel<T, W, P, kWhole>, grid, Team<W>::THREADS, 0, &p, stream);
@@ -467,11 +487,11 @@ cudaError_t norm_of(const RmsNormArgs &g, cudaStream_t stream)
 }
 
 // Blocks of the gradient's kernel: each holds a row of weight gradients.
-template <int W>
+template <class T, int W>
 unsigned backward_blocks(const RmsNormBackwardArgs &g)
 {
     const int64_t all = (g.rows + Team<W>::ROWS - 1) / Team<W>::ROWS;
-    const int64_t most = (int64_t)g.num_sms * (Team<W>::THREADS >= 1024 ? 1 : Team<W>::THREADS >= 512 ? 2 : 4);
+    const int64_t most = (int64_t)g.num_sms * backward_resident<T>(Team<W>::THREADS);
     return (unsigned)(all < most ? all : most);
 }
 
@@ -502,9 +522,9 @@ cudaError_t norm_backward_of(const RmsNormBackwardArgs &g, void *scratch, cudaSt
     p.dx = static_cast<T *>(g.grad_x), p.ld_dx = g.ld_gx;
     p.parts = g.grad_weight ? static_cast<float *>(scratch) : nullptr;
     const Layout layout = backward_layout<T>(g);
-    return with_shape(backward_cols<T>(g), [&](auto w, auto k) {
+    return with_shape<false>(backward_cols<T>(g), [&](auto w, auto k) {
         constexpr int W = decltype(w)::value, P = decltype(k)::value;
-        const unsigned grid = backward_blocks<W>(g);
+        const unsigned grid = backward_blocks<T, W>(g);
         // Warps add their weight gradients up in shared memory, shifted rows theirs.
         const bool adds = p.parts && (W == 1 || layout == kShifted);
         const int bytes = layout == kStaged || adds ? staging_bytes(g.cols, Team<W>::ROWS) : 0;
@@ -515,8 +535,8 @@ cudaError_t norm_backward_of(const RmsNormBackwardArgs &g, void *scratch, cudaSt
                     ? launch(rms_norm_backward_kernel<T, W, P, kShifted>, grid, Team<W>::THREADS, bytes, &p, stream)
                     : launch(rms_norm_backward_kernel<T, W, P, kStaged>, grid, Team<W>::THREADS, bytes, &p, stream);
         if (e != cudaSuccess || !g.grad_weight) return e;
-        add_parts_kernel<<<(unsigned)((g.cols + 31) / 32), 1024, 0, stream>>>(p.parts, (int)grid, (int)g.cols, g.grad_weight);
-        return cudaGetLastError();
+        return launch_after(add_parts_kernel, dim3((unsigned)((g.cols + 31) / 32)), dim3(1024), stream, (const float *)p.parts,
+                            (int)grid, (int)g.cols, g.grad_weight);
     });
 }
 
@@ -531,8 +551,10 @@ size_t rms_norm_backward_scratch_bytes(const RmsNormBackwardArgs &g)
 {
     if (!g.grad_weight) return 0;
     size_t bytes = 0;
-    with_shape(g.bf16 ? backward_cols<__nv_bfloat16>(g) : backward_cols<float>(g), [&](auto w, auto) {
-        bytes = (size_t)backward_blocks<decltype(w)::value>(g) * (size_t)g.cols * 4;
+    with_shape<false>(g.bf16 ? backward_cols<__nv_bfloat16>(g) : backward_cols<float>(g), [&](auto w, auto) {
+        constexpr int W = decltype(w)::value;
+        const unsigned blocks = g.bf16 ? backward_blocks<__nv_bfloat16, W>(g) : backward_blocks<float, W>(g);
+        bytes = (size_t)blocks * (size_t)g.cols * 4;
         return cudaSuccess;
     });
     return bytes;

@@ -129,6 +129,26 @@ struct RmsNormBackwardArgs {
 size_t rms_norm_backward_scratch_bytes(const RmsNormBackwardArgs &g);
 cudaError_t launch_rms_norm_backward(const RmsNormBackwardArgs &g, void *scratch, cudaStream_t stream);
 
+// ---------------------------------------------------------------- host helpers
+
+// A launch whose blocks may begin before the stream's last kernel has ended:
+// they wait for that themselves (griddepcontrol.wait) before they read it.
+template <class... Params, class... Args>
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, dim3 block, cudaStream_t stream, Args... args)
+{
+    cudaLaunchConfig_t lc = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.gridDim = grid;
+    lc.blockDim = block;
+    lc.stream = stream;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&lc, kernel, static_cast<Params>(args)...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 // ------------------------------------------------------------ device helpers
 
 // N values of T as one access of up to 16 bytes.
@@ -193,25 +213,37 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8])
 
 // exp(x) by one multiplication and the hardware's 2^x: 2^-22 relative, and
 // |x| 2^-24 from the rounded argument, which matters where exp(x) itself is
-// small beside what it is added to.
-__device__ __forceinline__ float fast_exp(float x) { return __expf(x); }
+// small beside what it is added to. 0 below 2^-126.
+__device__ __forceinline__ float fast_exp(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.44269504088896341f));
+    return y;
+}
+
+// 1 / x by the hardware's reciprocal (1 ulp), for x >= 1; 0 past 2^126.
+__device__ __forceinline__ float fast_reciprocal(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 // 1 / (1 + exp(-x)); 0 where exp(-x) passes 2^126 (1e-38 at most is lost).
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.0f, 1.0f + fast_exp(-x)); }
+__device__ __forceinline__ float sigmoid(float x) { return fast_reciprocal(1.0f + fast_exp(-x)); }
 
 // The normal distribution's integral at z, and exp(-z^2 / 2) on the way:
 // formula 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical Functions,
-// for 1 - erf (absolute error 1.5e-7), without branches.
+// for 1 - erf (absolute error 1.5e-7), its coefficients halved, without branches.
 __device__ __forceinline__ float normal_integral(float z, float &e)
 {
-    const float x = fabsf(z) * 0.70710678118654752f;
-    const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
+    const float t = fast_reciprocal(fmaf(0.3275911f * 0.70710678118654752f, fabsf(z), 1.0f));
     e = fast_exp(-0.5f * z * z);
-    float q = fmaf(1.061405429f, t, -1.453152027f);
-    q = fmaf(q, t, 1.421413741f);
-    q = fmaf(q, t, -0.284496736f);
-    q = fmaf(q, t, 0.254829592f);
-    q = 0.5f * q * t * e;
+    float q = fmaf(0.5f * 1.061405429f, t, 0.5f * -1.453152027f);
+    q = fmaf(q, t, 0.5f * 1.421413741f);
+    q = fmaf(q, t, 0.5f * -0.284496736f);
+    q = fmaf(q, t, 0.5f * 0.254829592f);
+    q *= t * e;
     return z < 0.0f ? q : 1.0f - q;
 }
 
