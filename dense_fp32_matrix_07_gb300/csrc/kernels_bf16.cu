@@ -639,11 +639,20 @@ __device__ __forceinline__ void store_chunk(const Bf16Params &p, const Place<T> 
                 if constexpr (TMA_D) {
 #pragma unroll
                     for (int i = 0; i < AHEAD; ++i) {
-                        const uint32_t from = dbuf + (uint32_t)sizeof(T) * (32 * (r0 + (i0 + i) * PER_PASS) + c0);
+                        const int r = r0 + (i0 + i) * PER_PASS;
                         if constexpr (V == 1) {
-                            store_from_float(&d[i].v[0], ld_shared_f32(from));
+                            // Rows of pieces, each from its 16-byte boundary on.
+                            const uint32_t shift = (uint32_t)reinterpret_cast<uintptr_t>(q.D + (m + r) * p.ldd + n) & 15u;
+                            const uint32_t from = dbuf + r * (sizeof(T) == 4 ? 144 : 80) + shift + (uint32_t)sizeof(T) * c0;
+                            if constexpr (sizeof(T) == 4) {
+                                d[i].v[0] = ld_shared_f32(from);
+                            } else {
+                                uint16_t u;
+                                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(u) : "r"(from) : "memory");
+                                d[i].v[0] = *reinterpret_cast<const T *>(&u);
+                            }
                         } else {
-                            const uint4 u = ld_shared_u32x4(from);
+                            const uint4 u = ld_shared_u32x4(dbuf + (uint32_t)sizeof(T) * (32 * r + c0));
                             d[i] = *reinterpret_cast<const Values<T, V> *>(&u);
                         }
                     }
@@ -673,7 +682,8 @@ struct Chunk {
 };
 
 // A warp's chunks of D on their way to shared memory: those of one tile, in
-// order, as many as its buffers hold.
+// order, as many as its buffers hold. By TMA; where TMA cannot address D, in
+// the 16-byte pieces that a row's 32 values lie in, wherever they begin.
 template <class Cfg>
 struct Arrivals {
     uint32_t buffers, bars;
@@ -681,44 +691,75 @@ struct Arrivals {
     uint32_t asked = 0, taken = 0;
     bool ok = true;
 
-    __device__ __forceinline__ uint32_t depth(const Bf16Params &p) const { return p.c_bf16 ? 4 : 2; }
-    __device__ __forceinline__ uint32_t bytes(const Bf16Params &p) const { return Cfg::CHUNK * 32 * (p.c_bf16 ? 2 : 4); }
-    __device__ __forceinline__ uint32_t bar(const Bf16Params &p, uint32_t i) const { return bars + 8 * (i & (depth(p) - 1)); }
-    __device__ __forceinline__ uint32_t buffer(const Bf16Params &p, uint32_t i) const { return buffers + bytes(p) * (i & (depth(p) - 1)); }
+    static __device__ __forceinline__ int pieces(const Bf16Params &p) { return p.c_bf16 ? 5 : 9; }
+    static __device__ __forceinline__ uint32_t log_depth(const Bf16Params &p) { return (p.c_bf16 ? 2 : 1) - (p.vec ? 0 : 1); }
+    static __device__ __forceinline__ uint32_t bytes(const Bf16Params &p)
+    {
+        return Cfg::CHUNK * (p.vec ? 32 * (p.c_bf16 ? 2 : 4) : 16 * pieces(p));
+    }
+    __device__ __forceinline__ uint32_t slot(const Bf16Params &p, uint32_t i) const { return i & ((1u << log_depth(p)) - 1); }
+    __device__ __forceinline__ uint32_t buffer(const Bf16Params &p, uint32_t i) const { return buffers + bytes(p) * slot(p, i); }
 
-    // (Floats that TMA cannot address: copied one by one, as asynchronously.)
+    // Copies of row r's pieces; what lies outside D itself is not read.
+    template <class T, int PIECES>
+    static __device__ __forceinline__ void copy(const Bf16Params &p, const Item &w, const Chunk &c, uint32_t to, int lane)
+    {
+        const T *all = static_cast<const T *>(p.D);
+        const uintptr_t begin = reinterpret_cast<uintptr_t>(all);
+        const uintptr_t end = reinterpret_cast<uintptr_t>(
+            all + (p.mode == kBf16GroupK ? (p.groups - 1) * p.stride_c : 0) + (p.M - 1) * p.ldd + p.N);
+        const T *first = all + (p.mode == kBf16GroupK ? w.group * p.stride_c : 0) + c.m * p.ldd + c.n;
+        const int cols = c.cols < 32 ? c.cols : 32;
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            const int at = 32 * i + lane, r = at / PIECES, q = at % PIECES;
+            const uintptr_t row = reinterpret_cast<uintptr_t>(first + r * p.ldd), from = (row & ~uintptr_t(15)) + 16 * q;
+            if (r >= c.rows || from >= row + cols * sizeof(T)) continue;
+            const uint32_t dst = to + 16 * (r * PIECES + q);
+            if (from >= begin && from + 16 <= end) {
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(from) : "memory");
+            } else {
+                for (int e = 0; e < 16 / (int)sizeof(T); ++e) {
+                    const uintptr_t one = from + e * sizeof(T);
+                    if (one < begin || one + sizeof(T) > end) continue;
+                    if constexpr (sizeof(T) == 4)
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst + 4 * e), "f"(*reinterpret_cast<const float *>(one)) : "memory");
+                    else
+                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + 2 * e), "h"(*reinterpret_cast<const uint16_t *>(one)) : "memory");
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+
     __device__ __forceinline__ void ask(const Bf16Params &p, const CUtensorMap *map, const Item &w, int lane, int lane0, int col0)
     {
-        while (next < Cfg::CW && asked - taken < depth(p)) {
+        while (next < Cfg::CW && asked - taken < (1u << log_depth(p))) {
             const Chunk c(p, w, lane0, col0 + next);
             next += Cfg::CHUNK;
             if (!c.some()) continue;
-            if (!p.vec) {
-                const float *from = static_cast<const float *>(p.D) + (p.mode == kBf16GroupK ? w.group * p.stride_c : 0) +
-                                    c.m * p.ldd + c.n + lane;
-                const uint32_t to = buffer(p, asked) + 4 * lane;
-#pragma unroll 8
-                for (int r = 0; r < Cfg::CHUNK; ++r)
-                    if (r < c.rows && lane < c.cols)
-                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + 128 * r), "l"(from + r * p.ldd) : "memory");
-                ++asked;
-                continue;
+            if (p.vec) {
+                const uint32_t on = lane == 0, bar = bars + 8 * slot(p, asked);
+                mbar_expect_if(on, bar, bytes(p));
+                tma_load_if(on, buffer(p, asked), map, bar, c.n, c.m, p.mode == kBf16GroupK ? w.group : 0,
+                            ptx::policy_evict_last());
+            } else if (p.c_bf16) {
+                copy<__nv_bfloat16, 5>(p, w, c, buffer(p, asked), lane);
+            } else {
+                copy<float, 9>(p, w, c, buffer(p, asked), lane);
             }
-            const uint32_t on = lane == 0;
-            mbar_expect_if(on, bar(p, asked), bytes(p));
-            tma_load_if(on, buffer(p, asked), map, bar(p, asked), c.n, c.m, p.mode == kBf16GroupK ? w.group : 0,
-                        ptx::policy_evict_last());
             ++asked;
         }
     }
-    // Waits for the oldest chunk.
+    // Waits for the oldest chunk (copies: this lane's; a __syncwarp() makes it all).
     __device__ __forceinline__ void wait(const Bf16Params &p)
     {
         if (!p.vec) {
-            asm volatile("cp.async.wait_all;" ::: "memory");
+            if (asked - taken > 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+            else asm volatile("cp.async.wait_group 0;" ::: "memory");
             return;
         }
-        const uint32_t b = bar(p, taken), phase = (taken >> (p.c_bf16 ? 2 : 1)) & 1;
+        const uint32_t b = bars + 8 * slot(p, taken), phase = (taken >> log_depth(p)) & 1;
         ok = wait_bar(mbar_test(b, phase), b, phase) && ok;
     }
 };
@@ -739,7 +780,7 @@ __device__ __forceinline__ void store_part(const Bf16Params &p, const Item &w, u
         if constexpr (Cfg::JOINS) {
             const uint32_t from = d.buffer(p, d.taken);
             auto there = [&]() { d.wait(p); };
-            if (sizeof(T) == 2 || p.vec)
+            if (p.vec)
                 store_chunk<T, CHUNK, V, true>(p, q, st, lane, chunk, at.m, at.rows, at.n, at.cols, from, there);
             else
                 store_chunk<T, CHUNK, 1, true>(p, q, st, lane, chunk, at.m, at.rows, at.n, at.cols, from, there);
@@ -1488,7 +1529,7 @@ cudaError_t launch_bf16(const Bf16Args &g, cudaStream_t stream)
 {
     const Bf16Plan p = plan_bf16(g);
     if (p.grid == 0) return cudaSuccess;
-    if (p.pair && g.join != kJoinNone && (in_pieces(g) || !g.c_bf16))
+    if (p.pair && g.join != kJoinNone)
         return p.cols == 256 ? launch_cfg<Pair256Joins>(g, p, stream) : launch_cfg<Pair128Joins>(g, p, stream);
     if (p.pair) return p.cols == 256 ? launch_cfg<Pair256>(g, p, stream) : launch_cfg<Pair128>(g, p, stream);
     return p.cols == 128  ? launch_cfg<One128>(g, p, stream)

@@ -101,10 +101,13 @@ struct NormParams {
     int weight16;      // the weights lie on 16 bytes
 };
 
-// Eight weights from column c on, zeros outside the row.
+// Eight weights from column c on, zeros outside the row. (Where c is a
+// multiple of 8 the compiler is told so: choosing among twelve for any c costs
+// 24 instructions.)
+template <int LAYOUT>
 __device__ __forceinline__ void load_weight(const float *w, int c, int cols, bool whole16, float (&v)[8])
 {
-    const int off = c & 3;
+    const int off = LAYOUT == kShifted ? c & 3 : 0;
     if (whole16 && c >= 0 && c + (off ? 12 - off : 8) <= cols) {
         const float4 *at = reinterpret_cast<const float4 *>(w + (c - off));
         const float4 a = __ldg(at), b = __ldg(at + 1);
@@ -214,7 +217,7 @@ rms_norm_kernel(const __grid_constant__ NormParams<T> p)
         const int c = column<WARPS>(k, shift);
         if (p.weight) {
             float w[8];
-            load_weight(p.weight, c, cols, p.weight16, w);
+            load_weight<LAYOUT>(p.weight, c, cols, p.weight16, w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[k][e] = v[k][e] * inv * w[e];
         } else {
@@ -285,6 +288,22 @@ rms_norm_backward_kernel(const __grid_constant__ NormBackwardParams<T> p)
         for (int c = Tm::rank(); c < padded; c += Tm::SIZE) columns[c] = 0.0f;
         Tm::sync();
     }
+    // The weights of columns that stay the same stay in registers.
+    constexpr bool KEEP = PACKS == 1 && LAYOUT != kShifted;
+    float kept[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) kept[e] = 1.0f;
+    if (KEEP && p.weight) load_weight<LAYOUT>(p.weight, column<WARPS>(0, 0), cols, p.weight16, kept);
+    auto weights = [&](int c, float (&w)[8]) {
+        if constexpr (!KEEP) {
+            if (p.weight) {
+                load_weight<LAYOUT>(p.weight, c, cols, p.weight16, w);
+                return;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = kept[e];
+    };
     int turn = 0;
     // Rows are requested one ahead (63 -> 57 us for 16383 x 2048 bfloat16 with
     // a gradient along the residual).
@@ -307,11 +326,11 @@ rms_norm_backward_kernel(const __grid_constant__ NormBackwardParams<T> p)
 #pragma unroll
         for (int k = 0; k < PACKS; ++k) {
             float w[8];
-            if (p.weight) load_weight(p.weight, column<WARPS>(k, shift), cols, p.weight16, w);
+            weights(column<WARPS>(k, shift), w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 s.x = fmaf(x[k].get(e), x[k].get(e), s.x);
-                s.y = fmaf(p.weight ? g[k].get(e) * w[e] : g[k].get(e), x[k].get(e), s.y);
+                s.y = fmaf(g[k].get(e) * w[e], x[k].get(e), s.y);
             }
             x0[k] = x[k], g0[k] = g[k];
             if (p.gs) gs0[k] = gs[k];
@@ -326,10 +345,10 @@ rms_norm_backward_kernel(const __grid_constant__ NormBackwardParams<T> p)
         for (int k = 0; k < PACKS; ++k) {
             const int c = column<WARPS>(k, shift);
             float w[8], d[8];
-            if (p.weight) load_weight(p.weight, c, cols, p.weight16, w);
+            weights(c, w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float h = x0[k].get(e) * inv, gw = p.weight ? g0[k].get(e) * w[e] : g0[k].get(e);
+                const float h = x0[k].get(e) * inv, gw = g0[k].get(e) * w[e];
                 if constexpr (LAYOUT == kShifted) dw[k][e] = g0[k].get(e) * h;
                 else dw[k][e] = fmaf(g0[k].get(e), h, dw[k][e]);
                 d[e] = inv * (gw - h * mean);
@@ -452,7 +471,7 @@ int staging_bytes(int64_t cols, int rows) { return (int)((cols + 7) / 8 * 32 * r
 template <class K>
 cudaError_t launch(K kernel, unsigned grid, int threads, int bytes, const void *params, cudaStream_t stream)
 {
-    if (bytes > 48 * 1024) {
+    if (bytes > 40 * 1024) {     // 48 KB with what the kernel declares
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
     }
