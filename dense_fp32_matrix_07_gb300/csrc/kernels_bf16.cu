@@ -1486,10 +1486,15 @@ Bf16Plan plan_bf16(const Bf16Args &g)
         // Row tiles of groups by their average, as the device finds them.
         const int64_t rows = g.mode == kBf16GroupRows ? hit * ceil_div(per, tm) : ceil_div(g.M, tm);
         const int64_t tiles = rows * ceil_div(g.N, tn) * (g.mode == kBf16GroupK ? g.groups : 1);
-        const int64_t at_once = sms / ((pair ? 2 : 1) * split);
-        const int64_t waves = ceil_div(tiles, at_once > 0 ? at_once : 1);
+        const int64_t at_once = sms / ((pair ? 2 : 1) * split), units = at_once > 0 ? at_once : 1;
+        const int64_t last = tiles % units;
+        // A dense product's last wave is cut into pieces of a half or a quarter,
+        // which take more than that of the time: the lanes' operand is as wide.
+        const bool cut = pair && g.mode == kBf16Dense;
+        const double half = cols == 256 ? 0.58 : 0.84, quarter = cols == 256 ? 0.49 : 0.76;
+        const double waves = (double)(tiles / units) + (last == 0 ? 0.0 : !cut || 2 * last > units ? 1.0 : 4 * last > units ? half : quarter);
         const double slab = pair ? 80.0 + 1.75 * cols : 220.0 + 1.4 * cols;
-        const double time = (double)waves * ((double)ceil_div(nk, split) * slab + 600.0 + 8.0 * cols) + (split > 1 ? 1500.0 : 0.0);
+        const double time = waves * ((double)ceil_div(nk, split) * slab + 600.0 + 8.0 * cols) + (split > 1 ? 1500.0 : 0.0);
         if (least == 0.0 || time < least) {
             least = time;
             best = Bf16Plan{cols, pair, swap, split, 0};
@@ -1501,14 +1506,18 @@ Bf16Plan plan_bf16(const Bf16Args &g)
         if (g.mode == kBf16Dense && cols > 16) consider(cols, false, false, 1);
         if (g.mode != kBf16GroupK)
             for (int split = 2; split <= 8; split *= 2)
-                if (nk >= 4 * split && tiles_of(cols, 128) * split <= sms) consider(cols, false, true, split);
+                // Clusters of 8 do not fill the SMs: 16 of them take two turns
+                // (256 x 256 x 16384 in 32 columns 29 us, 8 in 64 columns 17).
+                if (nk >= 4 * split && tiles_of(cols, 128) * split <= (split == 8 ? sms * 3 / 4 : sms)) consider(cols, false, true, split);
     }
     for (int cols = 128; sms >= 2 && cols <= 256; cols *= 2) consider(cols, true, g.mode == kBf16GroupRows, 1);
     const int64_t lanes = best.pair ? 256 : 128;
     const int64_t tiles = best.swap ? tiles_of(best.cols, lanes) : tiles_of(lanes, best.cols);
     const int64_t cluster = best.pair ? 2 : best.split;
     const int64_t most = sms / cluster * cluster;
-    best.grid = tiles * cluster < most ? tiles * cluster : most;
+    // A single wave that leaves half of the SMs idle, in its pieces.
+    const int64_t pieces = !best.pair || g.mode != kBf16Dense || 2 * tiles * cluster > most ? 1 : 4 * tiles * cluster > most ? 2 : 4;
+    best.grid = tiles * cluster * pieces < most ? tiles * cluster * pieces : most;
     return best;
 }
 
