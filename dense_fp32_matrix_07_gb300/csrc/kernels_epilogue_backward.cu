@@ -3,8 +3,8 @@
 //   dz = g act'(z) [* D],   dD = g act(z),   db[n] = sum over a group's rows of dz[., n]
 //
 // Bound by memory: g, z and D are read once, dz and dD written once. A block
-// takes 64 rows of one group by 256 columns at a time, a warp every eighth of
-// the rows, a lane eight columns, whose sums it keeps; the block's sums go to
+// takes 32 to 256 rows of one group by 256 columns at a time, a warp every
+// eighth of the rows, a lane eight columns, whose sums it keeps; the block's sums go to
 // scratch, and a second launch adds each group's in order (no atomics: the
 // result does not depend on timing). db sums the unrounded dz, in FP32.
 #include "layers.cuh"
@@ -14,7 +14,6 @@ namespace sgemm_gb300 {
 
 namespace {
 
-constexpr int kRows = 64;     // rows of a block's unit
 constexpr int kCols = 256;    // columns of a block's unit: 32 lanes, 8 each
 
 template <class T>
@@ -27,6 +26,7 @@ struct Params {
     T *dz, *dD;
     int64_t ld_dz, ld_dD;
     float *parts;             // sums of each unit of rows, or null
+    int unit_rows;            // rows of a block's unit
     int units;                // units of rows, at most
     int strips;               // of kCols columns
 };
@@ -42,39 +42,41 @@ __device__ __forceinline__ void group_rows(const int32_t *offsets, int groups, i
     hi = hi < lo ? lo : hi > rows ? rows : hi;
 }
 
-// table[g] = units of the groups before g, held to `units` (offsets that are
-// not a partition may sum to anything). By one block of 256 threads or more.
-__device__ void fill_table(int *table, const int32_t *offsets, int groups, int64_t rows, int units)
+__device__ __forceinline__ int group_units(const int32_t *offsets, int groups, int64_t rows, int unit_rows, int g)
 {
-    __shared__ int sums[256];
-    const bool mine_too = threadIdx.x < 256;
-    const int per = (groups + 255) / 256, first = mine_too ? threadIdx.x * per : groups;
-    int64_t mine = 0;
-    for (int g = first; g < first + per && g < groups; ++g) {
-        int64_t lo, hi;
-        group_rows(offsets, groups, rows, g, lo, hi);
-        mine += (hi - lo + kRows - 1) / kRows;
+    if (g >= groups) return 0;
+    int64_t lo, hi;
+    group_rows(offsets, groups, rows, g, lo, hi);
+    return (int)((hi - lo + unit_rows - 1) / unit_rows);
+}
+
+// table[g] = units of the groups before g, held to `units` (offsets that are
+// not a partition may sum to anything). By one block of 256 threads, two
+// groups each.
+static_assert(kMaxGroups <= 512, "two groups per thread");
+
+__device__ void fill_table(int *table, const int32_t *offsets, int groups, int64_t rows, int unit_rows, int units)
+{
+    __shared__ int64_t ends[8];
+    const int g = 2 * threadIdx.x, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int first = group_units(offsets, groups, rows, unit_rows, g);
+    const int64_t mine = (int64_t)first + group_units(offsets, groups, rows, unit_rows, g + 1);
+    int64_t sum = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += up;
     }
-    if (mine_too) sums[threadIdx.x] = (int)(mine < units ? mine : units);
+    if (lane == 31) ends[warp] = sum;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        int64_t at = 0;
-        for (int i = 0; i < 256; ++i) {
-            const int n = sums[i];
-            sums[i] = (int)at;
-            at = at + n < units ? at + n : units;
-        }
-        table[groups] = (int)at;
-    }
-    __syncthreads();
-    int64_t at = mine_too ? sums[threadIdx.x] : 0;
-    for (int g = first; g < first + per && g < groups; ++g) {
-        int64_t lo, hi;
-        group_rows(offsets, groups, rows, g, lo, hi);
-        table[g] = (int)at;
-        at += (hi - lo + kRows - 1) / kRows;
-        at = at < units ? at : units;
-    }
+    int64_t before = sum - mine;
+#pragma unroll
+    for (int w = 0; w < 8; ++w)
+        if (w < warp) before += ends[w];
+    auto held = [&](int64_t n) { return (int)(n < units ? n : units); };
+    if (g <= groups) table[g] = held(before);
+    if (g + 1 <= groups) table[g + 1] = held(before + first);
+    if (threadIdx.x == 255 && groups == 512) table[512] = held(before + mine);
     __syncthreads();
 }
 
@@ -189,7 +191,7 @@ epilogue_backward_kernel(const __grid_constant__ Params<T> p, const bool vec)
     __shared__ int table[kMaxGroups + 1];
     __shared__ float sums[8][kCols];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    if (p.offsets) fill_table(table, p.offsets, p.groups, p.rows, p.units);
+    if (p.offsets) fill_table(table, p.offsets, p.groups, p.rows, p.unit_rows, p.units);
     const int units = p.offsets ? table[p.groups] : p.units;
     const int64_t all = (int64_t)units * p.strips;
     for (int64_t t = blockIdx.x; t < all; t += gridDim.x) {
@@ -206,8 +208,8 @@ epilogue_backward_kernel(const __grid_constant__ Params<T> p, const bool vec)
             first = unit - table[a];
             group_rows(p.offsets, p.groups, p.rows, a, lo, hi);
         }
-        lo += (int64_t)first * kRows;
-        hi = lo + kRows < hi ? lo + kRows : hi;
+        lo += (int64_t)first * p.unit_rows;
+        hi = lo + p.unit_rows < hi ? lo + p.unit_rows : hi;
         const int64_t c0 = (int64_t)strip * kCols;
         const int cols = (int)(p.cols - c0 < kCols ? p.cols - c0 : kCols);
         float sum[8] = {};
@@ -229,41 +231,63 @@ epilogue_backward_kernel(const __grid_constant__ Params<T> p, const bool vec)
     }
 }
 
-// db[g][c] = sum of the parts of group g's units, in order within 32 runs. Its
-// launch overlaps the end of the kernel before, for whose end it waits.
+// db[g][c] = sum of the parts of group g's units, in order within interleaved
+// runs, a warp each (32 at most; a choice by the sizes alone). Its launch overlaps the end of the kernel before, for whose end it waits.
 __global__ void __launch_bounds__(1024)
-add_units_kernel(const float *parts, int64_t rows, int64_t cols, int groups, const int32_t *offsets, int units,
+add_units_kernel(const float *parts, int64_t rows, int64_t cols, int groups, const int32_t *offsets, int unit_rows, int units,
                  float *grad_bias, int64_t stride)
 {
-    __shared__ int table[kMaxGroups + 1];
+    __shared__ int64_t counts[32];
     __shared__ float sums[32][33];
-    const int lane = threadIdx.x % 32, run = threadIdx.x / 32, g = blockIdx.y;
+    const int lane = threadIdx.x % 32, run = threadIdx.x / 32, g = blockIdx.y, runs = blockDim.x / 32;
     ptx::grid_dependency_wait();
     int u0 = 0, u1 = units;
     if (offsets) {
-        fill_table(table, offsets, groups, rows, units);
-        u0 = table[g], u1 = table[g + 1];
+        // The units of the groups before.
+        int64_t n = 0;
+        for (int i = threadIdx.x; i < g; i += blockDim.x) n += group_units(offsets, groups, rows, unit_rows, i);
+#pragma unroll
+        for (int d = 16; d; d /= 2) n += __shfl_xor_sync(0xffffffffu, n, d);
+        if (lane == 0) counts[run] = n;
+        __syncthreads();
+        n = lane < runs ? counts[lane] : 0;
+#pragma unroll
+        for (int d = 16; d; d /= 2) n += __shfl_xor_sync(0xffffffffu, n, d);
+        u0 = (int)(n < units ? n : units);
+        n += group_units(offsets, groups, rows, unit_rows, g);
+        u1 = (int)(n < units ? n : units);
     }
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
     float s = 0.0f;
     if (c < cols) {
 #pragma unroll 4
-        for (int u = u0 + run; u < u1; u += 32) s += parts[(int64_t)u * cols + c];
+        for (int u = u0 + run; u < u1; u += runs) s += parts[(int64_t)u * cols + c];
     }
     sums[run][lane] = s;
     __syncthreads();
     if (run == 0 && c < cols) {
-#pragma unroll
-        for (int i = 1; i < 32; ++i) s += sums[i][lane];
+        for (int i = 1; i < runs; ++i) s += sums[i][lane];
         grad_bias[g * stride + c] = s;
     }
+}
+
+// Rows of a unit: many, for few sums to be stored and added, where there are
+// units for six turns of all SMs, two blocks in each; with fewer the last turn
+// counts (8191 x 4096 gelu: 64 rows 48 us, 128 rows 50).
+int unit_rows_of(const EpilogueBackwardArgs &g)
+{
+    const int64_t strips = (g.cols + kCols - 1) / kCols, enough = 12 * (int64_t)g.num_sms;
+    int n = 256;
+    while (n > 32 && g.rows / n * strips < enough) n /= 2;
+    return n;
 }
 
 // Units of rows at most: each group's last may be short.
 int64_t most_units(const EpilogueBackwardArgs &g)
 {
-    if (!g.offsets) return (g.rows + kRows - 1) / kRows;
-    return g.rows / kRows + (g.groups < g.rows ? g.groups : g.rows);
+    const int n = unit_rows_of(g);
+    if (!g.offsets) return (g.rows + n - 1) / n;
+    return g.rows / n + (g.groups < g.rows ? g.groups : g.rows);
 }
 
 bool pieces16(const void *p, int64_t ld, int64_t per16)
@@ -285,6 +309,7 @@ cudaError_t backward_of(const EpilogueBackwardArgs &g, void *scratch, cudaStream
     p.dz = static_cast<T *>(g.grad_pre), p.ld_dz = g.ld_gp;
     p.dD = static_cast<T *>(g.grad_D), p.ld_dD = g.ld_gd;
     p.parts = g.grad_bias ? static_cast<float *>(scratch) : nullptr;
+    p.unit_rows = unit_rows_of(g);
     p.units = (int)most_units(g);
     p.strips = (int)((g.cols + kCols - 1) / kCols);
     const bool vec = pieces16(p.g, p.ld_g, per16) && pieces16(p.z, p.ld_z, per16) && pieces16(p.dz, p.ld_dz, per16) &&
@@ -309,8 +334,10 @@ cudaError_t backward_of(const EpilogueBackwardArgs &g, void *scratch, cudaStream
     }
     if (g.grad_bias) {
         const dim3 grid((unsigned)((g.cols + 31) / 32), (unsigned)g.groups);
-        return launch_after(add_units_kernel, grid, dim3(1024), stream, (const float *)p.parts, g.rows, g.cols, g.groups,
-                            g.offsets, p.units, g.grad_bias, g.stride_gb);
+        const int64_t each = p.units / g.groups;
+        const unsigned runs = each > 64 ? 32 : each > 16 ? 8 : 4;
+        return launch_after(add_units_kernel, grid, dim3(32 * runs), stream, (const float *)p.parts, g.rows, g.cols, g.groups,
+                            g.offsets, p.unit_rows, p.units, g.grad_bias, g.stride_gb);
     }
     return cudaSuccess;
 }
