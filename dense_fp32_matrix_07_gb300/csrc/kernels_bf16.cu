@@ -68,7 +68,7 @@ struct Bf16Cfg {
     static constexpr int P_TILE = 128 * 128;
     static constexpr int Q_TILE = (QR < 64 ? 64 : QR) * 128;       // a box of 64 x 64 at least
     static constexpr int STAGE_BYTES = P_TILE + Q_TILE;
-    static constexpr int STAGES = PAIR ? (BN == 256 ? 6 : 8) - (JOINS ? BN == 256 ? 2 : 3 : 0) : BN == 128 ? 5 : BN == 64 ? 8 : 8;
+    static constexpr int STAGES = PAIR ? (BN == 256 ? 6 : 8) - (JOINS ? BN == 256 ? 2 : 3 : 0) : BN == 128 ? 5 : 8;
     static constexpr int NBUF = 2;
     static constexpr int TMEM_COLS = NBUF * BN < 32 ? 32 : NBUF * BN;
     static constexpr int EPI_WARPS = BN >= 128 ? 8 : 4;
@@ -305,6 +305,8 @@ struct Shares {
     // Gives a group's tiles, `cost` each: `rounds` to all of the `units`
     // walkers and `extra` (below units) to those with the least work, by their
     // numbers where that is equal. Which of the extra ones walker `unit` gets
+    // Nothing is added: C stays as it is.
+    if (it.k0 >= it.k1 && p.join == kJoinAdd) it.m_end = it.m;
     // (`extra`: none).
     __device__ __forceinline__ uint32_t give(uint32_t units, uint32_t unit, uint32_t rounds, uint32_t extra, uint32_t cost, int lane)
     {
@@ -1328,7 +1330,9 @@ cudaError_t encode_bf16(CUtensorMap *map, const void *ptr, int64_t inner, int64_
     const auto encode = tensor_map_encoder();
     if (!encode) return cudaErrorNotSupported;
     const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)outer, (cuuint64_t)groups};
-    const cuuint64_t strides[2] = {(cuuint64_t)(2 * ld), (cuuint64_t)(2 * stride)};
+    // (The stride of a single row or matrix is not used, whatever it is.)
+    const int64_t row = outer > 1 ? ld : (inner + 7) / 8 * 8;
+    const cuuint64_t strides[2] = {(cuuint64_t)(2 * row), (cuuint64_t)(2 * (groups > 1 ? stride : row * outer))};
     const cuuint32_t box[3] = {(cuuint32_t)kSlab, (cuuint32_t)box_rows, 1};
     const cuuint32_t elem[3] = {1, 1, 1};
     const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, elem,
@@ -1344,7 +1348,8 @@ cudaError_t encode_d(CUtensorMap *map, const Bf16Args &g, int box_rows)
     if (!encode) return cudaErrorNotSupported;
     const int64_t size = g.c_bf16 ? 2 : 4, many = g.mode == kBf16GroupK ? g.groups : 1;
     const cuuint64_t dims[3] = {(cuuint64_t)g.N, (cuuint64_t)g.M, (cuuint64_t)many};
-    const cuuint64_t strides[2] = {(cuuint64_t)(g.ldd * size), (cuuint64_t)((many > 1 ? g.stride_c : g.M * g.ldd) * size)};
+    const int64_t row = g.M > 1 ? g.ldd : (g.N + 7) / 8 * 8;
+    const cuuint64_t strides[2] = {(cuuint64_t)(row * size), (cuuint64_t)((many > 1 ? g.stride_c : g.M * row) * size)};
     const cuuint32_t box[3] = {32, (cuuint32_t)box_rows, 1};
     const cuuint32_t elem[3] = {1, 1, 1};
     const CUresult r = encode(map, g.c_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,

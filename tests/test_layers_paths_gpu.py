@@ -132,6 +132,30 @@ def test_groups_along_k_spread_evenly(cuda_device, ctype, accumulate, E, M, N):
         assert torch.equal(C[e], (z + c[e].double() if accumulate else z).to(dtype)), e
 
 
+def test_an_empty_group_added_to_stays_as_it_was(cuda_device):
+    """In every bit, negative zeros and NaN among them; a single row with any leading dimension."""
+    E, M, N = 3, 300, 264
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[2:] = 5
+    g = gen(1)
+    a, b = whole(g, 5, M).bfloat16(), whole(g, 5, N).bfloat16()
+    A, lda = operand(a)
+    B, ldb = operand(b)
+    C = torch.full((E, M, N), -0.0, device="cuda")
+    C[0, 3, 4] = float("nan")
+    was = C.clone()
+    ok(sg.sgemm_bf16_grouped_k(E, off.data_ptr(), 5, M, N, A.data_ptr(), lda, B.data_ptr(), ldb, 1, C.data_ptr(), F32, N, M * N, stream()))
+    finish()
+    for e in (0, 2):
+        assert torch.equal(C[e].view(torch.int32), was[e].view(torch.int32))
+    assert torch.equal(C[1].double(), a.double().t() @ b.double())
+    out = torch.full((1, N), 5.0, device="cuda")
+    W, ldw = operand(whole(g, N, M).bfloat16())
+    ok(sg.sgemm_bf16(0, 1, 1, N, M, A.data_ptr(), 2 ** 50, W.data_ptr(), ldw, 0, 0, 0, 0, 0, 0, 0, out.data_ptr(), F32, 2 ** 50, stream()))
+    finish()
+    assert torch.equal(out.double(), a[:1].double() @ W[:, :M].double().t())
+
+
 def far(rows, cols, apart, dtype):
     """A matrix whose rows are `apart` elements from each other (its memory is not touched in between)."""
     buf = torch.empty((rows - 1) * apart + cols, dtype=dtype, device="cuda")
