@@ -10,7 +10,8 @@
 // cores cut the sums off after each 16 of K instead of rounding them, which
 // adds up along K (relative errors of 1.7e-6 at K = 2049, 4.4e-6 at 4096); it
 // is far below a bfloat16 C's rounding, but an FP32 C is summed in tensor
-// memory over 768 of K at a time, and these sums in FP32 registers.
+// memory over 768 of K at a time, and these sums in FP32 registers. (A
+// bfloat16 C's sums are cut off by up to 1.1e-9 K of their size.)
 //
 // A tile has 128 (or, by a pair of CTAs, 256) lanes of tensor memory, which
 // hold rows of C, and BN columns, which hold columns of C; with `swap` it is
@@ -38,6 +39,22 @@
 //
 // Every wait is bounded; a role that gives up sets the device error word and
 // goes to the teardown, which drains copies and MMAs.
+//
+// What bounds it, and what it measured (one GB300, in a row of calls):
+//   16384 x 4096 x 4096, bfloat16: 286 to 292 us, 1.9 PFLOP/s, bound by the
+//   tensor cores (the library's product takes 276 to 282); with bias,
+//   gelu_tanh and pre 298 to 300 (tensor pipe 90 % active). MMAs and copies
+//   want their operands in registers that a warp shares: without uniform() it
+//   took 306. A CTA per tile of 128 x 128 instead of pairs took 457 for 286.
+//   4097 x 3001 x 2049 into FP32 with bias, gelu and D: 90 us (tensor pipe
+//   25 % active, issue slots 32 %): 204 tiles of 256 x 256 are 2.7 waves of
+//   76 pairs, and rows that TMA cannot store leave as single values.
+//   16384 rows over 60 experts of 2048 x 2048 with silu and a factor: 147 us;
+//   741 MB, DRAM 62 % busy, tensor pipe 43 %.
+//   16 x 4096 x 4096: 11 us, of which 5 are the weights (DRAM 24 % busy).
+//   96 rows over 48 experts: 68 to 70 us, the weights at 5.8 TB/s.
+// Not taken: FP32 D held in registers for a whole chunk (100 us for 90, it
+// spills); groups of rows cut into pieces for their last wave (no change).
 #include "common.cuh"
 #include "layers.cuh"
 #include "ptx.cuh"
@@ -55,9 +72,10 @@ constexpr int kItemBytes = 32;
 constexpr int kStaging = 4096;   // 32 x 32 floats on their way to C
 constexpr int kRaster = 16;      // row tiles walked together, so that a wave of CTAs shares both operands in L2
 
-// JOINS: D comes by TMA, ahead of the sums. With 32 KB of operands per 512
-// cycles and five stages of them on their way, a load of D's by the warps
-// that use it waits 2500 cycles in the queue.
+// JOINS: D comes ahead of the sums, by TMA or asynchronous copies. With 32 KB
+// of operands per 512 cycles and several stages of them on their way, a load of
+// D's by the warps that use it waits 2500 cycles in the queue (16384 rows over
+// 60 experts of 2048 x 2048 with silu and a factor 165 us, with D ahead 152).
 template <int BN_, bool PAIR_, bool JOINS_ = false>
 struct Bf16Cfg {
     static constexpr int BN = BN_;
@@ -287,14 +305,16 @@ __device__ __forceinline__ Item k_item(const Bf16Params &p, int g, uint32_t t)
     it.n = at.y * p.tn;
     group_range(p.offsets, g, p.K, it.k0, it.k1);
     it.cols = whole_columns<Cfg>(p.swap ? it.m_end - it.m : p.N - it.n);
+    // Nothing is added: C stays as it is.
+    if (it.k0 >= it.k1 && p.join == kJoinAdd) it.m_end = it.m;
     return it;
 }
 
 // What the CTAs (pairs) have been given, for groups of uneven length: the
 // tiles of a group that are left over after each has had the same number go to
 // those that have the least so far. (Every units-th tile instead leaves 16
-// groups' weight gradients of 2048 x 2048 from 16383 rows at 119 us for 93
-// with even groups; shares of neighbouring tiles, even in their work, at 158:
+// groups' weight gradients of 2048 x 2048 from 16383 rows at 119 us for 111,
+// with even groups 95; shares of neighbouring tiles, even in their work, at 158:
 // CTAs that are at different groups share no operands in L2.) A warp's lanes
 // hold the work of walkers lane, lane + 32, ..; all warps find the same.
 constexpr int kWalkers = 5;    // per lane: up to 160
@@ -305,8 +325,6 @@ struct Shares {
     // Gives a group's tiles, `cost` each: `rounds` to all of the `units`
     // walkers and `extra` (below units) to those with the least work, by their
     // numbers where that is equal. Which of the extra ones walker `unit` gets
-    // Nothing is added: C stays as it is.
-    if (it.k0 >= it.k1 && p.join == kJoinAdd) it.m_end = it.m;
     // (`extra`: none).
     __device__ __forceinline__ uint32_t give(uint32_t units, uint32_t unit, uint32_t rounds, uint32_t extra, uint32_t cost, int lane)
     {
@@ -1419,8 +1437,9 @@ cudaError_t launch_cfg(const Bf16Args &g, const Bf16Plan &plan, cudaStream_t str
                                                     : (int64_t)p.row_tiles * g.groups;
     if (rows + 2 * kRaster > INT32_MAX / p.col_tiles - 2 * kRaster) return cudaErrorInvalidValue;
     p.by_cols = fast_div((uint32_t)p.col_tiles);
-    // Worth it where a group's tiles are about a wave of CTAs: with many more
-    // the rest matters little, with few (and many groups) the finding does.
+    // Worth it where a group's tiles are about a wave of CTAs (16 uneven groups
+    // of 2048 x 2048, 64 tiles for 76 pairs: 119 -> 111 us): with many more the
+    // rest matters little, with few and many groups the finding costs more.
     const int64_t units = plan.grid / (Cfg::PAIR ? 2 : 1), each = (int64_t)p.row_tiles * p.col_tiles;
     p.even = g.mode == kBf16GroupK && g.groups > 1 && g.groups <= 128 && units <= 32 * kWalkers && 4 * each >= units &&
              each <= 16 * units && each % units != 0;

@@ -55,10 +55,11 @@ def sum_error(S, n):
     return (n + n // 512 + 2) * 2.0 ** -23 * S
 
 
-# The activations' slopes are at most 1.13 in magnitude (gelu; silu 1.1). Their own evaluation in FP32: an erf, a tanh
-# or an exponential (4 * 2^-24 each, relative to a result of at most 1, 2 or the sigmoid), an argument rounded at most
-# four times whose effect on the result is at most 4 * 2^-24 |z| (|x sech^2 x|, |x exp(-x^2)| and |x s'(x)| stay below
-# 1), and three products or quotients (2 * 2^-24 each): together at most 16 * 2^-24 |z|, here twice that.
+# The activations' slopes are at most 1.13 in magnitude (gelu; silu 1.1). Their own evaluation in FP32: silu and gelu_tanh
+# are z times a sigmoid, whose exponential is off by 4 * 2^-24 of itself and by its argument's rounding (4 * 2^-24 of the
+# argument; |x s(x) (1 - s(x))| <= 0.23), its sum, reciprocal and product by 2 * 2^-24 each; gelu's integral is within
+# 1.5e-7 / 2 < 2 * 2^-24 by its formula, its six operations on values of at most 1 within 8 * 2^-24 and its exponential as
+# above (|x^2 exp(-x^2 / 2)| <= 0.74). Together below 16 * 2^-24 |z|; twice that is allowed.
 ACT_SLOPE = 1.13
 ACT_ERROR = 32.0 * 2.0 ** -24
 
