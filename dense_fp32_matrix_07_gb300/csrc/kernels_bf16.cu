@@ -43,7 +43,7 @@
 // What bounds it, and what it measured (one GB300, in a row of calls):
 //   16384 x 4096 x 4096, bfloat16: 286 to 292 us, 1.9 PFLOP/s, bound by the
 //   tensor cores (the library's product takes 276 to 282); with bias,
-//   gelu_tanh and pre 298 to 300 (tensor pipe 90 % active). MMAs and copies
+//   gelu_tanh and pre 298 to 311 (tensor pipe 90 % active). MMAs and copies
 //   want their operands in registers that a warp shares: without uniform() it
 //   took 306. A CTA per tile of 128 x 128 instead of pairs took 457 for 286.
 //   4097 x 3001 x 2049 into FP32 with bias, gelu and D: 90 us (tensor pipe
@@ -51,7 +51,8 @@
 //   76 pairs, and rows that TMA cannot store leave as single values.
 //   16384 rows over 60 experts of 2048 x 2048 with silu and a factor: 147 us;
 //   741 MB, DRAM 62 % busy, tensor pipe 43 %.
-//   16 x 4096 x 4096: 11 us, of which 5 are the weights (DRAM 24 % busy).
+//   16 x 4096 x 4096: 16 us with cold caches (the weights alone 5; DRAM 24 %
+//   busy), 11 where a part of the weights is still in L2.
 //   96 rows over 48 experts: 68 to 70 us, the weights at 5.8 TB/s.
 // Not taken: FP32 D held in registers for a whole chunk (100 us for 90, it
 // spills); groups of rows cut into pieces for their last wave (no change).
