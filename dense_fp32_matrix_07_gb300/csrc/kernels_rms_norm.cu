@@ -471,16 +471,27 @@ cudaError_t with_shape(int64_t cols, F f)
     return call(integral_constant<int, 32>{}, integral_constant<int, 2>{});
 }
 
-// Shared memory of a block whose rows pass through it.
-int staging_bytes(int64_t cols, int rows) { return (int)((cols + 7) / 8 * 32 * rows); }
+// Shared memory of a block whose rows pass through it. Up to 32 KB, except for
+// rows of more than 8192 columns (32 warps, two eights each): these kernels are
+// allowed their most once, by prepare_rms_norm(), as what a call set for
+// itself another thread's call could undo before the launch.
+constexpr int staging_bytes(int64_t cols, int rows) { return (int)((cols + 7) / 8 * 32 * rows); }
+
+template <class T>
+cudaError_t prepare_widest()
+{
+    constexpr int most = staging_bytes(kMaxNormCols, 1);
+    cudaError_t e = cudaFuncSetAttribute(rms_norm_kernel<T, 32, 2, kStaged>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(rms_norm_backward_kernel<T, 32, 2, kStaged>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(rms_norm_backward_kernel<T, 32, 2, kShifted>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    return e;
+}
 
 template <class K>
 cudaError_t launch(K kernel, unsigned grid, int threads, int bytes, const void *params, cudaStream_t stream)
 {
-    if (bytes > 40 * 1024) {     // 48 KB with what the kernel declares
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e != cudaSuccess) return e;
-    }
     void *args[] = {const_cast<void *>(params)};
     const cudaError_t e = cudaLaunchKernel(reinterpret_cast<const void *>(kernel), dim3(grid), dim3(threads), args,
                                            (size_t)bytes, stream);
@@ -566,6 +577,12 @@ cudaError_t norm_backward_of(const RmsNormBackwardArgs &g, void *scratch, cudaSt
 }
 
 }  // namespace
+
+cudaError_t prepare_rms_norm()
+{
+    const cudaError_t e = prepare_widest<float>();
+    return e != cudaSuccess ? e : prepare_widest<__nv_bfloat16>();
+}
 
 cudaError_t launch_rms_norm(const RmsNormArgs &g, cudaStream_t stream)
 {

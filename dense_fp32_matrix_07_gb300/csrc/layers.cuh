@@ -108,6 +108,8 @@ struct RmsNormArgs {
     int64_t lds;
     int num_sms;
 };
+// One-time set-up of the device (shared memory above 48 KB).
+cudaError_t prepare_rms_norm();
 cudaError_t launch_rms_norm(const RmsNormArgs &g, cudaStream_t stream);
 
 struct RmsNormBackwardArgs {

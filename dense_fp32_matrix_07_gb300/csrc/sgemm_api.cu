@@ -155,7 +155,7 @@ int device_info(DeviceInfo *out)
         std::lock_guard<std::mutex> lock(g_mutex);
         if (!dev->experts_ready) {
             if (take_test_failure(g_fail_setups) || prepare_fp8() != cudaSuccess || prepare_route() != cudaSuccess ||
-                prepare_bf16() != cudaSuccess) {
+                prepare_bf16() != cudaSuccess || prepare_rms_norm() != cudaSuccess) {
                 cudaGetLastError();
                 return SGEMM_ERR_CUDA;
             }
