@@ -7,11 +7,13 @@
 // dense, over groups of rows of A with a B (and bias) each, or over each
 // group's rows as K (tcgen05.mma .kind::f16, FP32 sums in tensor memory). The
 // epilogue is FP32, with one rounding as C and pre are stored. The tensor
-// cores cut the sums off after each 16 of K instead of rounding them, which
-// adds up along K (relative errors of 1.7e-6 at K = 2049, 4.4e-6 at 4096); it
-// is far below a bfloat16 C's rounding, but an FP32 C is summed in tensor
-// memory over 768 of K at a time, and these sums in FP32 registers. (A
-// bfloat16 C's sums are cut off by up to 1.1e-9 K of their size.)
+// cores cut the sums off with each 16 of K instead of rounding them, which
+// adds up along K: measured, sums of random sign are off by 1.7e-6 at K = 2049
+// and 4.4e-6 at 4096, and sums of positive values, where each cut is a loss,
+// lose 6e-9 K of their size on average (1.6e-3 at 2^18, 6.6e-3 at 2^20). So an
+// FP32 C is summed in tensor memory over 768 of K at a time, and these sums in
+// FP32 registers; a bfloat16 C, whose rounding takes up to 3.9e-3, over 8192 of
+// K at a time (a loss of 4e-5).
 //
 // A tile has 128 (or, by a pair of CTAs, 256) lanes of tensor memory, which
 // hold rows of C, and BN columns, which hold columns of C; with `swap` it is
@@ -67,7 +69,8 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kSlab = 64;        // K values per stage: 128 bytes of a row
-constexpr int kPart = 12;        // slabs that an FP32 C is summed over in tensor memory
+constexpr int kPart = 12 * kSlab;          // K that an FP32 C (and a split tile) is summed over in tensor memory
+constexpr int kPartBf16 = 128 * kSlab;     // the same of a bfloat16 C
 constexpr int kItems = 4;        // tiles found ahead of their sums
 constexpr int kItemBytes = 32;
 constexpr int kStaging = 4096;   // 32 x 32 floats on their way to C
@@ -579,14 +582,15 @@ __device__ __forceinline__ void stage(uint32_t st, int lane, bool swap, const fl
 // `cols` of them exist), V values of a row per access; put() stages them.
 // What of D a lane needs is requested before that, unless it comes by TMA:
 // then `dbuf` is where, in rows of 32 values, once there() returns.
-template <class T, int R, int V, bool TMA_D, class Put, class There>
+// HELD: the warp's sums are in registers meanwhile.
+template <class T, int R, int V, bool TMA_D, bool HELD, class Put, class There>
 __device__ __forceinline__ void store_chunk(const Bf16Params &p, const Place<T> &q, uint32_t st, int lane, Put put, int64_t m,
                                             int rows, int n, int cols, uint32_t dbuf, There there)
 {
     constexpr int PER_ROW = 32 / V, PER_PASS = 32 / PER_ROW, PASSES = R / PER_PASS;
     // Rows whose sums are in registers together: of one, each activation would
     // wait for the one before (600 cycles a row where C goes by single values).
-    constexpr int MOST = V == 1 ? 8 : V == 4 ? 2 : 4, AHEAD = PASSES < MOST ? PASSES : MOST;
+    constexpr int MOST = V == 1 ? 8 : V == 4 ? 2 : HELD ? 1 : 4, AHEAD = PASSES < MOST ? PASSES : MOST;
     const int r0 = lane / PER_ROW, c0 = (lane % PER_ROW) * V;
     const bool whole = V == 1 ? c0 < cols : c0 + V <= cols;
     Values<T, V> d[AHEAD];
@@ -787,12 +791,13 @@ struct Arrivals {
 
 // A warp's part of a tile: CW columns from the tile's column col0 on; put(c)
 // stages the chunk from its column c on.
-template <class T, class Cfg, class Put>
+template <class T, class Cfg, bool HELD, class Put>
 __device__ __forceinline__ void store_part(const Bf16Params &p, const Item &w, uint32_t st, int lane, int lane0, int col0,
                                            Put put, const CUtensorMap *map, Arrivals<Cfg> &d)
 {
     constexpr int CHUNK = Cfg::CHUNK, V = 16 / (int)sizeof(T);
-    const Place<T> q = place_of<T>(p, w.group);
+    Place<T> q = place_of<T>(p, w.group);
+    if constexpr (Cfg::PAIR && !Cfg::JOINS) q.D = nullptr;     // as the host chose this kernel
 #pragma unroll 1
     for (int c = 0; c < Cfg::CW; c += CHUNK) {
         const Chunk at(p, w, lane0, col0 + c);
@@ -802,15 +807,15 @@ __device__ __forceinline__ void store_part(const Bf16Params &p, const Item &w, u
             const uint32_t from = d.buffer(p, d.taken);
             auto there = [&]() { d.wait(p); };
             if (p.vec)
-                store_chunk<T, CHUNK, V, true>(p, q, st, lane, chunk, at.m, at.rows, at.n, at.cols, from, there);
+                store_chunk<T, CHUNK, V, true, HELD>(p, q, st, lane, chunk, at.m, at.rows, at.n, at.cols, from, there);
             else
-                store_chunk<T, CHUNK, 1, true>(p, q, st, lane, chunk, at.m, at.rows, at.n, at.cols, from, there);
+                store_chunk<T, CHUNK, 1, true, HELD>(p, q, st, lane, chunk, at.m, at.rows, at.n, at.cols, from, there);
             ++d.taken;
             d.ask(p, map, w, lane, lane0, col0);
         } else if (p.vec) {
-            store_chunk<T, CHUNK, V, false>(p, q, st, lane, chunk, at.m, at.rows, at.n, at.cols, 0, [] {});
+            store_chunk<T, CHUNK, V, false, HELD>(p, q, st, lane, chunk, at.m, at.rows, at.n, at.cols, 0, [] {});
         } else {
-            store_chunk<T, CHUNK, 1, false>(p, q, st, lane, chunk, at.m, at.rows, at.n, at.cols, 0, [] {});
+            store_chunk<T, CHUNK, 1, false, HELD>(p, q, st, lane, chunk, at.m, at.rows, at.n, at.cols, 0, [] {});
         }
     }
 }
@@ -930,7 +935,7 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
         if (lane == 0) atomicOr(p.status, kStatusTimeout);
     };
     // K that an accumulator takes before it is handed on.
-    const int part = p.c_bf16 && split == 1 ? INT32_MAX : kPart * kSlab;
+    const int part = p.c_bf16 && split == 1 ? kPartBf16 : kPart;
     // Where this CTA's lanes and its rows of the columns' operand begin.
     const int pair_rank = PAIR ? rank : 0;
 
@@ -1188,10 +1193,10 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
                 d.ask(p, &mapD, w, lane, lane0, col0);
             }
             uint32_t from;
-            if (part == INT32_MAX) {
-                // bfloat16 C: from tensor memory.
+            if (part == kPartBf16 && w.k1 - w.k0 <= kPartBf16) {
+                // bfloat16 C, its sums whole: from tensor memory.
                 if (!take(from)) break;
-                store_part<__nv_bfloat16, Cfg>(p, w, st, lane, lane0, col0, [&](int c) {
+                store_part<__nv_bfloat16, Cfg, false>(p, w, st, lane, lane0, col0, [&](int c) {
                     uint32_t v[CHUNK];
                     float z[CHUNK];
                     tmem_ld_chunk<CHUNK>(from + c, v);
@@ -1229,11 +1234,13 @@ bf16_product_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_const
             } while (k < w.k1);
             if (!ok) break;
             if (split == 1) {
-                store_part<float, Cfg>(p, w, st, lane, lane0, col0, [&](int c) {
+                auto put = [&](int c) {
 #pragma unroll
                     for (int i = 0; i < CW; i += CHUNK)
                         if (c == i) stage<CHUNK>(st, lane, p.swap, sum + i);
-                }, &mapD, d);
+                };
+                if (p.c_bf16) store_part<__nv_bfloat16, Cfg, true>(p, w, st, lane, lane0, col0, put, &mapD, d);
+                else store_part<float, Cfg, true>(p, w, st, lane, lane0, col0, put, &mapD, d);
             } else if constexpr (Cfg::CAN_SPLIT) {
                 // To the CTA that adds column j over the cluster: j % split.
                 const int per = BN / split, shift = __ffs(split) - 1;
