@@ -247,15 +247,7 @@ __device__ __forceinline__ Item dense_item(const Bf16Params &p, const Walk &walk
     if (cut) {
         const int wide = whole_columns<Cfg>((it.cols + (int)walk.pieces - 1) / (int)walk.pieces);
         it.cols = wide;
-        if (p.swap) {
-            it.m = it.m_end - it.m < piece * wide ? it.m_end : it.m + piece * wide;
-            it.m_end = it.m_end - it.m < wide ? it.m_end : it.m + wide;
-        } else {
-            // Columns past the tile's: this piece has none.
-            const int end = it.n + Cfg::BN;
-            it.n += piece * wide;
-            if (it.n >= end) it.m_end = it.m;
-        }
+        it.n += piece * wide;      // past C's columns: this piece has none
     }
     split_range(p, rank, it);
     return it;
@@ -272,14 +264,15 @@ __device__ __forceinline__ Group group_of(const Bf16Params &p, int g)
     Group o;
     group_range(p.offsets, g, p.M, o.lo, o.hi);
     o.tiles = (int)(((uint32_t)(o.hi - o.lo) + (uint32_t)p.tm - 1) / (uint32_t)p.tm);
-    // The columns' rows evenly over the tiles: of 273, 160 and 113 take less
-    // than 256 and 17.
+    // Evenly over the tiles, whose columns they are: of 273, 160 and 113 take
+    // less than 256 and 17.
     const int each = o.tiles > 1 ? (o.hi - o.lo + o.tiles - 1) / o.tiles : o.hi - o.lo;
-    o.tall = p.swap ? whole_columns<Cfg>(each) : p.tm;
+    o.tall = whole_columns<Cfg>(each);
     return o;
 }
 
-// Tile t of the groups' rows: table[g] row tiles are in the groups before g.
+// Tile t of the groups' rows, which lie on the columns (swap): table[g] row
+// tiles are in the groups before g.
 template <class Cfg>
 __device__ __forceinline__ Item rows_item(const Bf16Params &p, const int *table, uint32_t t, int rank)
 {
@@ -293,7 +286,7 @@ __device__ __forceinline__ Item rows_item(const Bf16Params &p, const int *table,
     it.n = at.y * p.tn;
     it.k0 = 0;
     it.k1 = p.K;
-    it.cols = whole_columns<Cfg>(p.swap ? it.m_end - it.m : p.N - it.n);
+    it.cols = whole_columns<Cfg>(it.m_end - it.m);
     split_range(p, rank, it);
     return it;
 }
@@ -1406,16 +1399,11 @@ cudaError_t prepare_cfg()
     return cudaFuncSetAttribute(bf16_product_kernel<Cfg>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
 }
 
-bool pieces16(const void *p, int64_t ld, int64_t per16)
-{
-    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % per16 == 0;
-}
-
 // Whether C, pre and D can be accessed 16 bytes at a time.
 bool in_pieces(const Bf16Args &g)
 {
     const int64_t per16 = g.c_bf16 ? 8 : 4;
-    return pieces16(g.C, g.ldc, per16) && (!g.pre || pieces16(g.pre, g.ld_pre, per16)) &&
+    return pieces16(g.C, g.ldc, per16) && pieces16(g.pre, g.ld_pre, per16) &&
            (g.join == kJoinNone || pieces16(g.D, g.ldd, per16)) && (g.mode != kBf16GroupK || g.stride_c % per16 == 0);
 }
 

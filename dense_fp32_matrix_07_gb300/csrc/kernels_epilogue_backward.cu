@@ -12,6 +12,7 @@
 // with the bias gradient; 16 groups of 16383 x 2048 with those 60 and 68.
 #include "layers.cuh"
 #include "ptx.cuh"
+#include "tc_roles.cuh"
 
 namespace sgemm_gb300 {
 
@@ -34,22 +35,22 @@ struct Params {
     int strips;               // of kCols columns
 };
 
-__device__ __forceinline__ void group_rows(const int32_t *offsets, int groups, int64_t rows, int g, int64_t &lo, int64_t &hi)
+__device__ __forceinline__ void group_rows(const int32_t *offsets, int64_t rows, int g, int64_t &lo, int64_t &hi)
 {
     if (!offsets) {
         lo = 0, hi = rows;
         return;
     }
-    lo = offsets[g], hi = offsets[g + 1];
-    lo = lo < 0 ? 0 : lo > rows ? rows : lo;
-    hi = hi < lo ? lo : hi > rows ? rows : hi;
+    int first, end;
+    group_range(offsets, g, (int)rows, first, end);
+    lo = first, hi = end;
 }
 
 __device__ __forceinline__ int group_units(const int32_t *offsets, int groups, int64_t rows, int unit_rows, int g)
 {
     if (g >= groups) return 0;
     int64_t lo, hi;
-    group_rows(offsets, groups, rows, g, lo, hi);
+    group_rows(offsets, rows, g, lo, hi);
     return (int)((hi - lo + unit_rows - 1) / unit_rows);
 }
 
@@ -209,7 +210,7 @@ epilogue_backward_kernel(const __grid_constant__ Params<T> p, const bool vec)
                 else b = mid - 1;
             }
             first = unit - table[a];
-            group_rows(p.offsets, p.groups, p.rows, a, lo, hi);
+            group_rows(p.offsets, p.rows, a, lo, hi);
         }
         lo += (int64_t)first * p.unit_rows;
         hi = lo + p.unit_rows < hi ? lo + p.unit_rows : hi;
@@ -291,11 +292,6 @@ int64_t most_units(const EpilogueBackwardArgs &g)
     const int n = unit_rows_of(g);
     if (!g.offsets) return (g.rows + n - 1) / n;
     return g.rows / n + (g.groups < g.rows ? g.groups : g.rows);
-}
-
-bool pieces16(const void *p, int64_t ld, int64_t per16)
-{
-    return !p || ((reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % per16 == 0);
 }
 
 template <class T>

@@ -106,7 +106,6 @@ struct RmsNormArgs {
     int64_t ldq;
     float *scales;
     int64_t lds;
-    int num_sms;
 };
 // One-time set-up of the device (shared memory above 48 KB).
 cudaError_t prepare_rms_norm();
@@ -132,6 +131,12 @@ size_t rms_norm_backward_scratch_bytes(const RmsNormBackwardArgs &g);
 cudaError_t launch_rms_norm_backward(const RmsNormBackwardArgs &g, void *scratch, cudaStream_t stream);
 
 // ---------------------------------------------------------------- host helpers
+
+// Whether a matrix's rows (null: none) can be accessed 16 bytes at a time.
+inline bool pieces16(const void *p, int64_t ld, int64_t per16)
+{
+    return !p || ((reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % per16 == 0);
+}
 
 // A launch whose blocks may begin before the stream's last kernel has ended:
 // they wait for that themselves (griddepcontrol.wait) before they read it.

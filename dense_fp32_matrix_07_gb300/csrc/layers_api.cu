@@ -279,7 +279,6 @@ int sgemm_rms_norm(int64_t rows, int64_t cols, int type, const void *x, int64_t 
     g.weight = weight, g.eps = eps;
     g.sum = sum, g.ld_sum = ld_sum, g.y = y, g.ldy = ldy;
     g.q = q, g.ldq = ldq, g.scales = scales, g.lds = lds;
-    g.num_sms = dev.num_sms;
     return launched(launch_rms_norm(g, stream));
 }
 
