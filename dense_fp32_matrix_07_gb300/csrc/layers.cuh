@@ -219,8 +219,7 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8])
 }
 
 // exp(x) by one multiplication and the hardware's 2^x: 2^-22 relative, and
-// |x| 2^-24 from the rounded argument, which matters where exp(x) itself is
-// small beside what it is added to. 0 below 2^-126.
+// 1.5 |x| 2^-24 from the rounded argument and its constant. 0 below 2^-126.
 __device__ __forceinline__ float fast_exp(float x)
 {
     float y;
@@ -239,17 +238,23 @@ __device__ __forceinline__ float fast_reciprocal(float x)
 // 1 / (1 + exp(-x)); 0 where exp(-x) passes 2^126 (1e-38 at most is lost).
 __device__ __forceinline__ float sigmoid(float x) { return fast_reciprocal(1.0f + fast_exp(-x)); }
 
-// The normal distribution's integral at z, and exp(-z^2 / 2) on the way:
-// formula 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical Functions,
-// for 1 - erf (absolute error 1.5e-7), its coefficients halved, without branches.
+// The normal distribution's integral at z, and exp(-z^2 / 2) on the way, without
+// branches: for z >= 0 the integral at -z is exp(-z^2 / 2) t P(t), t = 1 / (1 +
+// 0.3 z). P is of degree 7, fitted in 64 bits for z up to 14 (least squares of
+// the relative error, weights raised where it is largest) to 1.7e-7 of the
+// integral itself: a formula of absolute error (1.5e-7 of erf) was off by 4.7e-4
+// of gelu at -4 and 1e-2 at -8. With roundings, (32 + 2 z^2) 2^-24 relative.
 __device__ __forceinline__ float normal_integral(float z, float &e)
 {
-    const float t = fast_reciprocal(fmaf(0.3275911f * 0.70710678118654752f, fabsf(z), 1.0f));
+    const float t = fast_reciprocal(fmaf(0.3f, fabsf(z), 1.0f));
     e = fast_exp(-0.5f * z * z);
-    float q = fmaf(0.5f * 1.061405429f, t, 0.5f * -1.453152027f);
-    q = fmaf(q, t, 0.5f * 1.421413741f);
-    q = fmaf(q, t, 0.5f * -0.284496736f);
-    q = fmaf(q, t, 0.5f * 0.254829592f);
+    float q = fmaf(0.0356747786f, t, -0.157203101f);
+    q = fmaf(q, t, 0.206353537f);
+    q = fmaf(q, t, -0.0536836714f);
+    q = fmaf(q, t, 0.12856164f);
+    q = fmaf(q, t, 0.0999134882f);
+    q = fmaf(q, t, 0.120753957f);
+    q = fmaf(q, t, 0.119629299f);
     q *= t * e;
     return z < 0.0f ? q : 1.0f - q;
 }
