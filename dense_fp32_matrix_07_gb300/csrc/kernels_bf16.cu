@@ -43,20 +43,21 @@
 // goes to the teardown, which drains copies and MMAs.
 //
 // What bounds it, and what it measured (one GB300, in a row of calls):
-//   16384 x 4096 x 4096, bfloat16: 286 to 292 us, 1.9 PFLOP/s, bound by the
-//   tensor cores (the library's product takes 276 to 282); with bias,
-//   gelu_tanh and pre 298 to 311 (tensor pipe 90 % active). MMAs and copies
-//   want their operands in registers that a warp shares: without uniform() it
-//   took 306. A CTA per tile of 128 x 128 instead of pairs took 457 for 286.
-//   4097 x 3001 x 2049 into FP32 with bias, gelu and D: 90 us (tensor pipe
-//   25 % active, issue slots 32 %). Cold 97; with rows on 16 bytes 72, without
-//   D 71, without bias and gelu 91: a D off 16 bytes arrives a chunk at a time.
+//   16384 x 4096 x 4096, bfloat16: 284 to 326 us, 1.9 to 1.7 PFLOP/s, bound by
+//   the tensor cores and, in a long row of calls, the power cap on the clock (the
+//   library's product in the same run: 282 to 316); with bias, gelu_tanh and pre
+//   293 to 342 (tensor pipe 90 % active). MMAs and copies want their operands in
+//   registers that a warp shares: without uniform() it took 306 for 286. A CTA
+//   per tile of 128 x 128 instead of pairs took 457 for 286.
+//   4097 x 3001 x 2049 into FP32 with bias, gelu and D: 89 us (tensor pipe
+//   25 % active, issue slots 32 %). Cold 95; with rows on 16 bytes 72, without
+//   D 70, without bias and gelu 87: a D off 16 bytes arrives a chunk at a time.
 //   16384 rows over 60 experts of 2048 x 2048 with silu and a factor: 147 us;
-//   741 MB, DRAM 62 % busy, tensor pipe 43 %.
-//   16 x 4096 x 4096: 16 us with cold caches (the weights alone 5; DRAM 24 %
+//   741 MB (operands, D and C are 705), DRAM 62 % busy, tensor pipe 43 %.
+//   16 x 4096 x 4096: 17 us with cold caches (the weights alone 5; DRAM 24 %
 //   busy), 11 where a part of the weights is still in L2.
 //   96 rows over 48 experts: 68 to 70 us, the weights at 5.8 TB/s.
-// Not taken: FP32 D held in registers for a whole chunk (100 us for 90, it
+// Not taken: FP32 D held in registers for a whole chunk (100 us for 89, it
 // spills); groups of rows cut into pieces for their last wave (no change).
 #include "common.cuh"
 #include "layers.cuh"
@@ -192,7 +193,9 @@ __device__ __forceinline__ int whole_columns(int n)
 
 // How a grid of `units` pairs walks `tiles`: where the last wave would leave
 // half of them (or three quarters) idle, its tiles are cut into two (four)
-// pieces along the accumulator's columns.
+// pieces along the accumulator's columns (80 tiles for 76 pairs, 2560 x 2048 x
+// 2048: 23.3 us for 29.6; 8191 x 2048 x 4096 87.0 for 89.9; 16384 x 4096 x 4096
+// 327 for 331, in turn).
 struct Walk {
     uint32_t whole, pieces, steps;   // tiles that are not cut, pieces of the others, all in all
     __device__ __forceinline__ Walk(uint32_t tiles, uint32_t units, bool cut)
@@ -722,7 +725,7 @@ struct Arrivals {
     // Copies of a chunk's pieces. What lies between D's rows is not read: it may
     // be anyone's. Only chunks at the ends of rows (of D, where nothing lies
     // between its rows) look at what each piece may hold; done for all, 4097 x
-    // 3001 x 2049 with everything took 103 us for 90.
+    // 3001 x 2049 with everything took 103 us for 88.
     template <class T, int PIECES>
     static __device__ __forceinline__ void copy(const Bf16Params &p, const Item &w, const Chunk &c, uint32_t to, int lane)
     {

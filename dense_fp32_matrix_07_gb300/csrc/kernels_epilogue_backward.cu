@@ -7,9 +7,11 @@
 // a lane eight columns, whose sums it keeps; the block's sums go to scratch,
 // and a second launch adds each group's in order (no atomics: the result does
 // not depend on timing). db sums the unrounded dz, in FP32. Measured on one
-// GB300, bfloat16: 8191 x 4096 with gelu and the bias gradient 49 us (4.1 TB/s;
-// DRAM 51 % busy, issue slots 66 %), with silu and a factor 56 (6.0 TB/s), 63
-// with the bias gradient; 16 groups of 16383 x 2048 with those 60 and 68.
+// GB300 in a row of calls, bfloat16: 8191 x 4096 with gelu and the bias gradient
+// 48 us (4.2 TB/s; DRAM 51 % busy, issue slots 66 %), with silu and a factor 54
+// (6.2 TB/s), 60 with the bias gradient; 16 groups of 16383 x 2048 with those 57
+// and 65. Rows off 16 bytes go a value at a time: 8191 x 4095 105 and 156; FP32
+// takes 39 and 54 for half of the rows, 40 and 124 of 4095 columns.
 #include "layers.cuh"
 #include "ptx.cuh"
 #include "tc_roles.cuh"
@@ -236,7 +238,8 @@ epilogue_backward_kernel(const __grid_constant__ Params<T> p, const bool vec)
 }
 
 // db[g][c] = sum of the parts of group g's units, in order within interleaved
-// runs, a warp each (32 at most; a choice by the sizes alone). Its launch overlaps the end of the kernel before, for whose end it waits.
+// runs, a warp each (32 at most; a choice by the sizes alone). Its launch
+// overlaps the end of the kernel before, for whose end it waits.
 __global__ void __launch_bounds__(1024)
 add_units_kernel(const float *parts, int64_t rows, int64_t cols, int groups, const int32_t *offsets, int unit_rows, int units,
                  float *grad_bias, int64_t stride)

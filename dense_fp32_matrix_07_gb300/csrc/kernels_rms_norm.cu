@@ -12,9 +12,11 @@
 // stored value is rounded once. The gradient takes s as it was stored and
 // finds i again from it. Bound by memory; measured on one GB300 (in a row of
 // calls): 8191 x 4096 bfloat16 with the residual, y and q 47 us (6.45 TB/s);
-// the gradient of 16383 x 2048 with one along the residual 47.5 us (5.6 TB/s,
-// issue slots 62 % busy), with the weights' 54: their sums per block go to
-// scratch and a second, overlapped launch adds them in order.
+// the gradient of 16383 x 2048 with one along the residual 45.5 us (5.9 TB/s,
+// issue slots 62 % busy), with the weights' 51: their sums per block go to
+// scratch and a second, overlapped launch adds them in order. Above 4096 columns
+// the gradient's rows do not fit the registers of their 1024 threads: 4095 x
+// 8192 67 us (4.0 TB/s), 2047 x 16384 101 (2.7).
 //
 // Rows that do not begin on 16 bytes (an odd number of columns): where all
 // matrices' rows lie alike, the threads' eights are shifted so that they begin

@@ -151,7 +151,8 @@ int sgemm_epilogue_backward(int64_t rows, int64_t cols, int type, const void *gr
  *   scales, lds     is rounded to `type`): ldq >= cols, a multiple of 16, on
  *                   16 bytes; ceil(cols/128) x rows scales, lds >= rows.
  *
- * eps >= 0; a row of zeros with eps = 0 is NaN.
+ * eps >= 0; a row of zeros with eps = 0 is NaN. Squares are summed in FP32: where
+ * they pass its range (values of 2^64), y is 0, as beside an infinity.
  */
 int sgemm_rms_norm(int64_t rows, int64_t cols, int type, const void *x, int64_t ldx, const void *residual, int64_t ld_res,
                    const float *weight, float eps, void *sum, int64_t ld_sum, void *y, int64_t ldy,
