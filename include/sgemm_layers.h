@@ -41,7 +41,8 @@ extern "C" {
  * Evaluated in FP32, from z in FP32, each is within this part of its value, in
  * units of 2^-24 (before it is rounded to its type): silu 8 + 2 |z|, gelu 32 +
  * 2 z^2, gelu_tanh 8 + 12 |z| + 0.5 |z|^3; values below |z| 2^-125 may be 0.
- * Slopes are that near relative to the sum of their terms' magnitudes. */
+ * Slopes are within 8 more of the sum of their two terms' magnitudes (Phi + z phi;
+ * s + z s (1 - s) x' for a sigmoid s of x). */
 enum { SGEMM_ACT_NONE = 0, SGEMM_ACT_RELU = 1, SGEMM_ACT_GELU = 2, SGEMM_ACT_GELU_TANH = 3, SGEMM_ACT_SILU = 4 };
 enum { SGEMM_JOIN_NONE = 0, SGEMM_JOIN_ADD = 1, SGEMM_JOIN_MUL = 2 };
 enum { SGEMM_BF16_DENSE = 0, SGEMM_BF16_GROUPED = 1, SGEMM_BF16_GROUPED_K = 2 };
